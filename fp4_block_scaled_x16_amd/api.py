@@ -7,6 +7,7 @@ library's HIP kernels.  The library is loaded on first use; if it is missing
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -16,14 +17,17 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libfp4_mi355x.so")
 
-NVFP4, UE5M3, MXFP4, MXFP8 = 0, 1, 2, 3
-FORMATS = {"nvfp4": NVFP4, "ue5m3": UE5M3, "mxfp4": MXFP4, "mxfp8": MXFP8}
-BLOCK_LEN = {NVFP4: 16, UE5M3: 16, MXFP4: 32, MXFP8: 32}
+NVFP4, UE5M3, MXFP4, MXFP8, FP8_E4M3, FP8_E5M2 = 0, 1, 2, 3, 5, 6
+FORMATS = {"nvfp4": NVFP4, "ue5m3": UE5M3, "mxfp4": MXFP4, "mxfp8": MXFP8, "fp8": FP8_E4M3,
+           "fp8_e5m2": FP8_E5M2}
+FP8 = (FP8_E4M3, FP8_E5M2)      # one power-of-two scale per block of 128
+BLOCK_LEN = {NVFP4: 16, UE5M3: 16, MXFP4: 32, MXFP8: 32, FP8_E4M3: 128, FP8_E5M2: 128}
 RNE, SR = 0, 1
-BLOCK_1D, BLOCK_2D16 = 0, 1
+BLOCK_1D, BLOCK_2D16, BLOCK_2D128 = 0, 1, 2
 ROWWISE, COLWISE = 0, 1
-SCALES_ROWMAJOR, SCALES_TILED = 0, 1
-SCALE_LAYOUTS = {"rowmajor": SCALES_ROWMAJOR, "tiled": SCALES_TILED}
+SCALES_ROWMAJOR, SCALES_TILED, SCALES_KMAJOR = 0, 1, 2
+SCALE_LAYOUTS = {"rowmajor": SCALES_ROWMAJOR, "tiled": SCALES_TILED, "kmajor": SCALES_KMAJOR}
+ACTS = {"swiglu": 0, "relu2": 1}
 GLOBAL_TENSOR, GLOBAL_ROW = 0, 1
 COUNT_LEVELS = {"all": 0, "scales": 1}
 GLOBAL_SCOPES = {"tensor": GLOBAL_TENSOR, "row": GLOBAL_ROW}
@@ -67,6 +71,7 @@ class Operand(ctypes.Structure):
 
 _lib = None
 EXPORTS = ("fp4_amax", "fp4_quantize", "fp4_dequantize", "fp4_rht16", "fp4_gemm",
+           "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward",
            "fp4_status_string", "fp4_last_error")
 
 
@@ -90,13 +95,17 @@ def load_library(path=None):
                                       i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.fp4_dequantize.argtypes = [i32, i32, i32, vp, vp, vp, i32, i64, i64, vp, i32, vp]
     lib.fp4_rht16.argtypes = [ctypes.POINTER(QuantDesc), vp, i64, i64, i64, vp, vp]
+    lib.fp4_requantize_t.argtypes = [i32, vp, vp, i64, i64, vp, vp, vp]
+    lib.fp4_act_quantize.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp]
+    lib.fp4_act_backward.argtypes = [i32, vp, vp, vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp,
+                                     vp, i64, vp, i64, vp]
     lib.fp4_gemm.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), i64, i64, i64, vp,
                              i32, i64, i32, vp]
     lib.fp4_selftest_sweep.argtypes = [i32, vp, i32, vp, vp]
     lib.fp4_selftest_gemm_decode.argtypes = [i32, vp, vp]
     lib.fp4_selftest_set_geometry.argtypes = [i32, i32]
     for f in ("fp4_amax", "fp4_quantize", "fp4_quantize_dual", "fp4_dequantize", "fp4_rht16",
-              "fp4_gemm", "fp4_selftest_sweep", "fp4_selftest_gemm_decode",
+              "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_selftest_sweep", "fp4_selftest_gemm_decode",
               "fp4_selftest_set_geometry"):
         getattr(lib, f).restype = ctypes.c_int
     lib.fp4_status_string.argtypes = [ctypes.c_int]
@@ -120,6 +129,14 @@ def _ptr(t):
 
 def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _current(device):
+    """The context in which a call on `device` launches: that device made
+    current where another one is."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _as_bf16_bits(x):
@@ -164,10 +181,11 @@ class Quantized:
     block: int
     rows: int               # rows of the code matrix
     cols: int               # cols of the code matrix (the blocked axis for 1D)
-    codes: torch.Tensor     # uint8 [rows, cols/2] (MXFP8: [rows, cols], a byte per element)
+    codes: torch.Tensor     # uint8 [rows, cols/2] (MXFP8: [rows, cols], a byte per element;
+                            # FP8: [rows, cols up to 128], zeros from cols on)
     scales: torch.Tensor    # uint8 1D: [rows, cols/BS] (TILED: flat, tiled_scale_bytes);
-                            # 2D: [rows/16, cols/16]
-    s_dec: torch.Tensor     # fp32 [1], or [rows] with per-row global scales
+                            # 2D: [rows/16, cols/16]; FP8: [blocks of cols, rows up to 16]
+    s_dec: torch.Tensor     # fp32 [1], or [rows] with per-row global scales (FP8: None)
     amax: torch.Tensor      # fp32 [1] or [rows] (two-level formats)
     codes_t: torch.Tensor = None   # 2D with emit_transpose: [cols, rows/2]
     scale_layout: int = SCALES_ROWMAJOR
@@ -183,7 +201,13 @@ class Quantized:
         bs = BLOCK_LEN[self.fmt]
         if self.fmt == MXFP8:
             raise ValueError("no GEMM takes MXFP8 operands")
-        if self.block == BLOCK_1D:
+        if self.fmt in FP8:
+            if transposed:
+                raise ValueError("an FP8 transpose is a Quantized of its own (quantize_dual)")
+            op = Operand(self.fmt, self.codes.data_ptr(), self.codes.shape[1],
+                         self.scales.data_ptr(), 0, self.scales.shape[1], 1, None, SCALES_KMAJOR,
+                         GLOBAL_TENSOR)
+        elif self.block == BLOCK_1D:
             assert not transposed
             op = Operand(self.fmt, self.codes.data_ptr(), self.cols // 2, self.scales.data_ptr(),
                          self.cols // bs, 1, 1, self.s_dec.data_ptr(), self.scale_layout,
@@ -207,10 +231,12 @@ def tiled_scale_bytes(rows, blocks_per_row):
 
 def quantize(x, fmt="nvfp4", block="1d", orient="row", rnd="rne", seed=0, offset=0, rht=False,
              signs=0, target=448.0, amax_in=None, emit_transpose=False, counters=None,
-             scale_layout="rowmajor", rht_n=16, scale_round="rne", global_scope="tensor",
+             scale_layout=None, rht_n=16, scale_round="rne", global_scope="tensor",
              count="all"):
     """Quantize a bf16 [R, C] matrix.  orient="col" quantizes X^T ([C, R]).
-    scale_layout: "rowmajor" or "tiled" (1D blocks only).  rht_n: size of
+    scale_layout: "rowmajor" (the default) or "tiled" (1D blocks only).
+    fmt "fp8" (E4M3) and "fp8_e5m2": any R and C, block "1d" (1x128) or "2d"
+    (128x128), orient "row" or "col", rnd "rne"; scales "kmajor".  rht_n: size of
     the RHT (4, 16, 32, 64, 128); signs: its sign mask, up to 128 bits.
     scale_round: "rne" or "up" (truncation-free block scales).
     global_scope: "tensor" or "row" (rowwise 1D NVFP4 / UE5M3: one global
@@ -223,6 +249,11 @@ def quantize(x, fmt="nvfp4", block="1d", orient="row", rnd="rne", seed=0, offset
     """
     x = _as_bf16_bits(x)
     f = _fmt(fmt)
+    if f in FP8:
+        return _quantize_fp8(x, f, block, orient, orient != "col", orient == "col", rnd, rht,
+                             amax_in, emit_transpose, counters, scale_layout, global_scope,
+                             count)[0]
+    scale_layout = "rowmajor" if scale_layout is None else scale_layout
     R, C = x.shape
     blk = BLOCK_2D16 if block == "2d" else BLOCK_1D
     col = orient == "col"
@@ -264,8 +295,8 @@ def _scales_1d(rows, blocks, layout, dev):
 
 def quantize_dual(x, fmt="nvfp4", rnd="rne", seed=0, offset=0, offset_t=None, rht=False, signs=0,
                   target=448.0, amax_in=None, amax_t_in=None, counters=None,
-                  scale_layout="rowmajor", scale_layout_t=None, rht_n=16, scale_round="rne",
-                  rht_row=False, signs_row=0, rht_n_row=16, count="all"):
+                  scale_layout=None, scale_layout_t=None, rht_n=16, scale_round="rne",
+                  rht_row=False, signs_row=0, rht_n_row=16, count="all", block="1d"):
     """Rowwise and colwise 1D quantization of a bf16 [R, C] matrix from one
     read: returns (rowwise Quantized [R, C], colwise Quantized of X^T [C, R]).
 
@@ -275,10 +306,21 @@ def quantize_dual(x, fmt="nvfp4", rnd="rne", seed=0, offset=0, offset_t=None, rh
     the rows (rht_row/signs_row, rht_n_row 4 or 16).  amax_in / amax_t_in:
     None -> computed on the device, else device fp32 [1] tensors read as
     the given amax of each side.  count: "all" or "scales" (block-scale
-    events only).
+    events only).  block: "1d", or with the FP8 formats "2d" (one scale per
+    128x128 tile, so the colwise codes are the rowwise ones transposed).
     """
     x = _as_bf16_bits(x)
     f = _fmt(fmt)
+    if f in FP8:
+        if scale_layout_t is not None and scale_layout is None:
+            scale_layout = scale_layout_t
+        return _quantize_fp8(x, f, block, "row", True, True, rnd, rht or rht_row,
+                             amax_in if amax_in is not None else amax_t_in, False, counters,
+                             scale_layout, "tensor", count)
+    if block != "1d":
+        raise ValueError("2D dual quantization needs an FP8 format (NVFP4, UE5M3: quantize with "
+                         "emit_transpose)")
+    scale_layout = "rowmajor" if scale_layout is None else scale_layout
     R, C = x.shape
     bs = BLOCK_LEN[f]
     dev = x.device
@@ -313,6 +355,192 @@ def quantize_dual(x, fmt="nvfp4", rnd="rne", seed=0, offset=0, offset_t=None, rh
                                  _ptr(counters), _stream(dev)), "fp4_quantize_dual")
     return (Quantized(f, BLOCK_1D, R, C, codes, scales, s_dec, am, None, lay),
             Quantized(f, BLOCK_1D, C, R, codes_t, scales_t, s_dec_t, am_t, None, lay_t))
+
+
+def _up(v, to):
+    return -(-v // to) * to
+
+
+def _fp8_buffers(fmt, rows, cols, device, block=BLOCK_1D):
+    """An FP8 code matrix [rows, cols] whose contents a kernel writes."""
+    kb = -(-cols // 128)
+    codes = torch.empty((rows, 128 * kb), dtype=torch.uint8, device=device)
+    scales = torch.empty((kb, _up(rows, 16)), dtype=torch.uint8, device=device)
+    return Quantized(fmt, block, rows, cols, codes, scales, None, None,
+                     scale_layout=SCALES_KMAJOR)
+
+
+def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpose, counters,
+                  scale_layout, global_scope, count):
+    R, C = x.shape
+    if block not in ("1d", "2d") or orient not in ("row", "col"):
+        raise ValueError("block must be '1d' or '2d' and orient 'row' or 'col'")
+    if scale_layout is None:
+        scale_layout = SCALES_KMAJOR
+    elif isinstance(scale_layout, str):
+        scale_layout = SCALE_LAYOUTS[scale_layout]
+    blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
+    q = [_fp8_buffers(f, R, C, x.device, blk)] if row else []
+    q += [_fp8_buffers(f, C, R, x.device, blk)] if col else []
+    d = [QuantDesc(f, blk, o, SR if rnd == "sr" else RNE, 0, 0, int(bool(rht)), 0, 448.0,
+                   int(amax_in is not None), int(bool(emit_transpose)), int(scale_layout), 0,
+                   (ctypes.c_uint32 * 3)(), 0, GLOBAL_SCOPES[global_scope], COUNT_LEVELS[count])
+         for o, on in ((ROWWISE, row), (COLWISE, col)) if on]
+    lib = load_library()
+    with _current(x.device):
+        if row and col:
+            _check(lib.fp4_quantize_dual(ctypes.byref(d[0]), ctypes.byref(d[1]), _ptr(x), R, C,
+                                         _ld(x), _ptr(q[0].codes), _ptr(q[0].scales),
+                                         _ptr(q[1].codes), _ptr(q[1].scales), None, None, None,
+                                         None, _ptr(counters), _stream(x.device)),
+                   "fp4_quantize_dual")
+        else:
+            _check(lib.fp4_quantize(ctypes.byref(d[0]), _ptr(x), R, C, _ld(x),
+                                    _ptr(q[0].codes), _ptr(q[0].scales), None, None, None,
+                                    _ptr(counters), _stream(x.device)), "fp4_quantize")
+    return tuple(q)
+
+
+def fp8_matrix(codes, scales, rows, cols, fmt="fp8"):
+    """A Quantized of FP8 codes and scales that exist already (a checkpoint's
+    weights): codes uint8 (or a float8 dtype) [rows, cols up to 128], zeros from
+    cols on; scales uint8 [blocks of cols, rows up to 16], the byte of (block j,
+    row r) being e + 127 of the scale 2^e."""
+    f = _fmt(fmt)
+    if f not in FP8:
+        raise ValueError("fmt must be 'fp8' or 'fp8_e5m2'")
+    if codes.dtype != torch.uint8:
+        codes = codes.view(torch.uint8)
+    if scales.dtype != torch.uint8:
+        scales = scales.view(torch.uint8)
+    kb = -(-cols // 128)
+    if codes.shape != (rows, 128 * kb) or not codes.is_contiguous():
+        raise ValueError("codes must be a contiguous [%d, %d] tensor" % (rows, 128 * kb))
+    if scales.shape != (kb, _up(rows, 16)) or not scales.is_contiguous():
+        raise ValueError("scales must be a contiguous [%d, %d] tensor" % (kb, _up(rows, 16)))
+    if codes.device != scales.device:
+        raise ValueError("codes and scales are on different devices")
+    return Quantized(f, BLOCK_1D, rows, cols, codes, scales, None, None,
+                     scale_layout=SCALES_KMAJOR)
+
+
+def _fp8_only(q, what):
+    if q.fmt not in FP8:
+        raise ValueError("%s takes FP8 codes" % what)
+
+
+def requantize_t(q: Quantized):
+    """The Quantized [cols, rows] of the transpose, in blocks along q's rows,
+    from FP8 codes along its columns: the Wgrad operand of an activation that
+    was kept as its 8-bit Fprop operand alone.  Exact but for elements below the
+    normal range of their new block."""
+    _fp8_only(q, "requantize_t")
+    t = _fp8_buffers(q.fmt, q.cols, q.rows, q.codes.device)
+    lib = load_library()
+    with _current(q.codes.device):
+        _check(lib.fp4_requantize_t(q.fmt, _ptr(q.codes), _ptr(q.scales), q.rows, q.cols,
+                                    _ptr(t.codes), _ptr(t.scales), _stream(q.codes.device)),
+               "fp4_requantize_t")
+    return t
+
+
+# ------------------------------------------------------------ activation --
+def _checkpoint_cols(act, cols):
+    """Columns of the checkpoint of an activation of `cols` outputs: SwiGLU's u
+    starts at a whole block."""
+    return _up(cols, 128) + cols if act == "swiglu" else cols
+
+
+def _ld(x):
+    """Row pitch of a bf16 matrix for the library (a multiple of 8): a single
+    row's is free to choose."""
+    return x.stride(0) if x.shape[0] > 1 else _up(x.shape[1], 8)
+
+
+def _bf16_rows(rows, cols, device):
+    """A bf16 [rows, cols] matrix whose rows start 16-byte aligned."""
+    return torch.empty((rows, _up(cols, 8)), dtype=torch.bfloat16, device=device)[:, :cols]
+
+
+def _act_bits(x, name):
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.stride(1) != 1:
+        raise ValueError("%s must be a row-major 2-D bfloat16 tensor" % name)
+    return x
+
+
+def act_quantize(h, act="swiglu", a="fp8", checkpoint=True):
+    """(a, checkpoint) of a feed-forward layer's activation, from one read of
+    bf16 h: [tokens, 2F] = [g | u] for "swiglu" (a = silu(g) u, F a multiple of
+    8), [tokens, F] for "relu2" (a = max(h, 0)^2).
+
+    a: "fp8" -> the E4M3 Quantized [tokens, F] that the second linear's product
+    takes; "bf16" -> the values, for a linear of another format; None -> None.
+    checkpoint: h as E4M3 codes (a Quantized; its u starts at a multiple of 128
+    columns), from which `act_backward` works; False -> None.
+    """
+    h = _act_bits(h, "h")
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % (tuple(ACTS),))
+    if a not in ("fp8", "bf16", None):
+        raise ValueError("a must be 'fp8', 'bf16' or None")
+    rows, cols = h.shape
+    if act == "swiglu":
+        if cols % 2:
+            raise ValueError("h must be [tokens, 2F] for 'swiglu'")
+        cols //= 2
+    dev = h.device
+    qa = _fp8_buffers(FP8_E4M3, rows, cols, dev) if a == "fp8" else None
+    av = _bf16_rows(rows, cols, dev) if a == "bf16" else None
+    qh = _fp8_buffers(FP8_E4M3, rows, _checkpoint_cols(act, cols), dev) if checkpoint else None
+    lib = load_library()
+    with _current(dev):
+        _check(lib.fp4_act_quantize(ACTS[act], _ptr(h), rows, cols, _ld(h),
+                                    _ptr(qa and qa.codes), _ptr(qa and qa.scales), _ptr(av),
+                                    0 if av is None else _ld(av), _ptr(qh and qh.codes),
+                                    _ptr(qh and qh.scales), _stream(dev)), "fp4_act_quantize")
+    return (av if a == "bf16" else qa), qh
+
+
+def act_backward(qh: Quantized, da, act="swiglu", fmt="fp8", out="fp8"):
+    """The backward pass of `act_quantize` at the values of its checkpoint qh,
+    for da, the bf16 [tokens, F] gradient of a.
+
+    out "fp8": (dh, dh_t, a_t) -- dh along its rows (columns as the checkpoint's)
+    and dh^T [2F or F, tokens] in `fmt` ("fp8" or "fp8_e5m2"), the operands of the
+    first linear's Dgrad and Wgrad, and E4M3 a^T [F, tokens], recomputed, of
+    the second linear's Wgrad.
+    out "bf16": (dh [tokens, 2F or F], a [tokens, F]) as values.
+    """
+    da = _act_bits(da, "da")
+    f = _fmt(fmt)
+    if act not in ACTS:
+        raise ValueError("act must be one of %s" % (tuple(ACTS),))
+    if f not in FP8 or out not in ("fp8", "bf16"):
+        raise ValueError("fmt must be 'fp8' or 'fp8_e5m2' and out 'fp8' or 'bf16'")
+    rows, cols = da.shape
+    if qh.fmt != FP8_E4M3 or (qh.rows, qh.cols) != (rows, _checkpoint_cols(act, cols)):
+        raise ValueError("the checkpoint must be the E4M3 [%d, %d] one of act_quantize"
+                         % (rows, _checkpoint_cols(act, cols)))
+    dev = da.device
+    if qh.codes.device != dev:
+        raise ValueError("the checkpoint and da are on different devices")
+    halves = 2 if act == "swiglu" else 1
+    o = [None] * 6
+    dh = av = None
+    if out == "fp8":
+        q = (_fp8_buffers(f, rows, qh.cols, dev), _fp8_buffers(f, halves * cols, rows, dev),
+             _fp8_buffers(FP8_E4M3, cols, rows, dev))
+        o = [t for p in q for t in (p.codes, p.scales)]
+    else:
+        dh, av = _bf16_rows(rows, halves * cols, dev), _bf16_rows(rows, cols, dev)
+    lib = load_library()
+    with _current(dev):
+        _check(lib.fp4_act_backward(ACTS[act], _ptr(qh.codes), _ptr(qh.scales), _ptr(da), rows,
+                                    cols, _ld(da), f, *[_ptr(t) for t in o], _ptr(dh),
+                                    0 if dh is None else _ld(dh), _ptr(av),
+                                    0 if av is None else _ld(av), _stream(dev)),
+               "fp4_act_backward")
+    return q if out == "fp8" else (dh, av)
 
 
 def new_counters(device="cuda"):
@@ -366,14 +594,26 @@ OUT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 def gemm(a: Operand, b: Operand, M, N, K, out=None, accumulate=False, device=None,
          out_dtype=torch.float32):
     """D[M, N] (+)= s_A s_B sum_k a[m, k] b[n, k], written as fp32 or bf16
-    (the dtype of `out` when given, else out_dtype)."""
+    (the dtype of `out` when given, else out_dtype).  FP8: a is "fp8" or
+    "fp8_e5m2" and b "fp8"; K is their code matrices' cols, whole."""
+    if a.format in FP8 and b.format in FP8:
+        qa, qb = getattr(a, "_owner", None), getattr(b, "_owner", None)
+        if qa and qb and (qa.cols != K or qb.cols != K or M > qa.rows or N > qb.rows):
+            raise ValueError("operands [%d, %d] and [%d, %d] do not make a product of M=%d, N=%d, "
+                             "K=%d" % (qa.rows, qa.cols, qb.rows, qb.cols, M, N, K))
+        if device is None and qa:
+            device = qa.codes.device
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=device or "cuda")
-    if out.dtype not in OUT_TYPES or out.dim() != 2 or out.stride(1) != 1:
+    if out.dtype not in OUT_TYPES or out.dim() != 2 or (out.stride(1) != 1 and out.shape[1] > 1):
         raise ValueError("out must be a row-major 2-D fp32 or bf16 tensor")
+    if out.shape[0] < M or out.shape[1] < N:
+        raise ValueError("out is smaller than [%d, %d]" % (M, N))
     lib = load_library()
-    _check(lib.fp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, _ptr(out), OUT_TYPES[out.dtype],
-                        out.stride(0), int(bool(accumulate)), _stream(out.device)), "fp4_gemm")
+    with _current(out.device):
+        _check(lib.fp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, _ptr(out),
+                            OUT_TYPES[out.dtype], out.stride(0), int(bool(accumulate)),
+                            _stream(out.device)), "fp4_gemm")
     return out
 
 

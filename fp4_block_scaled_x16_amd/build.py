@@ -30,6 +30,8 @@ SOURCES = [("quant.hip", "quant", []), ("quant_rowscope.hip", "quant_rowscope", 
     ("gemm_nv.hip", "gemm_nv_%d" % f, ["-DFP4_NV_FMT=%d" % f]) for f in (0, 1)] + [
     ("gemm_nv_dma.hip", "gemm_nv_dma_%d_%d" % (f, mi), ["-DFP4_DMA_FMT=%d" % f, "-DFP4_DMA_MI=%d" % mi])
     for f in (0, 1) for mi in (4, 3)] + [
+    ("quant_fp8.hip", "quant_fp8", []), ("act_fp8.hip", "act_fp8", []),
+    ("gemm_fp8.hip", "gemm_fp8", []), ("fp8_api.cpp", "fp8_api", []),
     ("gemm_mx.hip", "gemm_mx", []), ("gemm_mx_dma.hip", "gemm_mx_dma", []),
     ("selftest.hip", "selftest", []), ("fp4_api.cpp", "fp4_api", [])]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -85,7 +87,7 @@ SANITIZED_LIB = os.path.join(BUILD, "sanitize", "libfp4_mi355x_sanitized.so")
 
 
 def build_sanitized():
-    """The C ABI's host code (fp4_api.cpp: every argument check) built as
+    """The C ABI's host code (fp4_api.cpp, fp8_api.cpp: every argument check) built as
     plain host C++ with AddressSanitizer and UndefinedBehaviorSanitizer
     (every UB report fatal), linked against host-only stand-ins for the
     kernel launchers (csrc/sanitize_stubs.cpp).  Loaded in place of the real
@@ -97,7 +99,7 @@ def build_sanitized():
              "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
              "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I" + os.path.join(ROOT, "include")]
     objs = []
-    for src in ("fp4_api.cpp", "sanitize_stubs.cpp"):
+    for src in ("fp4_api.cpp", "fp8_api.cpp", "sanitize_stubs.cpp"):
         obj = os.path.join(out_dir, src.replace(".cpp", ".o"))
         _run([CLANG] + flags + ["-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)

@@ -10,13 +10,16 @@
 
 #include "../../include/fp4.h"
 #include "../../include/fp4_selftest.h"
+#include "api_common.hpp"
 #include "fp4_internal.hpp"
 
-#define FP4_EXPORT extern "C" __attribute__((visibility("default")))
+using namespace fp4api;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
+
+namespace fp4api {
 
 fp4_status fail(fp4_status st, const char* fmt, ...) {
   char buf[512];
@@ -33,12 +36,9 @@ fp4_status ok() {
   return FP4_OK;
 }
 
-fp4_status device_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(FP4_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
-  return ok();
-}
+}  // namespace fp4api
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+namespace {
 
 // MX formats: 1x32 blocks of power-of-two scales and no tensor scale.
 bool is_mx(fp4_format f) { return f == FP4_MXFP4 || f == FP4_MXFP8; }
@@ -131,6 +131,8 @@ FP4_EXPORT fp4_status fp4_quantize(const fp4_quant_desc* d, const uint16_t* x, i
                                    uint8_t* codes_t, float* amax, float* s_dec,
                                    fp4_counters* counters, void* stream) {
   if (!d) return fail(FP4_ERR_ARG, "desc is null");
+  if (is_fp8(d->format))
+    return quantize_fp8(d, x, rows, cols, ld, codes, scales, codes_t, counters, stream);
   if (!valid_format(d->format)) return fail(FP4_ERR_ARG, "bad format %d", (int)d->format);
   if (d->block != FP4_BLOCK_1D && d->block != FP4_BLOCK_2D16)
     return fail(FP4_ERR_ARG, "bad block %d", (int)d->block);
@@ -240,6 +242,9 @@ FP4_EXPORT fp4_status fp4_quantize_dual(const fp4_quant_desc* rd, const fp4_quan
                                         float* s_dec, float* s_dec_t, fp4_counters* counters,
                                         void* stream) {
   if (!rd || !cd) return fail(FP4_ERR_ARG, "desc is null");
+  if (is_fp8(rd->format) || is_fp8(cd->format))
+    return quantize_dual_fp8(rd, cd, x, rows, cols, ld, codes, scales, codes_t, scales_t, counters,
+                             stream);
   const fp4_quant_desc* ds[2] = {rd, cd};
   for (int i = 0; i < 2; ++i) {
     const fp4_quant_desc* d = ds[i];
@@ -370,6 +375,9 @@ FP4_EXPORT fp4_status fp4_dequantize(fp4_format format, fp4_block block,
                                      const uint8_t* scales, const float* s_dec,
                                      fp4_global_scope s_dec_scope, int64_t rows, int64_t cols,
                                      void* out, int out_fp32, void* stream) {
+  if (is_fp8(format))
+    return dequantize_fp8(format, block, scale_layout, codes, scales, s_dec_scope, rows, cols, out,
+                          out_fp32, stream);
   if (!valid_format(format)) return fail(FP4_ERR_ARG, "bad format %d", (int)format);
   if (block != FP4_BLOCK_1D && block != FP4_BLOCK_2D16) return fail(FP4_ERR_ARG, "bad block %d", (int)block);
   if (scale_layout != FP4_SCALES_ROWMAJOR && scale_layout != FP4_SCALES_TILED)
@@ -433,6 +441,8 @@ FP4_EXPORT fp4_status fp4_gemm(const fp4_operand* A, const fp4_operand* B, int64
                                int64_t K, void* D, fp4_out_type d_type, int64_t ldd,
                                int accumulate, void* stream) {
   if (!A || !B) return fail(FP4_ERR_ARG, "operand descriptor is null");
+  if (is_fp8(A->format) || is_fp8(B->format))
+    return gemm_fp8(A, B, M, N, K, D, d_type, ldd, accumulate, stream);
   if (!valid_format(A->format) || !valid_format(B->format)) return fail(FP4_ERR_ARG, "bad format");
   if (A->format != B->format) return fail(FP4_ERR_UNSUPPORTED, "A and B formats differ");
   if (A->format == FP4_MXFP8) return fail(FP4_ERR_UNSUPPORTED, "no GEMM takes MXFP8 operands");

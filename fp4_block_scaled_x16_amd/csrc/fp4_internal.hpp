@@ -42,6 +42,60 @@ struct GemmOperand {
   bool s_dec_rows;       // s_dec holds one decode scale per operand row
 };
 
+// FP8 (block 128): either orientation's outputs may be null, not both.
+struct Fp8QuantArgs {
+  const uint16_t* x;
+  int64_t rows, cols, ld;
+  int e5m2, block2d;
+  uint8_t* codes;        // rowwise [rows, cols up to 128]
+  uint8_t* scales;       // KMAJOR
+  uint8_t* codes_t;      // colwise [cols, rows up to 128]
+  uint8_t* scales_t;
+  fp4_counters* counters;
+};
+
+struct Fp8GemmArgs {
+  const uint8_t* codes[2];
+  int64_t ld[2];
+  const uint8_t* scales[2];
+  int64_t s_kblk[2];     // KMAJOR: bytes from one K block's scales to the next's
+  int64_t M, N, nkb;     // nkb: K blocks of 128
+  void* D;
+  int64_t ldd;
+  int d_bf16, accumulate;
+  int a_e5m2;            // operand A is E5M2 (B is E4M3)
+};
+
+struct Fp8ActArgs {
+  int act;
+  const uint16_t* h;
+  int64_t rows, cols, ld;
+  uint8_t* a_codes;
+  uint8_t* a_scales;
+  uint16_t* a;
+  int64_t ld_a;
+  uint8_t* h_codes;
+  uint8_t* h_scales;
+};
+
+struct Fp8ActGradArgs {
+  int act, e5m2;
+  const uint8_t* h_codes;
+  const uint8_t* h_scales;
+  const uint16_t* da;
+  int64_t rows, cols, ld;
+  uint8_t* dh_codes;
+  uint8_t* dh_scales;
+  uint8_t* dh_t_codes;
+  uint8_t* dh_t_scales;
+  uint8_t* a_t_codes;
+  uint8_t* a_t_scales;
+  uint16_t* dh;
+  int64_t ld_dh;
+  uint16_t* a;
+  int64_t ld_a;
+};
+
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
 // Workgroups of a persistent grid of per_cu workgroups per CU, capped by the
@@ -80,6 +134,16 @@ hipError_t launch_rht(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
 hipError_t launch_gemm(int format, const GemmOperand& A, const GemmOperand& B, int64_t M, int64_t N,
                        int64_t K, void* D, int d_bf16, int64_t ldd, int accumulate,
                        hipStream_t s);
+// FP8 block 128 (quant_fp8.hip, act_fp8.hip, gemm_fp8.hip); sizes are > 0
+// (the GEMM's nkb may be 0).
+hipError_t launch_quant_fp8(const Fp8QuantArgs& a, hipStream_t s);
+hipError_t launch_dequant_fp8(int e5m2, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                              int64_t cols, void* out, int out_fp32, hipStream_t s);
+hipError_t launch_requant_t_fp8(int e5m2, const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                int64_t cols, uint8_t* codes_t, uint8_t* scales_t, hipStream_t s);
+hipError_t launch_act_quant_fp8(const Fp8ActArgs& a, hipStream_t s);
+hipError_t launch_act_grad_fp8(const Fp8ActGradArgs& a, hipStream_t s);
+hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
 // Exhaustive conversion checks (selftest.hip).
 hipError_t launch_selftest_sweep(int kind, const uint32_t* thresholds, int n, uint64_t* result,
                                  hipStream_t s);

@@ -1,0 +1,297 @@
+// Device helpers of the FP8 block-128 kernels: block scales, element
+// conversions, and the 128 x 128 tile in which the quantizers and the
+// activation kernels encode a matrix along its rows and its columns.
+//
+// Formats (include/fp4.h): element = RNE(x * 2^-e) in E4M3 (E5 false, largest
+// value 1.75 * 2^8) or E5M2 (E5 true, 1.75 * 2^15); block scale byte e + 127,
+// e the smallest integer with largest * 2^e >= amax, at least -127.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "fp4_device.hpp"
+#include "fp4_internal.hpp"
+#include "quant_common.hpp"
+
+namespace fp8dev {
+
+using fp4dev::bf16_to_f32;
+
+__host__ __device__ __forceinline__ int64_t up16(int64_t v) { return (v + 15) & ~int64_t(15); }
+__host__ __device__ __forceinline__ int64_t up128(int64_t v) { return (v + 127) & ~int64_t(127); }
+
+// amax = m * 2^k, 1 <= m < 2: e = k - 8 (E5M2: k - 15) if m <= 1.75, one
+// more otherwise.  Adding 2^21 - 1 to the bits carries into the exponent
+// field exactly when the mantissa exceeds 0x600000 (m > 1.75).  Subnormal
+// amaxes and zero land below 0 and are clamped, which is e = -127; an
+// infinite amax gives the code of the largest finite one.
+template <bool E5>
+__device__ __forceinline__ uint32_t scale_code(float amax) {
+  const int e = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - (E5 ? 15 : 8);
+  return static_cast<uint32_t>(e > 0 ? e : 0);
+}
+
+// 2^-e of a scale code that scale_code can give (at most 247): normal.
+__device__ __forceinline__ float enc_scale(uint32_t code) {
+  return __uint_as_float((254u - code) << 23);
+}
+
+// Four element codes in one word, byte k from y_k, |y_k| within the format
+// (block scales are rounded up): gfx950's packed converts at unit scale.
+template <bool E5>
+__device__ __forceinline__ uint32_t pack4(float y0, float y1, float y2, float y3) {
+  if constexpr (E5) {
+    const fp4dev::s16x2 z = {0, 0};
+    const fp4dev::s16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(z, y0, y1, 1.0f, false);
+    const fp4dev::s16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(z, y2, y3, 1.0f, false);
+    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo),
+                                 0x05040100u);
+  } else {
+    return fp4dev::e4m3_pack4(y0, y1, y2, y3);
+  }
+}
+
+typedef float float2v __attribute__((ext_vector_type(2)));
+
+// The values of a word's four codes, unscaled (exact).
+template <bool E5>
+__device__ __forceinline__ void unpack4(uint32_t w, float* v) {
+  float2v lo, hi;
+  if constexpr (E5) {
+    lo = __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
+    hi = __builtin_amdgcn_cvt_pk_f32_bf8(w, true);
+  } else {
+    lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+    hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+  }
+  v[0] = lo.x;
+  v[1] = lo.y;
+  v[2] = hi.x;
+  v[3] = hi.y;
+}
+
+// fp32 -> bf16, nearest even; NaN stays a NaN.
+__device__ __forceinline__ uint32_t to_bf16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
+  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+// ------------------------------------------------------------ the tile ---
+// A workgroup of 512 threads holds a 128 x 128 tile: thread t has rows
+// 4 (t / 16) .. + 3 and columns 8 (t % 16) .. + 7, so 16 lanes cover a row's
+// block (a 256-byte run of bf16, a 128-byte run of codes), a wave 16 rows,
+// and the four rows of a thread are one word of a transposed code row and
+// one word of KMAJOR scales.
+constexpr int kTile = 128;
+constexpr int kTileThreads = 512;
+
+struct TilePos {
+  int64_t r0, c0;        // first row and column of the tile
+  int l, tr;             // column group (of 8) and row group (of 4) of the thread
+  __device__ __forceinline__ int64_t row(int p) const { return r0 + 4 * tr + p; }
+  __device__ __forceinline__ int64_t col() const { return c0 + 8 * l; }
+};
+
+__device__ __forceinline__ TilePos tile_pos(int64_t id, int64_t tiles_c) {
+  TilePos t;
+  const int64_t tr = id / tiles_c;
+  t.r0 = tr * kTile;
+  t.c0 = (id - tr * tiles_c) * kTile;
+  t.l = threadIdx.x & 15;
+  t.tr = threadIdx.x >> 4;
+  return t;
+}
+
+// 8 bf16 of row r from column c on; zeros outside [rows, cols].  The row
+// pitch is a multiple of 8 and the base 16-byte aligned; a partial group is
+// read element by element, so nothing behind column `cols` is touched.
+__device__ __forceinline__ uint4 load_bf16x8(const uint16_t* __restrict__ x, int64_t r, int64_t rows,
+                                             int64_t c, int64_t cols, int64_t ld) {
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  if (r < rows && c < cols) {
+    const uint16_t* p = x + r * ld + c;
+    if (c + 8 <= cols) {
+      q = *reinterpret_cast<const uint4*>(p);
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
+      q = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  return q;
+}
+
+// 8 values as bf16 into row r, columns c ..; a partial group element by
+// element.
+__device__ __forceinline__ void store_bf16x8(uint16_t* __restrict__ x, int64_t r, int64_t rows,
+                                             int64_t c, int64_t cols, int64_t ld,
+                                             const float (&v)[8]) {
+  if (r >= rows || c >= cols) return;
+  uint16_t* p = x + r * ld + c;
+  uint32_t h[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] = to_bf16(v[i]);
+  if (c + 8 <= cols) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16),
+                                              h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (c + i < cols) p[i] = static_cast<uint16_t>(h[i]);
+  }
+}
+
+// Largest over the 16 lanes of a row's block, in every one of them: the
+// rotations within a DPP row.
+template <int CTRL>
+__device__ __forceinline__ float dpp_max(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true);
+  return fmaxf(v, __builtin_bit_cast(float, o));
+}
+__device__ __forceinline__ float max16(float v) {
+  v = dpp_max<0x128>(v);   // row_ror:8
+  v = dpp_max<0x124>(v);
+  v = dpp_max<0x122>(v);
+  return dpp_max<0x121>(v);
+}
+
+__device__ __forceinline__ float absmax8(const float (&v)[8]) {
+  float m = 0.0f;          // fmaxf passes a NaN over
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+
+// Nonzero values that a word of four codes holds as zero.
+template <typename V>
+__device__ __forceinline__ uint32_t lost4(uint32_t w, const V& v) {
+  uint32_t n = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) n += (v(i) != 0.0f && ((w >> (8 * i)) & 0x7Fu) == 0u) ? 1u : 0u;
+  return n;
+}
+
+// Encode the thread's rows with their scale codes and store them: codes is
+// the row-major code matrix of pitch cp, `col` the code column; scales the
+// KMAJOR scales of block kb.
+template <bool E5, bool CNT>
+__device__ __forceinline__ void store_rows(const TilePos& t, const float (&v)[4][8],
+                                           const uint32_t (&sc)[4], int64_t rows, int64_t cp,
+                                           int64_t col, int64_t kb, uint8_t* __restrict__ codes,
+                                           uint8_t* __restrict__ scales, uint32_t& lost) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float s = enc_scale(sc[p]);
+    uint2 w;
+    w.x = pack4<E5>(v[p][0] * s, v[p][1] * s, v[p][2] * s, v[p][3] * s);
+    w.y = pack4<E5>(v[p][4] * s, v[p][5] * s, v[p][6] * s, v[p][7] * s);
+    if constexpr (CNT) {
+      lost += lost4(w.x, [&](int i) { return v[p][i]; });
+      lost += lost4(w.y, [&](int i) { return v[p][4 + i]; });
+    }
+    if (t.row(p) < rows) *reinterpret_cast<uint2*>(codes + t.row(p) * cp + col) = w;
+  }
+  const int64_t rp = up16(rows);
+  if (t.l == 0 && t.row(0) < rp)
+    *reinterpret_cast<uint32_t*>(scales + kb * rp + t.row(0)) =
+        sc[0] | (sc[1] << 8) | (sc[2] << 16) | (sc[3] << 24);
+}
+
+// Scale codes of the thread's rows in 1x128 blocks.
+template <bool E5>
+__device__ __forceinline__ void row_scales(const float (&v)[4][8], uint32_t (&sc)[4]) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) sc[p] = scale_code<E5>(max16(absmax8(v[p])));
+}
+
+// Column amaxes over the wave's 16 rows, one row of cmax[8][128] per wave;
+// the caller synchronizes, then col_max reads the whole column's.
+__device__ __forceinline__ void col_partial(const TilePos& t, const float (&v)[4][8],
+                                            float (*cmax)[kTile]) {
+  float m[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    m[c] = fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c])));
+    m[c] = fmaxf(m[c], __shfl_xor(m[c], 16, 64));
+    m[c] = fmaxf(m[c], __shfl_xor(m[c], 32, 64));
+  }
+  if ((threadIdx.x & 48) == 0) {
+    float4* d = reinterpret_cast<float4*>(&cmax[threadIdx.x >> 6][8 * t.l]);
+    d[0] = make_float4(m[0], m[1], m[2], m[3]);
+    d[1] = make_float4(m[4], m[5], m[6], m[7]);
+  }
+}
+
+__device__ __forceinline__ void col_max(const TilePos& t, const float (*cmax)[kTile], float (&m)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) m[c] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kTileThreads / 64; ++w) {
+    const float4* s = reinterpret_cast<const float4*>(&cmax[w][8 * t.l]);
+    const float4 a = s[0], b = s[1];
+    m[0] = fmaxf(m[0], a.x);
+    m[1] = fmaxf(m[1], a.y);
+    m[2] = fmaxf(m[2], a.z);
+    m[3] = fmaxf(m[3], a.w);
+    m[4] = fmaxf(m[4], b.x);
+    m[5] = fmaxf(m[5], b.y);
+    m[6] = fmaxf(m[6], b.z);
+    m[7] = fmaxf(m[7], b.w);
+  }
+}
+
+// Transposed code tile in LDS: 128 columns of 128 bytes.  Column c's word of
+// rows 4q .. 4q + 3 lies in row c ^ (c / 64), 16-byte chunk (q / 4) ^ (c / 8 % 8):
+// the 64 words that a wave writes at once (16 columns 8 apart, 4 row groups
+// of one chunk) are on 64 different banks, and a thread reads 16 bytes.
+constexpr int kTileWords = kTile * kTile / 4;
+__device__ __forceinline__ int tile_chunk(int c, int ch) {
+  return (c ^ (c >> 6)) * 8 + (ch ^ ((c >> 3) & 7));
+}
+
+// Encode the thread's columns with their scale codes into the LDS tile.
+template <bool E5, bool CNT>
+__device__ __forceinline__ void encode_cols(const TilePos& t, const float (&v)[4][8],
+                                            const uint32_t (&sc)[8], uint32_t* tile,
+                                            uint32_t& lost) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float s = enc_scale(sc[c]);
+    const uint32_t w = pack4<E5>(v[0][c] * s, v[1][c] * s, v[2][c] * s, v[3][c] * s);
+    if constexpr (CNT) lost += lost4(w, [&](int i) { return v[i][c]; });
+    tile[tile_chunk(8 * t.l + c, t.tr >> 2) * 4 + (t.tr & 3)] = w;
+  }
+}
+
+// The scale codes of 8 columns, consecutive in the transpose's KMAJOR scales.
+__device__ __forceinline__ void store_scales8(const uint32_t (&sc)[8], uint8_t* __restrict__ dst) {
+  *reinterpret_cast<uint2*>(dst) = make_uint2(sc[0] | (sc[1] << 8) | (sc[2] << 16) | (sc[3] << 24),
+                                              sc[4] | (sc[5] << 8) | (sc[6] << 16) | (sc[7] << 24));
+}
+
+// The LDS tile to rows col0 .. of the transpose's code matrix (pitch rp, a
+// multiple of 128): 8 lanes write a row's 128 bytes.  `n`: columns of the
+// tile inside the matrix.
+__device__ __forceinline__ void store_cols(const TilePos& t, const uint32_t* tile, int64_t n,
+                                           int64_t col0, int64_t rp, uint8_t* __restrict__ codes_t) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int q = threadIdx.x + k * kTileThreads;
+    const int c = q >> 3, ch = q & 7;
+    if (c < n)
+      *reinterpret_cast<uint4*>(codes_t + (col0 + c) * rp + t.r0 + 16 * ch) =
+          reinterpret_cast<const uint4*>(tile)[tile_chunk(c, ch)];
+  }
+}
+
+// Workgroups for `tiles` tiles, at most per_cu per CU.
+inline int tile_grid(int64_t tiles, int per_cu) {
+  const int64_t cap = fp4lib::grid_cap(per_cu);
+  return static_cast<int>(tiles < cap ? tiles : cap);
+}
+
+}  // namespace fp8dev

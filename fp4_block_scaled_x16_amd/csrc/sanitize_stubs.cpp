@@ -1,5 +1,5 @@
-// Host-only stand-ins for the kernel launchers, linked with fp4_api.cpp into
-// the AddressSanitizer / UndefinedBehaviorSanitizer build of the C ABI's
+// Host-only stand-ins for the kernel launchers, linked with fp4_api.cpp and fp8_api.cpp
+// into the AddressSanitizer / UndefinedBehaviorSanitizer build of the C ABI's
 // validation code (build.py build_sanitized).  That build runs the
 // argument-checking tests, which never reach a device: any call that passes
 // validation reports "no device" here instead of launching.
@@ -42,6 +42,18 @@ hipError_t launch_gemm(int, const GemmOperand&, const GemmOperand&, int64_t, int
                        int, int64_t, int, hipStream_t) {
   return hipErrorNoDevice;
 }
+hipError_t launch_quant_fp8(const Fp8QuantArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_dequant_fp8(int, const uint8_t*, const uint8_t*, int64_t, int64_t, void*, int,
+                              hipStream_t) {
+  return hipErrorNoDevice;
+}
+hipError_t launch_requant_t_fp8(int, const uint8_t*, const uint8_t*, int64_t, int64_t, uint8_t*,
+                                uint8_t*, hipStream_t) {
+  return hipErrorNoDevice;
+}
+hipError_t launch_act_quant_fp8(const Fp8ActArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_act_grad_fp8(const Fp8ActGradArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_gemm_fp8(const Fp8GemmArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_selftest_sweep(int, const uint32_t*, int, uint64_t*, hipStream_t) {
   return hipErrorNoDevice;
 }

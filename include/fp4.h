@@ -24,8 +24,9 @@
  *    call returns a nonzero fp4_status, enqueues nothing, and
  *    fp4_last_error() (thread-local) describes why.  A launch failure
  *    returns FP4_ERR_DEVICE.
- *  - Inputs must be finite; rows == 0 or cols == 0 is a valid empty call;
- *    rows and cols of a bf16 input are below 2^31.
+ *  - Inputs must be finite (the FP8 formats define what non-finite values
+ *    become); rows == 0 or cols == 0 is a valid empty call; rows and cols of
+ *    a bf16 input are below 2^31.
  *  - Calls that write the same output buffers on one stream are ordered by
  *    the stream; concurrent calls on different streams must not share
  *    output buffers.
@@ -64,9 +65,29 @@ extern "C" {
  *              blocks with a UE8M0 scale 2^e, e the smallest integer with
  *              448 * 2^e >= amax_B (rounded up like MXFP4's, App. B.4), no
  *              tensor scale; element code = E4M3 RNE of |x * 2^-e|.
- *              Quantize (1D, RNE) and dequantize only: no GEMM takes it. */
+ *              Quantize (1D, RNE) and dequantize only: no GEMM takes it.
+ *
+ * Two further 8-bit formats have one scale per block of 128, for the 8-bit
+ * matrix product and for activation checkpoints:
+ *   FP4_FP8_E4M3  E4M3 elements (sign, 4 exponent bits, 3 mantissa bits;
+ *              largest value 448)
+ *   FP4_FP8_E5M2  E5M2 elements (largest value 57344), for gradients
+ * One byte per element; blocks of 1x128 along the blocked axis or 128x128
+ * tiles; the block scale is a UE8M0 byte e + 127, e the smallest integer in
+ * [-127, 127] with max * 2^e >= amax_B (max = 448 or 57344; a zero block:
+ * -127), so no element saturates; element code = RNE of x * 2^-e, an exact
+ * product, so the codes are defined to the bit.  No tensor scale.
+ *   Code matrix [R, C]: rows of Cp = 128 ceil(C / 128) bytes; the bytes of
+ *   columns >= C are zero codes (written by the quantizers, and required by
+ *   fp4_gemm, which multiplies whole blocks).  Any R and C; no multiple of
+ *   the block is needed.
+ *   Scales: layout FP4_SCALES_KMAJOR, in 2D blocks too (a tile's scale is
+ *   repeated for each of its rows).
+ *   A NaN element becomes a NaN code, an infinite one a NaN (E4M3) or an
+ *   infinity (E5M2); a block's NaNs do not count towards amax_B, and a block
+ *   with an infinity has the scale of the largest finite fp32 value. */
 typedef enum fp4_format_e FP4_ENUM_INT {
-  FP4_NVFP4 = 0, FP4_UE5M3 = 1, FP4_MXFP4 = 2, FP4_MXFP8 = 3
+  FP4_NVFP4 = 0, FP4_UE5M3 = 1, FP4_MXFP4 = 2, FP4_MXFP8 = 3, FP4_FP8_E4M3 = 5, FP4_FP8_E5M2 = 6
 } fp4_format;
 
 /* Element rounding: nearest-even, or stochastic (NVFP4 paper §4.4). */
@@ -79,8 +100,11 @@ typedef enum fp4_round_e FP4_ENUM_INT { FP4_RNE = 0, FP4_SR = 1 } fp4_round;
  * rounded up (App. B.4). */
 typedef enum fp4_scale_round_e FP4_ENUM_INT { FP4_SCALE_RNE = 0, FP4_SCALE_UP = 1 } fp4_scale_round;
 
-/* 1D blocks along the blocked axis, or 16x16 tiles (NVFP4 paper §4.3). */
-typedef enum fp4_block_e FP4_ENUM_INT { FP4_BLOCK_1D = 0, FP4_BLOCK_2D16 = 1 } fp4_block;
+/* 1D blocks along the blocked axis, or 16x16 tiles (NVFP4 paper §4.3), or
+ * 128x128 tiles (the FP8 formats). */
+typedef enum fp4_block_e FP4_ENUM_INT {
+  FP4_BLOCK_1D = 0, FP4_BLOCK_2D16 = 1, FP4_BLOCK_2D128 = 2
+} fp4_block;
 
 /* Where the block scales of a 1D code matrix [R, C] (KB = C / BS blocks per
  * row) are stored.
@@ -93,8 +117,17 @@ typedef enum fp4_block_e FP4_ENUM_INT { FP4_BLOCK_1D = 0, FP4_BLOCK_2D16 = 1 } f
  *                        are padding, never written and never used.
  * TILED is a storage layout chosen for the GEMM: one 256-row output tile
  * reads the scales of 8 K-blocks as one contiguous 2 KiB run instead of 256
- * scattered pieces.  The scale values are the same in both layouts. */
-typedef enum fp4_scale_layout_e FP4_ENUM_INT { FP4_SCALES_ROWMAJOR = 0, FP4_SCALES_TILED = 1 } fp4_scale_layout;
+ * scattered pieces.  The scale values are the same in both layouts.
+ *
+ *   FP4_SCALES_KMAJOR    the FP8 formats' layout, and only theirs: scale of
+ *                        (row r, block j) at j * Rp + r with Rp = 16 ceil(R / 16);
+ *                        KB * Rp bytes (KB = ceil(C / 128)), 16-byte aligned;
+ *                        bytes of rows >= R are padding of unspecified value.
+ * A K step of the FP8 GEMM is one block, so a tile's scales for one step are
+ * contiguous, and those of 4 consecutive rows are one word. */
+typedef enum fp4_scale_layout_e FP4_ENUM_INT {
+  FP4_SCALES_ROWMAJOR = 0, FP4_SCALES_TILED = 1, FP4_SCALES_KMAJOR = 2
+} fp4_scale_layout;
 
 /* ROWWISE: blocks run along cols of X; output is [rows, cols] codes.
  * COLWISE: the matrix quantized is X^T; blocks run along rows of X and the
@@ -227,6 +260,11 @@ fp4_status fp4_amax(const fp4_quant_desc* desc /* host */, const uint16_t* x, in
  *   Shapes: the blocked axis (cols for ROWWISE, rows for COLWISE) must be a
  *   multiple of BS; 2D16 needs rows and cols multiples of 16; RHT needs 1D
  *   blocks and the blocked axis a multiple of its size N (rht_n).
+ *   FP8 formats: RNE, KMAJOR scales, no RHT, tensor amax or codes_t (amax
+ *   and s_dec unused, may be NULL); 1D or 2D128 blocks in either orientation;
+ *   any rows and cols (ld a multiple of 8); codes are [rows, Cp] (ROWWISE) or
+ *   [cols, Rp] (COLWISE) bytes, Cp and Rp the blocked axis rounded up to 128.
+ *   Counters: elem_underflow only.
  *   SR random bits: element index i in the output code matrix ([R_out,
  *   C_out], i = r * C_out + c) takes 16 bits u of Philox4x32-10(key = seed,
  *   counter = (i >> 3, offset)): output word (i & 7) >> 1, its upper half
@@ -267,6 +305,8 @@ fp4_status fp4_quantize(const fp4_quant_desc* desc /* host */,
  *           same amax_given (the amax is then computed once).
  *   s_dec, s_dec_t    device floats or NULL: the two global decode scales.
  *   counters  device fp4_counters or NULL: events of both sides, summed.
+ *   FP8 formats: any rows and cols; both descs 1D or both 2D128 (one scale
+ *   per 128x128 tile of x, so codes_t is the transpose of codes; weights).
  */
 fp4_status fp4_quantize_dual(const fp4_quant_desc* row_desc /* host */,
                              const fp4_quant_desc* col_desc /* host */,
@@ -286,6 +326,8 @@ fp4_status fp4_quantize_dual(const fp4_quant_desc* row_desc /* host */,
  *           is float[rows], row r decoded with s_dec[r].
  *   out     device, [rows, cols] row-major: fp32 if out_fp32, else bf16
  *           (v rounded to nearest even).
+ * FP8 formats: block 1D or 2D128 (stored alike), KMAJOR; codes rows are Cp
+ * bytes; any cols.
  */
 fp4_status fp4_dequantize(fp4_format format, fp4_block block, fp4_scale_layout scale_layout,
                           const uint8_t* codes, const uint8_t* scales, const float* s_dec,
@@ -319,7 +361,10 @@ fp4_status fp4_rht16(const fp4_quant_desc* desc /* host */, const uint16_t* x, i
  * scale is replicated per 1x16 block).  With scale_layout TILED the scales
  * are the TILED layout of the [rows, K] code matrix (KB = K / BS); the
  * strides are ignored, scale_row_group must be 1 and `scales` 16-byte
- * aligned. */
+ * aligned.  FP8 operands have scale_layout KMAJOR, scale_stride_kblk = Rp (a
+ * multiple of 16, at least the operand's rows), the other scale fields unused
+ * (scale_row_group 1), ld_codes >= 128 ceil(K / 128) and a multiple of 16, and
+ * s_dec ignored. */
 typedef struct {
   fp4_format format;
   const uint8_t* codes;       /* device, 16-byte aligned; ld_codes bytes per row,
@@ -348,18 +393,93 @@ typedef enum fp4_out_type_e FP4_ENUM_INT { FP4_OUT_F32 = 0, FP4_OUT_BF16 = 1 } f
  * global decode scales applied to the output) used for Fprop, Dgrad and
  * Wgrad (§4.1, Fig. 5).  A and B must have the same format; K must be a
  * multiple of the format's block length.
+ * FP8: A is E4M3 or E5M2 (a gradient), B is E4M3; any K (the code rows are
+ * zero from K to the next multiple of 128); the block scales are applied by
+ * the matrix instructions.  A NaN or infinite code makes the outputs of its
+ * row or column non-finite.
  *   D  device, row-major with leading dimension ldd >= N (in elements of
  *      d_type): fp32 (FP4_OUT_F32), or bf16 bits (FP4_OUT_BF16: every value
  *      is formed in fp32 as for an fp32 D -- with accumulate, the old bf16
  *      value widened and added in fp32 -- then rounded once to nearest even).
  *   accumulate  0: D = result; 1: D += result (e.g. Wgrad accumulation).
  * Accuracy (fp32 D): |D - exact| <= 1e-5 * s_dec_A * s_dec_B * sum_k |a b|
- * per element; a bf16 D is that fp32 value rounded to bf16.
+ * per element; a bf16 D is that fp32 value rounded to bf16.  FP8 with a bf16
+ * D: the 8-bit matrix instructions add 8 products at a time on a grid 2^-13
+ * below the largest one's binade, so the value before its rounding is within
+ * 1e-5 sum |a b| + 7 * 2^-13 of each group's largest |a b| (fp32 D: products
+ * and sums in fp32).
  * K == 0 writes zeros (or leaves D unchanged when accumulating).
  */
 fp4_status fp4_gemm(const fp4_operand* A /* host */, const fp4_operand* B /* host */,
                     int64_t M, int64_t N, int64_t K, void* D, fp4_out_type d_type,
                     int64_t ldd, int accumulate, void* stream);
+
+/*
+ * fp4_requantize_t -- the COLWISE operand of a matrix held as ROWWISE FP8
+ * codes: the codes of X^T in 1x128 blocks along the rows of X, from X's codes.
+ * A layer that keeps its input as the Fprop operand alone (one byte per
+ * element until the backward pass) makes its Wgrad operand so.  Scales are
+ * powers of two, so re-encoding an element is exact unless it falls below the
+ * normal range of its new block.
+ *   format  FP8_E4M3 or FP8_E5M2, of both sides.
+ *   codes   [rows, Cp], scales KMAJOR: X's rowwise code matrix (1D or 2D128).
+ *   codes_t [cols, 128 ceil(rows / 128)], scales_t KMAJOR of [cols, rows].
+ */
+fp4_status fp4_requantize_t(fp4_format format, const uint8_t* codes, const uint8_t* scales,
+                            int64_t rows, int64_t cols, uint8_t* codes_t, uint8_t* scales_t,
+                            void* stream);
+
+/* The activation between the two linears of a feed-forward layer.
+ *   SWIGLU  a = silu(g) u,  silu(g) = g / (1 + exp(-g)); h = [g | u], 2F columns
+ *   RELU2   a = max(h, 0)^2; h has F columns */
+typedef enum fp4_act_e FP4_ENUM_INT { FP4_ACT_SWIGLU = 0, FP4_ACT_RELU2 = 1 } fp4_act;
+
+/*
+ * fp4_act_quantize -- a = act(h) of the first linear's bf16 output, encoded
+ * for the second linear's product, and h itself encoded as the 8-bit
+ * checkpoint from which fp4_act_backward works; both E4M3 in 1x128 blocks
+ * along the rows, from one read of h.  a is formed in fp32 and rounded once.
+ *   h        [rows, 2F or F] bf16 (ld), device; F = cols.  SWIGLU: F % 8 == 0.
+ *   a_codes, a_scales  codes [rows, Fp] of a, Fp = 128 ceil(F / 128), scales
+ *            KMAJOR; both NULL to skip.
+ *   a        [rows, F] bf16 (ld_a), or NULL: the activation itself, for a
+ *            second linear of another format.
+ *   h_codes, h_scales  the checkpoint, both NULL to skip.  RELU2: codes
+ *            [rows, Fp].  SWIGLU: [rows, 2 Fp], g's codes from column 0 and u's
+ *            from column Fp (the columns between are zero): the code matrix
+ *            of a [rows, Fp + F] matrix.
+ */
+fp4_status fp4_act_quantize(fp4_act act, const uint16_t* h, int64_t rows, int64_t cols, int64_t ld,
+                            uint8_t* a_codes, uint8_t* a_scales, uint16_t* a, int64_t ld_a,
+                            uint8_t* h_codes, uint8_t* h_scales, void* stream);
+
+/*
+ * fp4_act_backward -- the gradient of h = [g | u] from that of a, at the
+ * values of the 8-bit checkpoint of h, with everything the two linears'
+ * backward products read, from one pass:
+ *   SWIGLU  s = 1 / (1 + exp(-g)); dg = da u s (1 + g (1 - s)); du = da g s
+ *   RELU2   dh = 2 max(h, 0) da
+ *   h_codes, h_scales  the checkpoint that fp4_act_quantize wrote.
+ *   da       [rows, F] bf16 (ld), device: the gradient of a; F = cols.
+ *   format   of the gradient's codes: FP8_E4M3 or FP8_E5M2.
+ *   dh_codes, dh_scales      rowwise codes of dh (Dgrad of the first linear),
+ *            columns as the checkpoint's.
+ *   dh_t_codes, dh_t_scales  codes of dh^T, [2F or F, 128 ceil(rows / 128)] (its
+ *            Wgrad); row F + f is u's column f: no gap.
+ *   a_t_codes, a_t_scales    E4M3 codes of a^T, [F, 128 ceil(rows / 128)], the
+ *            activation recomputed from the checkpoint (Wgrad of the second
+ *            linear).
+ *   dh, a    bf16 [rows, 2F or F] (ld_dh) and [rows, F] (ld_a): the same two
+ *            as values, for linears of another format.
+ *   Each output pair or matrix may be NULL.  Everything is formed in fp32 and
+ *   rounded once to its format.
+ */
+fp4_status fp4_act_backward(fp4_act act, const uint8_t* h_codes, const uint8_t* h_scales,
+                            const uint16_t* da, int64_t rows, int64_t cols, int64_t ld,
+                            fp4_format format, uint8_t* dh_codes, uint8_t* dh_scales,
+                            uint8_t* dh_t_codes, uint8_t* dh_t_scales, uint8_t* a_t_codes,
+                            uint8_t* a_t_scales, uint16_t* dh, int64_t ld_dh, uint16_t* a,
+                            int64_t ld_a, void* stream);
 
 /* Static description of a status code. */
 const char* fp4_status_string(fp4_status status);
