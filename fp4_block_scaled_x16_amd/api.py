@@ -71,7 +71,8 @@ class Operand(ctypes.Structure):
 
 _lib = None
 EXPORTS = ("fp4_amax", "fp4_quantize", "fp4_dequantize", "fp4_rht16", "fp4_gemm",
-           "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward",
+           "fp4_gemm_ws", "fp4_gemm_workspace", "fp4_requantize_t", "fp4_act_quantize",
+           "fp4_act_backward",
            "fp4_status_string", "fp4_last_error")
 
 
@@ -101,11 +102,15 @@ def load_library(path=None):
                                      vp, i64, vp, i64, vp]
     lib.fp4_gemm.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), i64, i64, i64, vp,
                              i32, i64, i32, vp]
+    lib.fp4_gemm_ws.argtypes = lib.fp4_gemm.argtypes[:-1] + [vp, i64, vp]
+    lib.fp4_gemm_workspace.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), i64, i64,
+                                       i64, i32]
+    lib.fp4_gemm_workspace.restype = i64
     lib.fp4_selftest_sweep.argtypes = [i32, vp, i32, vp, vp]
     lib.fp4_selftest_gemm_decode.argtypes = [i32, vp, vp]
     lib.fp4_selftest_set_geometry.argtypes = [i32, i32]
     for f in ("fp4_amax", "fp4_quantize", "fp4_quantize_dual", "fp4_dequantize", "fp4_rht16",
-              "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_selftest_sweep", "fp4_selftest_gemm_decode",
+              "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_gemm_ws", "fp4_selftest_sweep", "fp4_selftest_gemm_decode",
               "fp4_selftest_set_geometry"):
         getattr(lib, f).restype = ctypes.c_int
     lib.fp4_status_string.argtypes = [ctypes.c_int]
@@ -610,10 +615,13 @@ def gemm(a: Operand, b: Operand, M, N, K, out=None, accumulate=False, device=Non
     if out.shape[0] < M or out.shape[1] < N:
         raise ValueError("out is smaller than [%d, %d]" % (M, N))
     lib = load_library()
+    t = OUT_TYPES[out.dtype]
     with _current(out.device):
-        _check(lib.fp4_gemm(ctypes.byref(a), ctypes.byref(b), M, N, K, _ptr(out),
-                            OUT_TYPES[out.dtype], out.stride(0), int(bool(accumulate)),
-                            _stream(out.device)), "fp4_gemm")
+        n = lib.fp4_gemm_workspace(ctypes.byref(a), ctypes.byref(b), M, N, K, t)
+        ws = torch.empty(n, dtype=torch.uint8, device=out.device) if n else None
+        _check(lib.fp4_gemm_ws(ctypes.byref(a), ctypes.byref(b), M, N, K, _ptr(out), t,
+                               out.stride(0), int(bool(accumulate)), _ptr(ws), n,
+                               _stream(out.device)), "fp4_gemm")
     return out
 
 

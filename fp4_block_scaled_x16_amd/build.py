@@ -31,7 +31,8 @@ SOURCES = [("quant.hip", "quant", []), ("quant_rowscope.hip", "quant_rowscope", 
     ("gemm_nv_dma.hip", "gemm_nv_dma_%d_%d" % (f, mi), ["-DFP4_DMA_FMT=%d" % f, "-DFP4_DMA_MI=%d" % mi])
     for f in (0, 1) for mi in (4, 3)] + [
     ("quant_fp8.hip", "quant_fp8", []), ("act_fp8.hip", "act_fp8", []),
-    ("gemm_fp8.hip", "gemm_fp8", []), ("fp8_api.cpp", "fp8_api", []),
+    ("gemm_fp8.hip", "gemm_fp8", []), ("gemm_fp8_rows.hip", "gemm_fp8_rows", []),
+    ("fp8_api.cpp", "fp8_api", []),
     ("gemm_mx.hip", "gemm_mx", []), ("gemm_mx_dma.hip", "gemm_mx_dma", []),
     ("selftest.hip", "selftest", []), ("fp4_api.cpp", "fp4_api", [])]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

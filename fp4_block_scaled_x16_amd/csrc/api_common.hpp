@@ -36,6 +36,7 @@ fp4_status dequantize_fp8(fp4_format format, fp4_block block, fp4_scale_layout l
                           const uint8_t* codes, const uint8_t* scales, fp4_global_scope scope,
                           int64_t rows, int64_t cols, void* out, int out_fp32, void* stream);
 fp4_status gemm_fp8(const fp4_operand* A, const fp4_operand* B, int64_t M, int64_t N, int64_t K,
-                    void* D, fp4_out_type d_type, int64_t ldd, int accumulate, void* stream);
+                    void* D, fp4_out_type d_type, int64_t ldd, int accumulate, void* workspace,
+                    int64_t workspace_bytes, void* stream);
 
 }  // namespace fp4api

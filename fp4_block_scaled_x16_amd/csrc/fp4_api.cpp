@@ -440,9 +440,16 @@ FP4_EXPORT fp4_status fp4_rht16(const fp4_quant_desc* d, const uint16_t* x, int6
 FP4_EXPORT fp4_status fp4_gemm(const fp4_operand* A, const fp4_operand* B, int64_t M, int64_t N,
                                int64_t K, void* D, fp4_out_type d_type, int64_t ldd,
                                int accumulate, void* stream) {
+  return fp4_gemm_ws(A, B, M, N, K, D, d_type, ldd, accumulate, nullptr, 0, stream);
+}
+
+FP4_EXPORT fp4_status fp4_gemm_ws(const fp4_operand* A, const fp4_operand* B, int64_t M, int64_t N,
+                                  int64_t K, void* D, fp4_out_type d_type, int64_t ldd,
+                                  int accumulate, void* workspace, int64_t workspace_bytes,
+                                  void* stream) {
   if (!A || !B) return fail(FP4_ERR_ARG, "operand descriptor is null");
   if (is_fp8(A->format) || is_fp8(B->format))
-    return gemm_fp8(A, B, M, N, K, D, d_type, ldd, accumulate, stream);
+    return gemm_fp8(A, B, M, N, K, D, d_type, ldd, accumulate, workspace, workspace_bytes, stream);
   if (!valid_format(A->format) || !valid_format(B->format)) return fail(FP4_ERR_ARG, "bad format");
   if (A->format != B->format) return fail(FP4_ERR_UNSUPPORTED, "A and B formats differ");
   if (A->format == FP4_MXFP8) return fail(FP4_ERR_UNSUPPORTED, "no GEMM takes MXFP8 operands");

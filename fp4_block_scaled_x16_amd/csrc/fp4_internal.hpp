@@ -64,6 +64,8 @@ struct Fp8GemmArgs {
   int64_t ldd;
   int d_bf16, accumulate;
   int a_e5m2;            // operand A is E5M2 (B is E4M3)
+  float* part;           // the caller's workspace (gemm_fp8_workspace bytes), or null
+  int splits;            // set by the launcher
 };
 
 struct Fp8ActArgs {
@@ -144,6 +146,7 @@ hipError_t launch_requant_t_fp8(int e5m2, const uint8_t* codes, const uint8_t* s
 hipError_t launch_act_quant_fp8(const Fp8ActArgs& a, hipStream_t s);
 hipError_t launch_act_grad_fp8(const Fp8ActGradArgs& a, hipStream_t s);
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
+int64_t gemm_fp8_workspace(const Fp8GemmArgs& g);
 // Exhaustive conversion checks (selftest.hip).
 hipError_t launch_selftest_sweep(int kind, const uint32_t* thresholds, int n, uint64_t* result,
                                  hipStream_t s);

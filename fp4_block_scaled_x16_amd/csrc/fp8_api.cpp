@@ -155,8 +155,31 @@ fp4_status dequantize_fp8(fp4_format format, fp4_block block, fp4_scale_layout l
                        "fp4_dequantize launch");
 }
 
+namespace {
+
+fp4lib::Fp8GemmArgs gemm_args(const fp4_operand* const (&ops)[2], int64_t M, int64_t N, int64_t nkb,
+                              fp4_out_type d_type) {
+  fp4lib::Fp8GemmArgs g{};
+  for (int i = 0; i < 2; ++i) {
+    g.codes[i] = ops[i]->codes;
+    g.ld[i] = ops[i]->ld_codes;
+    g.scales[i] = ops[i]->scales;
+    g.s_kblk[i] = ops[i]->scale_stride_kblk;
+  }
+  g.M = M;
+  g.N = N;
+  g.nkb = nkb;
+  g.d_bf16 = d_type == FP4_OUT_BF16;
+  g.a_e5m2 = ops[0]->format == FP4_FP8_E5M2;
+  g.splits = 1;
+  return g;
+}
+
+}  // namespace
+
 fp4_status gemm_fp8(const fp4_operand* A, const fp4_operand* B, int64_t M, int64_t N, int64_t K,
-                    void* D, fp4_out_type d_type, int64_t ldd, int accumulate, void* stream) {
+                    void* D, fp4_out_type d_type, int64_t ldd, int accumulate, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
   if (!is_fp8(A->format) || !is_fp8(B->format))
     return fail(FP4_ERR_UNSUPPORTED, "A and B formats differ");
   if (B->format != FP4_FP8_E4M3)
@@ -193,26 +216,28 @@ fp4_status gemm_fp8(const fp4_operand* A, const fp4_operand* B, int64_t M, int64
   if (!D) return fail(FP4_ERR_ARG, "D is null");
   const int es = d_type == FP4_OUT_BF16 ? 2 : 4;
   if (reinterpret_cast<uintptr_t>(D) % es) return fail(FP4_ERR_ARG, "D must be aligned to its elements");
-  fp4lib::Fp8GemmArgs g{};
-  for (int i = 0; i < 2; ++i) {
-    g.codes[i] = ops[i]->codes;
-    g.ld[i] = ops[i]->ld_codes;
-    g.scales[i] = ops[i]->scales;
-    g.s_kblk[i] = ops[i]->scale_stride_kblk;
-  }
-  g.M = M;
-  g.N = N;
-  g.nkb = kp / 128;
+  if (workspace_bytes < 0 || (workspace && !aligned16(workspace)))
+    return fail(FP4_ERR_ARG, "the workspace must be 16-byte aligned and its size not negative");
+  fp4lib::Fp8GemmArgs g = gemm_args(ops, M, N, kp / 128, d_type);
   g.D = D;
   g.ldd = ldd;
-  g.d_bf16 = d_type == FP4_OUT_BF16;
   g.accumulate = accumulate != 0;
-  g.a_e5m2 = A->format == FP4_FP8_E5M2;
+  if (workspace && workspace_bytes >= fp4lib::gemm_fp8_workspace(g))
+    g.part = static_cast<float*>(workspace);
   return device_status(fp4lib::launch_gemm_fp8(g, static_cast<hipStream_t>(stream)),
                        "fp4_gemm launch");
 }
 
 }  // namespace fp4api
+
+FP4_EXPORT int64_t fp4_gemm_workspace(const fp4_operand* A, const fp4_operand* B, int64_t M, int64_t N,
+                                      int64_t K, fp4_out_type d_type) {
+  if (!A || !B || !is_fp8(A->format) || !is_fp8(B->format) || M <= 0 || N <= 0 || K <= 0 ||
+      M >= kMaxDim || N >= kMaxDim || K >= kMaxDim)
+    return 0;
+  const fp4_operand* ops[2] = {A, B};
+  return fp4lib::gemm_fp8_workspace(gemm_args(ops, M, N, (K + 127) / 128, d_type));
+}
 
 FP4_EXPORT fp4_status fp4_requantize_t(fp4_format format, const uint8_t* codes,
                                        const uint8_t* scales, int64_t rows, int64_t cols,

@@ -22,6 +22,7 @@
 #include "fp4_internal.hpp"
 #include "fp8_common.hpp"
 #include "gemm_common.hpp"
+#include "gemm_fp8_common.hpp"
 
 namespace fp8gemm {
 namespace {
@@ -118,32 +119,6 @@ __device__ __forceinline__ int8v frag(const uint4* base, int slot, int h) {
   return int8v{(int)x.x, (int)x.y, (int)x.z, (int)x.w, (int)y.x, (int)y.y, (int)y.z, (int)y.w};
 }
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-// 8 codes (two words) with their block's scale as bf16, exact.
-template <bool E5>
-__device__ __forceinline__ bf16x8 widen8(uint32_t w0, uint32_t w1, float s) {
-  bf16x2 a, b, c, d;
-  if constexpr (E5) {
-    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, s, false);
-    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w0, s, true);
-    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, s, false);
-    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(w1, s, true);
-  } else {
-    a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, false);
-    b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w0, s, true);
-    c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, false);
-    d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w1, s, true);
-  }
-  return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
-
-// 2^e of scale byte `k` of a word.
-__device__ __forceinline__ float scale_of(uint32_t word, int k) {
-  return __uint_as_float(((word >> (8 * k)) & 0xFFu) << 23);
-}
-
 template <int FA, int MI, int NI, int mi, int ni>
 __device__ __forceinline__ void mfma_one(floatx16 (&acc)[MI][NI], const int8v (&a)[MI],
                                          const int8v (&b)[NI], uint32_t sa, uint32_t sb) {
@@ -236,7 +211,8 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
 template <int FA, bool PREC, int MI, int NI>
 __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
   __shared__ Stage<MI, NI> s0, s1;
-  const fp4lib::Fp8GemmArgs& g = p.g;
+  int kb0, nkb;
+  const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
   int tm, tn;
   tile_coords(p, tm, tn);
   const int64_t m0 = static_cast<int64_t>(tm) * (64 * MI), n0 = static_cast<int64_t>(tn) * (64 * NI);
@@ -251,17 +227,17 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
   for (int j = 0; j < 2 * MI; ++j) {
     const int slot = wave * 16 * MI + 8 * j + (lane >> 3);
     const int64_t r = min(m0 + slot_row<MI>(slot), g.M - 1);
-    src.a[j] = g.codes[0] + r * g.ld[0] + 16 * ((lane & 7) ^ swizzle(slot));
+    src.a[j] = g.codes[0] + r * g.ld[0] + kb0 * kStepBytes + 16 * ((lane & 7) ^ swizzle(slot));
   }
 #pragma unroll
   for (int j = 0; j < 2 * NI; ++j) {
     const int slot = wave * 16 * NI + 8 * j + (lane >> 3);
     const int64_t r = min(n0 + slot_row<NI>(slot), g.N - 1);
-    src.b[j] = g.codes[1] + r * g.ld[1] + 16 * ((lane & 7) ^ swizzle(slot));
+    src.b[j] = g.codes[1] + r * g.ld[1] + kb0 * kStepBytes + 16 * ((lane & 7) ^ swizzle(slot));
   }
   // the scales' pitch is a multiple of 16 and at least the rows
-  src.sa = g.scales[0] + min(m0 + wm * 32 * MI + i * MI, g.s_kblk[0] - MI);
-  src.sb = g.scales[1] + min(n0 + wn * 32 * NI + i * NI, g.s_kblk[1] - NI);
+  src.sa = g.scales[0] + kb0 * g.s_kblk[0] + min(m0 + wm * 32 * MI + i * MI, g.s_kblk[0] - MI);
+  src.sb = g.scales[1] + kb0 * g.s_kblk[1] + min(n0 + wn * 32 * NI + i * NI, g.s_kblk[1] - NI);
   src.ska = g.s_kblk[0];
   src.skb = g.s_kblk[1];
 
@@ -271,7 +247,6 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx16{};
 
-  const int nkb = static_cast<int>(g.nkb);
   // One step on stage C: its DMA has landed for every wave, the other stage
   // N (read in the previous step) takes block kb + 1 (the last one again at
   // the end, unread).
@@ -348,13 +323,359 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
   epilogue<MI, NI>(g, acc, m0 + wm * 32 * MI, n0 + wn * 32 * NI, lane, buf);
 }
 
+
+// ------------------------------------------------------- 256 x 256, 8-bit --
+// The same product to bf16 for large outputs: a wave's 128 x 128 part needs
+// half the LDS reads per MFMA of a 64 x 64 one (the LDS pipe bounds the
+// smaller tile).  Two stages of 64 KiB; the operands of a step's first half
+// are read while the previous step's second half is multiplied, so the one
+// barrier of a step (stage Nx landed, stage C read by every wave) stands
+// between two halves whose operands are in registers.  sched_barrier(0) pins
+// one MFMA and its share of LDS reads and DMA together: left to the scheduler
+// the DMA sinks to the next barrier.
+struct Frags {
+  int8v a[4], b[4];
+};
+
+// Fragment x (0..7: b0 a0 b1 b2 b3 a1 a2 a3, the order of first use) of half KS.
+template <int KS, int X>
+__device__ __forceinline__ void read_frag(const Stage<4, 4>& S, Frags& f, int wm, int wn, int i, int h) {
+  constexpr bool kIsA = X == 1 || X >= 5;
+  constexpr int kT = X == 0 ? 0 : X == 1 ? 0 : X < 5 ? X - 1 : X - 4;
+  if constexpr (kIsA) f.a[kT] = frag<KS>(S.a, wm * 128 + kT * 32 + i, h);
+  else f.b[kT] = frag<KS>(S.b, wn * 128 + kT * 32 + i, h);
+}
+
+// The tile's code rows: a uniform base and a 32-bit offset per DMA (the host
+// keeps 256 row pitches below 2^31).
+struct WideSrc {
+  const uint8_t* base[2];
+  uint32_t off[2][8];
+};
+
+__device__ __forceinline__ void wide_dma(Stage<4, 4>& W, const WideSrc& s, int64_t koff, int wave, int x) {
+  dma16(s.base[x >> 3] + koff + s.off[x >> 3][x & 7],
+        (x < 8 ? W.a : W.b) + wave * 512 + (x & 7) * 64);
+}
+
+// Where a workgroup of the wide kernels stands: its tile, the wave's part, and
+// what its lanes load.
+struct WidePos {
+  int64_t m0, n0;
+  int lane, wave, wm, wn, i, h;
+  WideSrc src;
+  const uint8_t *psa, *psb;      // scales of this lane's 4 rows at the first block
+};
+
+__device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8GemmArgs& g, int kb0) {
+  WidePos w;
+  int tm, tn;
+  tile_coords(p, tm, tn);
+  w.m0 = static_cast<int64_t>(tm) * 256;
+  w.n0 = static_cast<int64_t>(tn) * 256;
+  w.lane = threadIdx.x & 63;
+  w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  w.wm = w.wave >> 1;
+  w.wn = w.wave & 1;
+  w.i = w.lane & 31;
+  w.h = w.lane >> 5;
+  w.src.base[0] = g.codes[0] + w.m0 * g.ld[0] + static_cast<int64_t>(kb0) * kStepBytes;
+  w.src.base[1] = g.codes[1] + w.n0 * g.ld[1] + static_cast<int64_t>(kb0) * kStepBytes;
+  const uint32_t last[2] = {static_cast<uint32_t>(min(g.M - 1 - w.m0, int64_t(255))),
+                            static_cast<uint32_t>(min(g.N - 1 - w.n0, int64_t(255)))};
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const int slot = w.wave * 64 + 8 * (x & 7) + (w.lane >> 3);
+    w.src.off[x >> 3][x & 7] = min(static_cast<uint32_t>(slot_row<4>(slot)), last[x >> 3]) *
+                                   static_cast<uint32_t>(g.ld[x >> 3]) +
+                               16 * ((w.lane & 7) ^ swizzle(slot));
+  }
+  w.psa = g.scales[0] + kb0 * g.s_kblk[0] + min(w.m0 + w.wm * 128 + w.i * 4, g.s_kblk[0] - 4);
+  w.psb = g.scales[1] + kb0 * g.s_kblk[1] + min(w.n0 + w.wn * 128 + w.i * 4, g.s_kblk[1] - 4);
+  return w;
+}
+
+// Half of a step: 16 MFMAs on `cur`, the reads of half KS of stage R into
+// `nxt` beside the first 8 and, if DMA, block kb into stage W beside all.
+template <int FA, int KS, bool DMA, int X = 0>
+__device__ __forceinline__ void wide_half(floatx16 (&acc)[4][4], const Frags& cur, uint32_t sa,
+                                          uint32_t sb, const Stage<4, 4>& R, Frags& nxt,
+                                          Stage<4, 4>& W, int64_t koff, const WidePos& w) {
+  if constexpr (X < 16) {
+    mfma_one<FA, 4, 4, X / 4, X % 4>(acc, cur.a, cur.b, sa, sb);
+    if constexpr (X < 8) read_frag<KS, X>(R, nxt, w.wm, w.wn, w.i, w.h);
+    if constexpr (DMA && X < 8) {
+      wide_dma(W, w.src, koff, w.wave, 2 * X);
+      wide_dma(W, w.src, koff, w.wave, 2 * X + 1);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    wide_half<FA, KS, DMA, X + 1>(acc, cur, sa, sb, R, nxt, W, koff, w);
+  }
+}
+
+template <int FA>
+__global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide(Params p) {
+  __shared__ Stage<4, 4> s0, s1;
+  int kb0, nkb;
+  const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
+  const WidePos w = wide_pos(p, g, kb0);
+
+  floatx16 acc[4][4];
+#pragma unroll
+  for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = floatx16{};
+
+  Frags f0, f1;
+  uint32_t sa, sb;
+  // Step kb on stage C, whose first half's operands and scales are in
+  // registers; block kb + 1 is in (or on its way to) Nx; C takes block kb + 2
+  // (past the end the last one again).  Steps go in pairs: with an odd number
+  // of blocks the last one is multiplied again under scales 2^-127 2^-127,
+  // whose products are zero in fp32 (a loop exit between the two steps makes
+  // the compiler move the 256 accumulators, and spill).
+  auto step = [&](Stage<4, 4>& C, Stage<4, 4>& Nx, int kb) {
+    const int k1 = min(kb + 1, nkb - 1), k2 = min(kb + 2, nkb - 1);
+    const uint32_t na = load_scales<4>(w.psa + k1 * g.s_kblk[0]);
+    const uint32_t nb = load_scales<4>(w.psb + k1 * g.s_kblk[1]);
+    wide_half<FA, 1, false>(acc, f0, sa, sb, C, f1, C, 0, w);
+    wait_vmcnt<0>();
+    ring_barrier();
+    wide_half<FA, 0, true>(acc, f1, sa, sb, Nx, f0, C, static_cast<int64_t>(k2) * kStepBytes, w);
+    sa = kb + 1 < nkb ? na : 0;
+    sb = kb + 1 < nkb ? nb : 0;
+  };
+  if (nkb > 0) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) wide_dma(s0, w.src, 0, w.wave, x);
+    sa = load_scales<4>(w.psa);
+    sb = load_scales<4>(w.psb);
+    wait_vmcnt<0>();
+    ring_barrier();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) wide_dma(s1, w.src, nkb > 1 ? kStepBytes : 0, w.wave, x);
+#pragma unroll
+    for (int mi = 0; mi < 4; ++mi) {
+      f0.a[mi] = frag<0>(s0.a, w.wm * 128 + mi * 32 + w.i, w.h);
+      f0.b[mi] = frag<0>(s0.b, w.wn * 128 + mi * 32 + w.i, w.h);
+    }
+    for (int kb = 0; kb < nkb; kb += 2) {
+      step(s0, s1, kb);
+      step(s1, s0, kb + 1);
+    }
+  }
+  wait_vmcnt<0>();
+  ring_barrier();
+  constexpr int kBuf = 32 * (32 * 4 + 4);
+  float* buf = reinterpret_cast<float*>(w.wave < 2 ? &s0 : &s1) + (w.wave & 1) * kBuf;
+  epilogue<4, 4>(g, acc, w.m0 + w.wm * 128, w.n0 + w.wn * 128, w.lane, buf);
+}
+
+// ------------------------------------------------------ 256 x 256, bf16 ---
+// The product to fp32 for large outputs: the wide tile with its codes widened
+// to bf16 in registers, two converts beside each MFMA.  A step is four
+// quarters of 32 K values; a lane's 16 bytes of each row in a quarter are two
+// products' operands (halves).  While a half is multiplied the next one is
+// widened, from bytes read from LDS a quarter ahead; the barrier stands before
+// the last quarter, whose bytes are then in registers, so the DMA of the
+// stage that it frees has most of a step to land.
+struct Raw {
+  uint4 a[4], b[4];
+};
+struct Wide {
+  uint32_t a[4][4], b[4][4];
+};
+
+// Tile t (0..3 B, 4..7 A) of quarter Q.
+template <int Q>
+__device__ __forceinline__ void read_raw(const Stage<4, 4>& S, Raw& r, int t, const WidePos& w) {
+  const int q = 2 * Q + w.h;
+  if (t < 4) {
+    const int slot = w.wn * 128 + t * 32 + w.i;
+    r.b[t] = S.b[slot * kChunks + (q ^ swizzle(slot))];
+  } else {
+    const int slot = w.wm * 128 + (t - 4) * 32 + w.i;
+    r.a[t - 4] = S.a[slot * kChunks + (q ^ swizzle(slot))];
+  }
+}
+
+// Word w (0, 1) of tile t's half HALF as four bf16.
+template <int FA, int HALF>
+__device__ __forceinline__ void widen_word(const Raw& r, Wide& f, int t, int w, const float (&s)[8]) {
+  const uint4& c = t < 4 ? r.b[t & 3] : r.a[t & 3];
+  const uint32_t x = HALF ? (w ? c.w : c.z) : (w ? c.y : c.x);
+  uint32_t* d = t < 4 ? f.b[t & 3] : f.a[t & 3];
+  bf16x2 lo, hi;
+  if (t >= 4 && FA == 1) {
+    lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, s[t], false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(x, s[t], true);
+  } else {
+    lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s[t], false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s[t], true);
+  }
+  d[2 * w] = __builtin_bit_cast(uint32_t, lo);
+  d[2 * w + 1] = __builtin_bit_cast(uint32_t, hi);
+}
+
+__device__ __forceinline__ bf16x8 as_bf16(const uint32_t (&w)[4]) {
+  return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
+// One half: 16 MFMAs on `cur`; beside MFMA x the widening of a word of half
+// NHALF of `raw` into `nxt`; if READ, beside the first 8 the bytes of quarter RQ
+// of stage R; if DMA, beside each the x-th DMA of block koff into stage W.
+template <int FA, int NHALF, bool READ, int RQ, bool DMA>
+__device__ __forceinline__ void prec_half(floatx16 (&acc)[4][4], const Wide& cur, Wide& nxt,
+                                          const Raw& raw, const float (&s)[8], const Stage<4, 4>& R,
+                                          Raw& rnext, Stage<4, 4>& W, int64_t koff, const WidePos& w) {
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    acc[x / 4][x % 4] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(cur.b[x % 4]), as_bf16(cur.a[x / 4]),
+                                                                acc[x / 4][x % 4], 0, 0, 0);
+    widen_word<FA, NHALF>(raw, nxt, x >> 1, x & 1, s);
+    if constexpr (READ) {
+      if (x < 8) read_raw<RQ>(R, rnext, x, w);
+    }
+    if constexpr (DMA) wide_dma(W, w.src, koff, w.wave, x);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+template <int FA>
+__global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_f32(Params p) {
+  __shared__ Stage<4, 4> s0, s1;
+  int kb0, nkb;
+  const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
+  const WidePos w = wide_pos(p, g, kb0);
+
+  floatx16 acc[4][4];
+#pragma unroll
+  for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = floatx16{};
+
+  Raw r0, r1;
+  Wide f0, f1;
+  float s[8];                 // block scales of B's and A's four tiles
+  auto set_scales = [&](uint32_t wa, uint32_t wb) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      s[t] = scale_of(wb, t);
+      s[4 + t] = scale_of(wa, t);
+    }
+  };
+  // Step kb on stage C: the bytes of its quarter 0 and its first half widened
+  // are in registers, with its scales; then as in k_gemm_fp8_wide.
+  auto step = [&](Stage<4, 4>& C, Stage<4, 4>& Nx, int kb) {
+    const int k1 = min(kb + 1, nkb - 1), k2 = min(kb + 2, nkb - 1);
+    const uint32_t na = load_scales<4>(w.psa + k1 * g.s_kblk[0]);
+    const uint32_t nb = load_scales<4>(w.psb + k1 * g.s_kblk[1]);
+    const int64_t koff = static_cast<int64_t>(k2) * kStepBytes;
+    prec_half<FA, 1, true, 1, false>(acc, f0, f1, r0, s, C, r1, C, 0, w);
+    prec_half<FA, 0, false, 0, false>(acc, f1, f0, r1, s, C, r0, C, 0, w);
+    prec_half<FA, 1, true, 2, false>(acc, f0, f1, r1, s, C, r0, C, 0, w);
+    prec_half<FA, 0, false, 0, false>(acc, f1, f0, r0, s, C, r1, C, 0, w);
+    prec_half<FA, 1, true, 3, false>(acc, f0, f1, r0, s, C, r1, C, 0, w);
+    prec_half<FA, 0, false, 0, false>(acc, f1, f0, r1, s, C, r0, C, 0, w);
+    wait_vmcnt<0>();
+    ring_barrier();
+    prec_half<FA, 1, true, 0, true>(acc, f0, f1, r1, s, Nx, r0, C, koff, w);
+    set_scales(kb + 1 < nkb ? na : 0, kb + 1 < nkb ? nb : 0);
+    prec_half<FA, 0, false, 0, false>(acc, f1, f0, r0, s, C, r1, C, 0, w);
+  };
+  if (nkb > 0) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) wide_dma(s0, w.src, 0, w.wave, x);
+    set_scales(load_scales<4>(w.psa), load_scales<4>(w.psb));
+    wait_vmcnt<0>();
+    ring_barrier();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) wide_dma(s1, w.src, nkb > 1 ? kStepBytes : 0, w.wave, x);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) read_raw<0>(s0, r0, t, w);
+#pragma unroll
+    for (int t = 0; t < 16; ++t) widen_word<FA, 0>(r0, f0, t >> 1, t & 1, s);
+    for (int kb = 0; kb < nkb; kb += 2) {
+      step(s0, s1, kb);
+      step(s1, s0, kb + 1);
+    }
+  }
+  wait_vmcnt<0>();
+  ring_barrier();
+  constexpr int kBuf = 32 * (32 * 4 + 4);
+  float* buf = reinterpret_cast<float*>(w.wave < 2 ? &s0 : &s1) + (w.wave & 1) * kBuf;
+  epilogue<4, 4>(g, acc, w.m0 + w.wm * 128, w.n0 + w.wn * 128, w.lane, buf);
+}
+
 template <int FA, bool PREC, int MI, int NI>
-hipError_t launch(const fp4lib::Fp8GemmArgs& g, hipStream_t s) {
+void launch_tile(const fp4lib::Fp8GemmArgs& g, hipStream_t s) {
   Params p{g, static_cast<int>((g.M + 64 * MI - 1) / (64 * MI)),
            static_cast<int>((g.N + 64 * NI - 1) / (64 * NI))};
-  hipLaunchKernelGGL((k_gemm_fp8<FA, PREC, MI, NI>), dim3(p.tiles_m * p.tiles_n), dim3(kThreads), 0,
-                     s, p);
-  return hipGetLastError();
+  const dim3 grid(p.tiles_m * p.tiles_n, g.splits);
+  if constexpr (MI == 4) {
+    if constexpr (PREC) hipLaunchKernelGGL(k_gemm_fp8_wide_f32<FA>, grid, dim3(kThreads), 0, s, p);
+    else hipLaunchKernelGGL(k_gemm_fp8_wide<FA>, grid, dim3(kThreads), 0, s, p);
+  } else {
+    hipLaunchKernelGGL((k_gemm_fp8<FA, PREC, MI, NI>), grid, dim3(kThreads), 0, s, p);
+  }
+}
+
+// D from the partial sums of `splits` workgroups per tile, in their order.
+__global__ __launch_bounds__(256) void k_gemm_fp8_join(fp4lib::Fp8GemmArgs g) {
+  const int64_t np = part_pitch(g.N), per_row = np / 4, n = g.M * per_row;
+  for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < n;
+       id += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t row = id / per_row, col = (id - row * per_row) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int k = 0; k < g.splits; ++k) {
+      const float4 a = *reinterpret_cast<const float4*>(g.part + (k * g.M + row) * np + col);
+      v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+    }
+    const float r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (col + e >= g.N) continue;
+      if (g.d_bf16) {
+        uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col + e;
+        const float o = g.accumulate ? __uint_as_float(static_cast<uint32_t>(*d) << 16) : 0.0f;
+        *d = static_cast<uint16_t>(fp8dev::to_bf16(g.accumulate ? r[e] + o : r[e]));
+      } else {
+        float* d = static_cast<float*>(g.D) + row * g.ldd + col + e;
+        *d = g.accumulate ? *d + r[e] : r[e];
+      }
+    }
+  }
+}
+
+// How a product runs: the kernel (0: few rows; 2, 4: tiles of 128, 256) and
+// the workgroups that share a tile's K.
+struct Plan {
+  int kind, splits;
+};
+
+Plan plan_of(const fp4lib::Fp8GemmArgs& g) {
+  const int64_t cus = fp4lib::device_cu_count();
+  Plan p{2, 1};
+  const int64_t wide = ((g.M + 255) / 256) * ((g.N + 255) / 256);
+  if (g.M <= kMaxRows) {
+    p.kind = 0;
+    p.splits = rows_splits(g);
+  } else if (wide >= cus / 2 && g.ld[0] < (1 << 23) && g.ld[1] < (1 << 23)) {
+    p.kind = 4;
+  } else {
+    const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
+    while (tiles * p.splits * 2 <= 2 * cus && g.nkb >= 8 * p.splits && p.splits < 16) p.splits *= 2;
+  }
+  return p;
+}
+
+template <int FA>
+void run(const fp4lib::Fp8GemmArgs& g, int kind, hipStream_t s) {
+  if (kind == 0) launch_rows(g, s);
+  else if (kind == 4 && g.d_bf16) launch_tile<FA, false, 4, 4>(g, s);
+  else if (kind == 4) launch_tile<FA, true, 4, 4>(g, s);
+  else if (g.d_bf16) launch_tile<FA, false, 2, 2>(g, s);
+  else launch_tile<FA, true, 2, 2>(g, s);
 }
 
 }  // namespace
@@ -362,10 +683,25 @@ hipError_t launch(const fp4lib::Fp8GemmArgs& g, hipStream_t s) {
 
 namespace fp4lib {
 
-hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s) {
-  using fp8gemm::launch;
-  if (g.a_e5m2) return g.d_bf16 ? launch<1, false, 2, 2>(g, s) : launch<1, true, 2, 2>(g, s);
-  return g.d_bf16 ? launch<0, false, 2, 2>(g, s) : launch<0, true, 2, 2>(g, s);
+int64_t gemm_fp8_workspace(const Fp8GemmArgs& g) {
+  const int splits = fp8gemm::plan_of(g).splits;
+  return splits > 1 ? splits * g.M * fp8gemm::part_pitch(g.N) * 4 : 0;
+}
+
+hipError_t launch_gemm_fp8(const Fp8GemmArgs& args, hipStream_t s) {
+  Fp8GemmArgs g = args;
+  fp8gemm::Plan p = fp8gemm::plan_of(g);
+  if (!g.part) p.splits = 1;            // without a workspace
+  g.splits = p.splits;
+  if (g.a_e5m2) fp8gemm::run<1>(g, p.kind, s);
+  else fp8gemm::run<0>(g, p.kind, s);
+  if (g.splits > 1) {
+    const int64_t n = g.M * fp8gemm::part_pitch(g.N) / 4;
+    const int64_t cap = static_cast<int64_t>(device_cu_count()) * 8, want = (n + 255) / 256;
+    hipLaunchKernelGGL(fp8gemm::k_gemm_fp8_join, dim3(static_cast<uint32_t>(want < cap ? want : cap)),
+                       dim3(256), 0, s, g);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace fp4lib

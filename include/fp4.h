@@ -406,13 +406,33 @@ typedef enum fp4_out_type_e FP4_ENUM_INT { FP4_OUT_F32 = 0, FP4_OUT_BF16 = 1 } f
  * per element; a bf16 D is that fp32 value rounded to bf16.  FP8 with a bf16
  * D: the 8-bit matrix instructions add 8 products at a time on a grid 2^-13
  * below the largest one's binade, so the value before its rounding is within
- * 1e-5 sum |a b| + 7 * 2^-13 of each group's largest |a b| (fp32 D: products
- * and sums in fp32).
+ * 1e-5 sum |a b| + 7 * 2^-13 of each group's largest |a b|, subnormal
+ * elements counted as the smallest normal one (fp32 D: products and sums in
+ * fp32).
  * K == 0 writes zeros (or leaves D unchanged when accumulating).
  */
 fp4_status fp4_gemm(const fp4_operand* A /* host */, const fp4_operand* B /* host */,
                     int64_t M, int64_t N, int64_t K, void* D, fp4_out_type d_type,
                     int64_t ldd, int accumulate, void* stream);
+
+/*
+ * fp4_gemm_ws -- fp4_gemm with a workspace, which lets an FP8 product with few
+ * output tiles share each tile's K among workgroups (their fp32 sums are
+ * joined in a fixed order by a second kernel on the stream).
+ *   workspace  device, 16-byte aligned, of workspace_bytes bytes, or NULL; its
+ *           contents before and after are of no account, and calls that may
+ *           run at the same time need one each.  With less than
+ *           fp4_gemm_workspace bytes the product runs unshared.
+ * fp4_gemm_workspace returns the bytes that a product can use on the current
+ * device, 0 where it needs none (the FP4 formats, many tiles, invalid
+ * arguments).
+ */
+fp4_status fp4_gemm_ws(const fp4_operand* A /* host */, const fp4_operand* B /* host */,
+                       int64_t M, int64_t N, int64_t K, void* D, fp4_out_type d_type,
+                       int64_t ldd, int accumulate, void* workspace, int64_t workspace_bytes,
+                       void* stream);
+int64_t fp4_gemm_workspace(const fp4_operand* A /* host */, const fp4_operand* B /* host */,
+                           int64_t M, int64_t N, int64_t K, fp4_out_type d_type);
 
 /*
  * fp4_requantize_t -- the COLWISE operand of a matrix held as ROWWISE FP8

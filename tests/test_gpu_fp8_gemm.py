@@ -17,6 +17,9 @@ TOL = 1e-5
 # The 8-bit MFMA adds 8 products on the grid 2^-13 below the largest one's
 # binade and cuts the others off there: at most 7 of the 8 lose less than
 # 2^-13 of the largest, so a group loses less than 7 * 2^-13 of its sum |a b|.
+# The binade is the sum of the operands' exponent fields, a subnormal's (and, at
+# worst, a zero's) being that of the smallest normal number: so |a| and |b|
+# count as at least 2^-6 (E5M2: 2^-14) of their blocks' scales.
 CUT = 7 * 2.0 ** -13
 
 
@@ -31,9 +34,21 @@ def operands(M, N, K, fa="fp8", block="2d", seed=0):
     return a, b
 
 
-def close(d, ref, bound):
+def floored(q):
+    """|values|, at least the smallest normal element of their blocks."""
+    fmt = "fp8" if q.fmt == api.FP8_E4M3 else "fp8_e5m2"
+    e = q.scales.cpu().numpy()[:, :q.rows].T.astype(np.int64) - 127 + 1 - fp8.FORMATS[fmt][0]
+    return np.maximum(np.abs(values(q)), np.repeat(np.exp2(e.astype(np.float64)), 128, 1))
+
+
+def product(a, b):
+    """(D, sum |a b|, what the 8-bit MFMA may cut off)"""
+    return (*fp8.gemm(values(a), values(b)), CUT * (floored(a) @ floored(b).T))
+
+
+def close(d, ref, bound, cut):
     if d.dtype == torch.bfloat16:
-        tol = (TOL + CUT) * bound
+        tol = TOL * bound + cut
         half = np.exp2(np.floor(np.log2(np.maximum(np.abs(ref) + tol, 1e-300))) - 8)
         bad = np.abs(as64(d) - ref) > tol + half
         assert not bad.any(), np.argwhere(bad)[:5].tolist()
@@ -47,7 +62,11 @@ def close(d, ref, bound):
 SHAPES = [(1, 1, 1), (1, 128, 128), (1, 200, 1000), (2, 64, 256), (15, 33, 127), (16, 512, 640),
           (17, 96, 300), (32, 130, 2048), (33, 256, 1111), (64, 64, 512), (65, 192, 384),
           (100, 1000, 260), (128, 128, 1024), (200, 129, 5000), (257, 255, 129), (256, 512, 256),
-          (300, 700, 384), (513, 260, 128)]
+          (300, 700, 384), (513, 260, 128),
+          # enough outputs for the 256 x 256 tiles; one, two, three and six K blocks
+          (2049, 4097, 128), (2100, 4200, 256), (2304, 4096, 300), (2100, 4100, 700),
+          # few outputs and a long K: K shared among workgroups
+          (1, 64, 20000), (20, 64, 20000), (64, 300, 20000), (130, 257, 20000)]
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
@@ -56,19 +75,20 @@ def test_gemm(M, N, K, out):
     a, b = operands(M, N, K)
     d = api.gemm(a.operand(), b.operand(), M, N, K, out_dtype=out)
     assert d.dtype == out and d.device == a.codes.device
-    close(d, *fp8.gemm(values(a), values(b)))
+    close(d, *product(a, b))
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 130, 1000), (16, 96, 256), (40, 200, 640), (100, 300, 1111),
-                                   (520, 520, 640), (300, 2048, 1024)])
+                                   (520, 520, 640), (300, 2048, 1024), (2300, 4200, 520)])
 def test_e5m2_gradient_and_1d_operands(M, N, K):
     a, b = operands(M, N, K, "fp8_e5m2", "1d", 7)
-    close(api.gemm(a.operand(), b.operand(), M, N, K), *fp8.gemm(values(a), values(b)))
+    close(api.gemm(a.operand(), b.operand(), M, N, K), *product(a, b))
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M,N,K", [(1, 40, 256), (30, 130, 130), (64, 128, 256), (130, 257, 300),
-                                   (300, 512, 256)])
+                                   (300, 512, 256), (2100, 4100, 384), (20, 130, 9000),
+                                   (100, 200, 9000)])
 @pytest.mark.parametrize("off,ld", [(0, 0), (4, 8), (1, 3)])
 def test_accumulate_into_views(M, N, K, out, off, ld):
     """The old D (bf16: widened) is added in fp32 before the one rounding; views
@@ -77,16 +97,16 @@ def test_accumulate_into_views(M, N, K, out, off, ld):
     big = torch.randn((M + 2, N + off + ld + (8 if off == 0 else 0)), generator=torch.Generator().manual_seed(M)).to(out).to(DEV)
     before = big.clone()
     view = big[1:M + 1, off:off + N]
-    ref, bound = fp8.gemm(values(a), values(b))
+    ref, bound, cut = product(a, b)
     old = as64(view)
     api.gemm(a.operand(), b.operand(), M, N, K, out=view, accumulate=True)
     # one more fp32 rounding of the sum: 2^-24 of |old| + |product|
-    close(view, ref + old, bound + np.abs(old) * (2.0 ** -24 / TOL))
+    close(view, ref + old, bound + np.abs(old) * (2.0 ** -24 / TOL), cut)
     again = big.clone()
     big[1:M + 1, off:off + N] = before[1:M + 1, off:off + N]
     assert torch.equal(big, before)
     api.gemm(a.operand(), b.operand(), M, N, K, out=view)
-    close(view, ref, bound)
+    close(view, ref, bound, cut)
     assert not torch.equal(again, big)
 
 
@@ -103,18 +123,46 @@ def test_rows_do_not_depend_on_their_neighbours(M):
     w[7] *= 2.0 ** -50
     a, b = api.quantize(bf16(x).to(DEV), "fp8"), api.quantize(bf16(w).to(DEV), "fp8")
     d = api.gemm(a.operand(), b.operand(), M, N, K)
-    close(d, *fp8.gemm(values(a), values(b)))
+    close(d, *product(a, b))
     assert not d[:, 5].any()
+
+
+def test_workspace():
+    """Without a workspace, or with one that is too small, the product runs
+    unshared, within the same bound; with one it is the same every time."""
+    import ctypes
+    lib = api.load_library()
+    M, N, K = 24, 256, 9000
+    a, b = operands(M, N, K)
+    ref, bound, cut = product(a, b)
+    oa, ob = a.operand(), b.operand()
+    n = lib.fp4_gemm_workspace(ctypes.byref(oa), ctypes.byref(ob), M, N, K, 0)
+    assert n > 0 and n % (4 * M * N) == 0
+    assert lib.fp4_gemm_workspace(ctypes.byref(oa), ctypes.byref(ob), 0, N, K, 0) == 0
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    d = torch.empty((M, N), device=DEV)
+    for size in (None, 0, n - 16, n):
+        ws = None if size is None else torch.full((n + 4096,), 0xFF, dtype=torch.uint8, device=DEV)
+        args = (ctypes.byref(oa), ctypes.byref(ob), M, N, K, ctypes.c_void_p(d.data_ptr()), 0, N, 0)
+        if size is None:
+            assert lib.fp4_gemm(*args, s) == 0
+        else:
+            assert lib.fp4_gemm_ws(*args, ctypes.c_void_p(ws.data_ptr()), size, s) == 0
+            assert bool((ws[size:] == 0xFF).all())
+        close(d, ref, bound, cut)
+    assert torch.equal(d, api.gemm(oa, ob, M, N, K))
+    bad = ctypes.c_void_p(ws.data_ptr() + 8)
+    assert lib.fp4_gemm_ws(*args, bad, n, s) == 1 and lib.fp4_gemm_ws(*args, None, -1, s) == 1
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("fa", ["fp8", "fp8_e5m2"])
-@pytest.mark.parametrize("M", [3, 40, 150, 300])
-def test_exact_sums(M, fa, out):
+@pytest.mark.parametrize("M,N", [(3, 270), (20, 270), (40, 270), (150, 270), (300, 270), (2500, 3500)])
+def test_exact_sums(M, N, fa, out):
     """Small whole numbers: every product (1 to 64, within the 13 bits of either
     instruction) and partial sum is exact in fp32; bf16 is the sum rounded."""
     rng = np.random.default_rng(5)
-    N, K = 270, 1000
+    K = 1000
     x, w = rng.integers(-8, 9, (M, K)), rng.integers(-8, 9, (N, K))
     if fa == "fp8_e5m2":
         x = np.where(np.abs(x) == 7, 6, np.where(np.abs(x) == 5, 4, x))    # 3 significant bits
@@ -176,10 +224,10 @@ def test_operands_of_fewer_rows():
     """The first M tokens of a larger code matrix."""
     a, b = operands(300, 256, 512)
     whole = api.gemm(a.operand(), b.operand(), 300, 256, 512)
-    ref, bound = fp8.gemm(values(a), values(b))
+    ref, bound, cut = product(a, b)
     for M in (1, 20, 100, 299):
         d = api.gemm(a.operand(), b.operand(), M, 256, 512)
-        close(d, ref[:M], bound[:M])
+        close(d, ref[:M], bound[:M], cut[:M])
     assert torch.equal(whole, api.gemm(a.operand(), b.operand(), 300, 256, 512))
 
 
@@ -198,15 +246,16 @@ def test_a_layers_three_products():
     dw = torch.zeros((O, I), device=DEV)
     for k in range(2):
         api.gemm(qdyt.operand(), qxt.operand(), O, I, T, out=dw, accumulate=True)
-    close(y, *fp8.gemm(values(qx), values(qw)))
-    close(dx, *fp8.gemm(values(qdy), values(qwt)))
-    ref, bound = fp8.gemm(values(qdyt), values(qxt))
-    close(dw, 2 * ref, 2 * bound)
+    close(y, *product(qx, qw))
+    close(dx, *product(qdy, qwt))
+    ref, bound, cut = product(qdyt, qxt)
+    close(dw, 2 * ref, 2 * bound, 2 * cut)
 
 
-@pytest.mark.parametrize("M", [1, 24, 64, 200, 600])
-def test_captured_graph(M):
-    N, K = 264, 640
+@pytest.mark.parametrize("M,K", [(1, 640), (24, 640), (24, 9000), (64, 640), (200, 640), (200, 9000),
+                                 (600, 640)])
+def test_captured_graph(M, K):
+    N = 264
     (a0, b), (a1, _) = operands(M, N, K, seed=1), operands(M, N, K, seed=5)
     a, _ = operands(M, N, K, seed=1)
     g = torch.cuda.CUDAGraph()
