@@ -7,8 +7,8 @@ library's HIP kernels.  The library is loaded on first use; if it is missing
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -136,12 +136,28 @@ def _stream(device=None):
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
-def _current(device):
-    """The context in which a call on `device` launches: that device made
+# the current stream's handle, without an object around it where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _launch(what, fn, device, *args):
+    """fn(*args, stream) on the device's current stream, with the device made
     current where another one is."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if device.type != "cuda":
+        raise ValueError("%s: tensors must be on the GPU (got %s)" % (what, device))
+    if device.index == torch.cuda.current_device():
+        stream = (_raw_stream(device.index) if _raw_stream
+                  else torch.cuda.current_stream(device).cuda_stream)
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if status:
+        _check(status, what)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _as_bf16_bits(x):
@@ -387,23 +403,25 @@ def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpo
     blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
     q = [_fp8_buffers(f, R, C, x.device, blk)] if row else []
     q += [_fp8_buffers(f, C, R, x.device, blk)] if col else []
-    d = [QuantDesc(f, blk, o, SR if rnd == "sr" else RNE, 0, 0, int(bool(rht)), 0, 448.0,
-                   int(amax_in is not None), int(bool(emit_transpose)), int(scale_layout), 0,
-                   (ctypes.c_uint32 * 3)(), 0, GLOBAL_SCOPES[global_scope], COUNT_LEVELS[count])
+    d = [ctypes.byref(_fp8_desc(f, blk, o, SR if rnd == "sr" else RNE, bool(rht),
+                                amax_in is not None, bool(emit_transpose), int(scale_layout),
+                                GLOBAL_SCOPES[global_scope], COUNT_LEVELS[count]))
          for o, on in ((ROWWISE, row), (COLWISE, col)) if on]
     lib = load_library()
-    with _current(x.device):
-        if row and col:
-            _check(lib.fp4_quantize_dual(ctypes.byref(d[0]), ctypes.byref(d[1]), _ptr(x), R, C,
-                                         _ld(x), _ptr(q[0].codes), _ptr(q[0].scales),
-                                         _ptr(q[1].codes), _ptr(q[1].scales), None, None, None,
-                                         None, _ptr(counters), _stream(x.device)),
-                   "fp4_quantize_dual")
-        else:
-            _check(lib.fp4_quantize(ctypes.byref(d[0]), _ptr(x), R, C, _ld(x),
-                                    _ptr(q[0].codes), _ptr(q[0].scales), None, None, None,
-                                    _ptr(counters), _stream(x.device)), "fp4_quantize")
+    if row and col:
+        _launch("fp4_quantize_dual", lib.fp4_quantize_dual, x.device, d[0], d[1], x.data_ptr(), R,
+                C, _ld(x), q[0].codes.data_ptr(), q[0].scales.data_ptr(), q[1].codes.data_ptr(),
+                q[1].scales.data_ptr(), None, None, None, None, _addr(counters))
+    else:
+        _launch("fp4_quantize", lib.fp4_quantize, x.device, d[0], x.data_ptr(), R, C, _ld(x),
+                q[0].codes.data_ptr(), q[0].scales.data_ptr(), None, None, None, _addr(counters))
     return tuple(q)
+
+
+@functools.lru_cache(maxsize=64)
+def _fp8_desc(f, block, orient, rnd, rht, amax_given, emit_transpose, layout, scope, count):
+    return QuantDesc(f, block, orient, rnd, 0, 0, int(rht), 0, 448.0, int(amax_given),
+                     int(emit_transpose), layout, 0, (ctypes.c_uint32 * 3)(), 0, scope, count)
 
 
 def fp8_matrix(codes, scales, rows, cols, fmt="fp8"):
@@ -441,11 +459,9 @@ def requantize_t(q: Quantized):
     normal range of their new block."""
     _fp8_only(q, "requantize_t")
     t = _fp8_buffers(q.fmt, q.cols, q.rows, q.codes.device)
-    lib = load_library()
-    with _current(q.codes.device):
-        _check(lib.fp4_requantize_t(q.fmt, _ptr(q.codes), _ptr(q.scales), q.rows, q.cols,
-                                    _ptr(t.codes), _ptr(t.scales), _stream(q.codes.device)),
-               "fp4_requantize_t")
+    _launch("fp4_requantize_t", load_library().fp4_requantize_t, q.codes.device, q.fmt,
+            q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, t.codes.data_ptr(),
+            t.scales.data_ptr())
     return t
 
 
@@ -497,12 +513,9 @@ def act_quantize(h, act="swiglu", a="fp8", checkpoint=True):
     qa = _fp8_buffers(FP8_E4M3, rows, cols, dev) if a == "fp8" else None
     av = _bf16_rows(rows, cols, dev) if a == "bf16" else None
     qh = _fp8_buffers(FP8_E4M3, rows, _checkpoint_cols(act, cols), dev) if checkpoint else None
-    lib = load_library()
-    with _current(dev):
-        _check(lib.fp4_act_quantize(ACTS[act], _ptr(h), rows, cols, _ld(h),
-                                    _ptr(qa and qa.codes), _ptr(qa and qa.scales), _ptr(av),
-                                    0 if av is None else _ld(av), _ptr(qh and qh.codes),
-                                    _ptr(qh and qh.scales), _stream(dev)), "fp4_act_quantize")
+    _launch("fp4_act_quantize", load_library().fp4_act_quantize, dev, ACTS[act], h.data_ptr(), rows,
+            cols, _ld(h), qa and qa.codes.data_ptr(), qa and qa.scales.data_ptr(), _addr(av),
+            0 if av is None else _ld(av), qh and qh.codes.data_ptr(), qh and qh.scales.data_ptr())
     return (av if a == "bf16" else qa), qh
 
 
@@ -538,13 +551,10 @@ def act_backward(qh: Quantized, da, act="swiglu", fmt="fp8", out="fp8"):
         o = [t for p in q for t in (p.codes, p.scales)]
     else:
         dh, av = _bf16_rows(rows, halves * cols, dev), _bf16_rows(rows, cols, dev)
-    lib = load_library()
-    with _current(dev):
-        _check(lib.fp4_act_backward(ACTS[act], _ptr(qh.codes), _ptr(qh.scales), _ptr(da), rows,
-                                    cols, _ld(da), f, *[_ptr(t) for t in o], _ptr(dh),
-                                    0 if dh is None else _ld(dh), _ptr(av),
-                                    0 if av is None else _ld(av), _stream(dev)),
-               "fp4_act_backward")
+    _launch("fp4_act_backward", load_library().fp4_act_backward, dev, ACTS[act],
+            qh.codes.data_ptr(), qh.scales.data_ptr(), da.data_ptr(), rows, cols, _ld(da), f,
+            *[_addr(t) for t in o], _addr(dh), 0 if dh is None else _ld(dh), _addr(av),
+            0 if av is None else _ld(av))
     return q if out == "fp8" else (dh, av)
 
 
@@ -615,14 +625,25 @@ def gemm(a: Operand, b: Operand, M, N, K, out=None, accumulate=False, device=Non
     if out.shape[0] < M or out.shape[1] < N:
         raise ValueError("out is smaller than [%d, %d]" % (M, N))
     lib = load_library()
-    t = OUT_TYPES[out.dtype]
-    with _current(out.device):
-        n = lib.fp4_gemm_workspace(ctypes.byref(a), ctypes.byref(b), M, N, K, t)
-        ws = torch.empty(n, dtype=torch.uint8, device=out.device) if n else None
-        _check(lib.fp4_gemm_ws(ctypes.byref(a), ctypes.byref(b), M, N, K, _ptr(out), t,
-                               out.stride(0), int(bool(accumulate)), _ptr(ws), n,
-                               _stream(out.device)), "fp4_gemm")
+    t, dev = OUT_TYPES[out.dtype], out.device
+    ws, n = None, 0
+    if a.format in FP8 and b.format in FP8:
+        n = _gemm_workspace(dev, M, N, K, t, a.format, b.format, a.ld_codes, b.ld_codes)
+        if n:
+            ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _launch("fp4_gemm", lib.fp4_gemm_ws, dev, ctypes.byref(a), ctypes.byref(b), M, N, K,
+            out.data_ptr(), t, out.stride(0), int(bool(accumulate)), _addr(ws), n)
     return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _gemm_workspace(device, M, N, K, out_type, fmt_a, fmt_b, ld_a, ld_b):
+    """Bytes of workspace that an FP8 product of these sizes can use."""
+    a = Operand(fmt_a, None, ld_a, None, 0, 0, 1, None, SCALES_KMAJOR, GLOBAL_TENSOR)
+    b = Operand(fmt_b, None, ld_b, None, 0, 0, 1, None, SCALES_KMAJOR, GLOBAL_TENSOR)
+    with torch.cuda.device(device):
+        return load_library().fp4_gemm_workspace(ctypes.byref(a), ctypes.byref(b), M, N, K,
+                                                 out_type)
 
 
 # ------------------------------------------------------------- self-test --

@@ -71,11 +71,13 @@ __device__ __forceinline__ void unpack4(uint32_t w, float* v) {
   v[3] = hi.y;
 }
 
-// fp32 -> bf16, nearest even; NaN stays a NaN.
-__device__ __forceinline__ uint32_t to_bf16(float v) {
-  const uint32_t u = __float_as_uint(v);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (u >> 16) | 0x40u;
-  return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+// fp32 -> bf16, nearest even (gfx950's packed convert); NaN stays a NaN.
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, bf16x2{static_cast<__bf16>(lo), static_cast<__bf16>(hi)});
+}
+__device__ __forceinline__ uint16_t to_bf16(float v) {
+  return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
 // ------------------------------------------------------------ the tile ---
@@ -132,16 +134,13 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* __restrict__ x, int64_t r
                                              const float (&v)[8]) {
   if (r >= rows || c >= cols) return;
   uint16_t* p = x + r * ld + c;
-  uint32_t h[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) h[i] = to_bf16(v[i]);
   if (c + 8 <= cols) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16),
-                                              h[4] | (h[5] << 16), h[6] | (h[7] << 16));
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                              pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
-      if (c + i < cols) p[i] = static_cast<uint16_t>(h[i]);
+      if (c + i < cols) p[i] = to_bf16(v[i]);
   }
 }
 

@@ -19,6 +19,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "fp4_internal.hpp"
 #include "fp8_common.hpp"
 #include "gemm_common.hpp"
@@ -48,9 +50,8 @@ __device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3)
 
 // Tile order: a contiguous range of tiles per XCD (consecutive workgroups go
 // round-robin over the 8), walked in groups of 8 tile rows.
-__device__ __forceinline__ void tile_coords(const Params& p, int& tm, int& tn) {
+__device__ __forceinline__ void tile_coords(const Params& p, int id, int& tm, int& tn) {
   const int T = p.tiles_m * p.tiles_n;
-  int id = blockIdx.x;
   if ((T & 7) == 0) id = (id & 7) * (T >> 3) + (id >> 3);
   constexpr int G = 8;
   const int per_group = G * p.tiles_n;
@@ -175,8 +176,7 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
             v.z += __uint_as_float(o.y << 16);
             v.w += __uint_as_float(o.y & 0xFFFF0000u);
           }
-          *d = make_uint2(fp8dev::to_bf16(v.x) | (fp8dev::to_bf16(v.y) << 16),
-                          fp8dev::to_bf16(v.z) | (fp8dev::to_bf16(v.w) << 16));
+          *d = make_uint2(fp8dev::pack_bf16(v.x, v.y), fp8dev::pack_bf16(v.z, v.w));
         } else {
           float4* d = reinterpret_cast<float4*>(static_cast<float*>(g.D) + row * g.ldd + col0 + c);
           if (g.accumulate) {
@@ -195,7 +195,7 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
         if (g.d_bf16) {
           uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col0 + c;
           if (g.accumulate) v += __uint_as_float(static_cast<uint32_t>(*d) << 16);
-          *d = static_cast<uint16_t>(fp8dev::to_bf16(v));
+          *d = fp8dev::to_bf16((v));
         } else {
           float* d = static_cast<float*>(g.D) + row * g.ldd + col0 + c;
           *d = g.accumulate ? *d + v : v;
@@ -214,7 +214,7 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
   int kb0, nkb;
   const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
   int tm, tn;
-  tile_coords(p, tm, tn);
+  tile_coords(p, blockIdx.x, tm, tn);
   const int64_t m0 = static_cast<int64_t>(tm) * (64 * MI), n0 = static_cast<int64_t>(tn) * (64 * NI);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -367,13 +367,15 @@ struct WidePos {
   const uint8_t *psa, *psb;      // scales of this lane's 4 rows at the first block
 };
 
-__device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8GemmArgs& g, int kb0) {
+__device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8GemmArgs& g, int id, int kb0) {
   WidePos w;
   int tm, tn;
-  tile_coords(p, tm, tn);
+  tile_coords(p, id, tm, tn);
   w.m0 = static_cast<int64_t>(tm) * 256;
   w.n0 = static_cast<int64_t>(tn) * 256;
   w.lane = threadIdx.x & 63;
+  // per tile, not once: addresses kept over the tile loop would be spilled
+  asm volatile("" : "+v"(w.lane));
   w.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   w.wm = w.wave >> 1;
   w.wn = w.wave & 1;
@@ -396,7 +398,9 @@ __device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8Ge
 }
 
 // Half of a step: 16 MFMAs on `cur`, the reads of half KS of stage R into
-// `nxt` beside the first 8 and, if DMA, block kb into stage W beside all.
+// `nxt` beside the first 8 and, if DMA, block kb into stage W, one DMA beside
+// each: evenly, for a burst holds the wave's next MFMA back (8192 x 4096 x 21504:
+// 534 us; two beside each of the first 8: 572, four beside 4: 594).
 template <int FA, int KS, bool DMA, int X = 0>
 __device__ __forceinline__ void wide_half(floatx16 (&acc)[4][4], const Frags& cur, uint32_t sa,
                                           uint32_t sb, const Stage<4, 4>& R, Frags& nxt,
@@ -404,64 +408,124 @@ __device__ __forceinline__ void wide_half(floatx16 (&acc)[4][4], const Frags& cu
   if constexpr (X < 16) {
     mfma_one<FA, 4, 4, X / 4, X % 4>(acc, cur.a, cur.b, sa, sb);
     if constexpr (X < 8) read_frag<KS, X>(R, nxt, w.wm, w.wn, w.i, w.h);
-    if constexpr (DMA && X < 8) {
-      wide_dma(W, w.src, koff, w.wave, 2 * X);
-      wide_dma(W, w.src, koff, w.wave, 2 * X + 1);
-    }
+    if constexpr (DMA) wide_dma(W, w.src, koff, w.wave, X);
     __builtin_amdgcn_sched_barrier(0);
     wide_half<FA, KS, DMA, X + 1>(acc, cur, sa, sb, R, nxt, W, koff, w);
   }
 }
 
+// A wave's 128 x 128 part of a bf16 D through 32 x 64 buffers of its own: a
+// lane's values of 8 accumulators are 4 consecutive columns each (8 bytes), and
+// 8 lanes write a row's 128 bytes.  row0, col: this lane's first row and column.
+constexpr int kWidePitch = 72;              // bf16 of a buffer row: 64 and 16 bytes of padding
+__device__ __forceinline__ void wide_store_bf16(const fp4lib::Fp8GemmArgs& g, floatx16 (&acc)[4][4],
+                                                const WidePos& w, int64_t row0, int64_t col,
+                                                uint16_t* buf) {
+  uint16_t* d = static_cast<uint16_t*>(g.D) + row0 * g.ldd + col;
+#pragma unroll
+  for (int mi = 0; mi < 4; ++mi) {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int k = 8 * half + e;
+        *reinterpret_cast<uint2*>(buf + w.i * kWidePitch + (8 * (e >> 2) + 4 * w.h + (e & 3)) * 4) =
+            make_uint2(fp8dev::pack_bf16(acc[mi][0][k], acc[mi][1][k]),
+                       fp8dev::pack_bf16(acc[mi][2][k], acc[mi][3][k]));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + (8 * r + (w.lane >> 3)) * kWidePitch + 8 * (w.lane & 7));
+        if (row0 + 32 * r + mi < g.M && col + 64 * half < g.N)
+          *reinterpret_cast<uint4*>(d + (32 * r + mi) * g.ldd + 64 * half) = v;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    }
+  }
+}
+
+// The scales of the wave's rows of A and B: of the block that is multiplied,
+// and of the one after it.
+struct WideScales {
+  uint32_t a, b, na, nb;
+};
+
+__device__ __forceinline__ WideScales wide_scales(const fp4lib::Fp8GemmArgs& g, const WidePos& w, int nkb) {
+  const int k1 = min(1, nkb - 1);
+  return WideScales{load_scales<4>(w.psa), load_scales<4>(w.psb), load_scales<4>(w.psa + k1 * g.s_kblk[0]),
+                    load_scales<4>(w.psb + k1 * g.s_kblk[1])};
+}
+
+// Blocks 0 and 1 of a tile on their way into the stages.
+__device__ __forceinline__ void wide_begin(Stage<4, 4>& s0, Stage<4, 4>& s1, const WidePos& w, int nkb) {
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int x = 0; x < 16; ++x) wide_dma(s0, w.src, 0, w.wave, x);
+#pragma unroll
+  for (int x = 0; x < 16; ++x) wide_dma(s1, w.src, nkb > 1 ? kStepBytes : 0, w.wave, x);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Step kb on stage C, whose first half's operands (f0) and scales are in
+// registers; block kb + 1 is in (or on its way to) Nx; C takes block kb + 2
+// (past the end the last one again).  Steps go in pairs: with an odd number
+// of blocks the last one is multiplied again under scales 2^-127 2^-127, whose
+// products are zero in fp32 (a loop exit between the two steps makes the
+// compiler move the 256 accumulators, and spill).  The scales of block kb + 2
+// are loaded before its DMA, a whole step before their use, so that no wait
+// for them is a wait for the DMA.
+template <int FA>
+__device__ __forceinline__ void wide_step(floatx16 (&acc)[4][4], Frags& f0, Frags& f1, WideScales& s,
+                                          Stage<4, 4>& C, Stage<4, 4>& Nx, int kb, int nkb,
+                                          const fp4lib::Fp8GemmArgs& g, const WidePos& w) {
+  const int k2 = min(kb + 2, nkb - 1);
+  wide_half<FA, 1, false>(acc, f0, s.a, s.b, C, f1, C, 0, w);
+  wait_vmcnt<0>();
+  ring_barrier();
+  const uint32_t pa = load_scales<4>(w.psa + k2 * g.s_kblk[0]);
+  const uint32_t pb = load_scales<4>(w.psb + k2 * g.s_kblk[1]);
+  wide_half<FA, 0, true>(acc, f1, s.a, s.b, Nx, f0, C, static_cast<int64_t>(k2) * kStepBytes, w);
+  s.a = kb + 1 < nkb ? s.na : 0;
+  s.b = kb + 1 < nkb ? s.nb : 0;
+  s.na = pa;
+  s.nb = pb;
+}
+
+__device__ __forceinline__ void wide_first_frags(const Stage<4, 4>& s0, Frags& f0, const WidePos& w) {
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    f0.a[t] = frag<0>(s0.a, w.wm * 128 + t * 32 + w.i, w.h);
+    f0.b[t] = frag<0>(s0.b, w.wn * 128 + t * 32 + w.i, w.h);
+  }
+}
+
+__device__ __forceinline__ void wide_zero(floatx16 (&acc)[4][4]) {
+#pragma unroll
+  for (int mi = 0; mi < 4; ++mi)
+#pragma unroll
+    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = floatx16{};
+}
+
+// Any D: one tile per workgroup.
 template <int FA>
 __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide(Params p) {
   __shared__ Stage<4, 4> s0, s1;
   int kb0, nkb;
   const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
-  const WidePos w = wide_pos(p, g, kb0);
-
+  const WidePos w = wide_pos(p, g, blockIdx.x, kb0);
   floatx16 acc[4][4];
-#pragma unroll
-  for (int mi = 0; mi < 4; ++mi)
-#pragma unroll
-    for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = floatx16{};
-
-  Frags f0, f1;
-  uint32_t sa, sb;
-  // Step kb on stage C, whose first half's operands and scales are in
-  // registers; block kb + 1 is in (or on its way to) Nx; C takes block kb + 2
-  // (past the end the last one again).  Steps go in pairs: with an odd number
-  // of blocks the last one is multiplied again under scales 2^-127 2^-127,
-  // whose products are zero in fp32 (a loop exit between the two steps makes
-  // the compiler move the 256 accumulators, and spill).
-  auto step = [&](Stage<4, 4>& C, Stage<4, 4>& Nx, int kb) {
-    const int k1 = min(kb + 1, nkb - 1), k2 = min(kb + 2, nkb - 1);
-    const uint32_t na = load_scales<4>(w.psa + k1 * g.s_kblk[0]);
-    const uint32_t nb = load_scales<4>(w.psb + k1 * g.s_kblk[1]);
-    wide_half<FA, 1, false>(acc, f0, sa, sb, C, f1, C, 0, w);
-    wait_vmcnt<0>();
-    ring_barrier();
-    wide_half<FA, 0, true>(acc, f1, sa, sb, Nx, f0, C, static_cast<int64_t>(k2) * kStepBytes, w);
-    sa = kb + 1 < nkb ? na : 0;
-    sb = kb + 1 < nkb ? nb : 0;
-  };
+  wide_zero(acc);
   if (nkb > 0) {
-#pragma unroll
-    for (int x = 0; x < 16; ++x) wide_dma(s0, w.src, 0, w.wave, x);
-    sa = load_scales<4>(w.psa);
-    sb = load_scales<4>(w.psb);
-    wait_vmcnt<0>();
+    WideScales sc = wide_scales(g, w, nkb);
+    Frags f0, f1;
+    wide_begin(s0, s1, w, nkb);
+    wait_vmcnt<16>();
     ring_barrier();
-#pragma unroll
-    for (int x = 0; x < 16; ++x) wide_dma(s1, w.src, nkb > 1 ? kStepBytes : 0, w.wave, x);
-#pragma unroll
-    for (int mi = 0; mi < 4; ++mi) {
-      f0.a[mi] = frag<0>(s0.a, w.wm * 128 + mi * 32 + w.i, w.h);
-      f0.b[mi] = frag<0>(s0.b, w.wn * 128 + mi * 32 + w.i, w.h);
-    }
+    wide_first_frags(s0, f0, w);
     for (int kb = 0; kb < nkb; kb += 2) {
-      step(s0, s1, kb);
-      step(s1, s0, kb + 1);
+      wide_step<FA>(acc, f0, f1, sc, s0, s1, kb, nkb, g, w);
+      wide_step<FA>(acc, f0, f1, sc, s1, s0, kb + 1, nkb, g, w);
     }
   }
   wait_vmcnt<0>();
@@ -469,6 +533,44 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide(Params p) {
   constexpr int kBuf = 32 * (32 * 4 + 4);
   float* buf = reinterpret_cast<float*>(w.wave < 2 ? &s0 : &s1) + (w.wave & 1) * kBuf;
   epilogue<4, 4>(g, acc, w.m0 + w.wm * 128, w.n0 + w.wn * 128, w.lane, buf);
+}
+
+// A bf16 D with 16-byte rows (and N a multiple of 8), not accumulated: a
+// workgroup per CU takes tile after tile, the first two blocks of the next
+// one on their way while a tile is stored.
+template <int FA>
+__global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_loop(Params p) {
+  __shared__ Stage<4, 4> s0, s1;
+  __shared__ __attribute__((aligned(16))) uint16_t ebuf[4][32 * kWidePitch];
+  const fp4lib::Fp8GemmArgs& g = p.g;
+  const int nkb = static_cast<int>(g.nkb), tiles = p.tiles_m * p.tiles_n;
+  int id = blockIdx.x;
+  WidePos w = wide_pos(p, g, id, 0);
+  WideScales sc = wide_scales(g, w, nkb);
+  wide_begin(s0, s1, w, nkb);
+  for (;;) {
+    floatx16 acc[4][4];
+    wide_zero(acc);
+    Frags f0, f1;
+    wait_vmcnt<0>();
+    ring_barrier();
+    wide_first_frags(s0, f0, w);
+    for (int kb = 0; kb < nkb; kb += 2) {
+      wide_step<FA>(acc, f0, f1, sc, s0, s1, kb, nkb, g, w);
+      wide_step<FA>(acc, f0, f1, sc, s1, s0, kb + 1, nkb, g, w);
+    }
+    id += gridDim.x;
+    const int64_t row0 = w.m0 + w.wm * 128 + (w.lane >> 3) * 4, col = w.n0 + w.wn * 128 + 8 * (w.lane & 7);
+    if (id < tiles) {
+      w = wide_pos(p, g, id, 0);
+      sc = wide_scales(g, w, nkb);
+    }
+    wait_vmcnt<0>();
+    ring_barrier();           // both stages are done with
+    if (id < tiles) wide_begin(s0, s1, w, nkb);
+    wide_store_bf16(g, acc, w, row0, col, ebuf[w.wave]);
+    if (id >= tiles) break;
+  }
 }
 
 // ------------------------------------------------------ 256 x 256, bf16 ---
@@ -546,7 +648,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_f32(Params p) {
   __shared__ Stage<4, 4> s0, s1;
   int kb0, nkb;
   const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
-  const WidePos w = wide_pos(p, g, kb0);
+  const WidePos w = wide_pos(p, g, blockIdx.x, kb0);
 
   floatx16 acc[4][4];
 #pragma unroll
@@ -614,6 +716,10 @@ void launch_tile(const fp4lib::Fp8GemmArgs& g, hipStream_t s) {
   const dim3 grid(p.tiles_m * p.tiles_n, g.splits);
   if constexpr (MI == 4) {
     if constexpr (PREC) hipLaunchKernelGGL(k_gemm_fp8_wide_f32<FA>, grid, dim3(kThreads), 0, s, p);
+    else if (g.d_bf16 && !g.accumulate && g.N % 8 == 0 && g.ldd % 8 == 0 && g.splits == 1 &&
+             reinterpret_cast<uintptr_t>(g.D) % 16 == 0)
+      hipLaunchKernelGGL(k_gemm_fp8_wide_loop<FA>, dim3(std::min<int>(grid.x, fp4lib::device_cu_count())),
+                         dim3(kThreads), 0, s, p);
     else hipLaunchKernelGGL(k_gemm_fp8_wide<FA>, grid, dim3(kThreads), 0, s, p);
   } else {
     hipLaunchKernelGGL((k_gemm_fp8<FA, PREC, MI, NI>), grid, dim3(kThreads), 0, s, p);
@@ -638,7 +744,7 @@ __global__ __launch_bounds__(256) void k_gemm_fp8_join(fp4lib::Fp8GemmArgs g) {
       if (g.d_bf16) {
         uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col + e;
         const float o = g.accumulate ? __uint_as_float(static_cast<uint32_t>(*d) << 16) : 0.0f;
-        *d = static_cast<uint16_t>(fp8dev::to_bf16(g.accumulate ? r[e] + o : r[e]));
+        *d = fp8dev::to_bf16((g.accumulate ? r[e] + o : r[e]));
       } else {
         float* d = static_cast<float*>(g.D) + row * g.ldd + col + e;
         *d = g.accumulate ? *d + r[e] : r[e];
@@ -660,7 +766,7 @@ Plan plan_of(const fp4lib::Fp8GemmArgs& g) {
   if (g.M <= kMaxRows) {
     p.kind = 0;
     p.splits = rows_splits(g);
-  } else if (wide >= cus / 2 && g.ld[0] < (1 << 23) && g.ld[1] < (1 << 23)) {
+  } else if (g.nkb > 0 && wide >= cus / 2 && g.ld[0] < (1 << 23) && g.ld[1] < (1 << 23)) {
     p.kind = 4;
   } else {
     const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);

@@ -6,10 +6,11 @@
 #include <stdint.h>
 
 #include "fp4_internal.hpp"
+#include "fp8_common.hpp"
 
 namespace fp8gemm {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+using fp8dev::bf16x2;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // 8 codes (two words) with their block's scale as bf16, exact.

@@ -116,7 +116,7 @@ __global__ __launch_bounds__(64 * (MT == 1 ? 16 : 8)) void k_gemm_fp8_rows(fp4li
     if (g.d_bf16) {
       uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col;
       if (g.accumulate) v += __uint_as_float(static_cast<uint32_t>(*d) << 16);
-      *d = static_cast<uint16_t>(fp8dev::to_bf16(v));
+      *d = fp8dev::to_bf16(v);
     } else {
       float* d = static_cast<float*>(g.D) + row * g.ldd + col;
       *d = g.accumulate ? *d + v : v;
