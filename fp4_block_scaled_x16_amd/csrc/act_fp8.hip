@@ -29,7 +29,7 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 
 template <bool GLU>
-__global__ __launch_bounds__(kTileThreads) void k_act_fp8(fp4lib::Fp8ActArgs a) {
+__global__ __launch_bounds__(kTileThreads, 4) void k_act_fp8(fp4lib::Fp8ActArgs a) {
   const int64_t tiles_c = (a.cols + kTile - 1) / kTile;
   const int64_t n = (a.rows + kTile - 1) / kTile * tiles_c;
   const int64_t fp = up128(a.cols);
@@ -85,51 +85,60 @@ __global__ __launch_bounds__(kTileThreads) void k_act_fp8(fp4lib::Fp8ActArgs a) 
   }
 }
 
-// The values of the tile's codes from code column `col` (block kb) on.
-__device__ __forceinline__ void load_codes(const TilePos& t, const uint8_t* __restrict__ codes,
-                                           const uint8_t* __restrict__ scales, int64_t rows,
-                                           int64_t hp, int64_t col, int64_t kb, float (&v)[4][8]) {
-  const int64_t rp = up16(rows);
-  uint2 q[4] = {};
-  uint32_t se = 0;
+// What a tile of the backward pass reads.
+template <bool GLU>
+struct GradInput {
+  RawCodes h[GLU ? 2 : 1];
+  uint4 da[4];
+};
+template <bool GLU>
+__device__ __forceinline__ GradInput<GLU> load_grad(const fp4lib::Fp8ActGradArgs& a, const TilePos& t) {
+  const int64_t fp = up128(a.cols), hp = (GLU ? 2 : 1) * fp, kb = t.c0 / kTile;
+  GradInput<GLU> in;
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-    if (t.row(p) < rows) q[p] = *reinterpret_cast<const uint2*>(codes + t.row(p) * hp + col);
-  if (t.row(0) < rp) se = *reinterpret_cast<const uint32_t*>(scales + kb * rp + t.row(0));
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const float s = t.row(p) < rows ? fp4dev::ue8m0_decode((se >> (8 * p)) & 0xFFu) : 0.0f;
-    unpack4<false>(q[p].x, v[p]);
-    unpack4<false>(q[p].y, v[p] + 4);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[p][i] *= s;
-  }
+  for (int p = 0; p < 4; ++p) in.da[p] = load_bf16x8(a.da, t.row(p), a.rows, t.col(), a.cols, a.ld);
+  in.h[0] = load_raw(t, a.h_codes, a.h_scales, a.rows, hp, t.col(), kb);
+  if constexpr (GLU) in.h[1] = load_raw(t, a.h_codes, a.h_scales, a.rows, hp, fp + t.col(), fp / kTile + kb);
+  return in;
 }
 
-template <bool GLU, bool E5>
-__global__ __launch_bounds__(kTileThreads) void k_act_grad_fp8(fp4lib::Fp8ActGradArgs a) {
+// VALUES: bf16 dh and a; else codes.
+//
+// SwiGLU to codes holds three fp32 tiles, 96 registers a thread and as many
+// again around them: one workgroup fits on a CU, so it loops over tiles and
+// loads the next one's input before it computes (8192 x 6144: 102 us, 4.5 TB/s;
+// two workgroups of 128 registers spill: 217 us).  The others fit twice, and
+// overlap each other better than a loop does (squared ReLU, 8192 x 21504: 219
+// us, 4.8 TB/s; 241 with the loop).
+template <bool GLU, bool VALUES>
+constexpr bool kGradLoop = GLU && !VALUES;
+
+template <bool GLU, bool E5, bool VALUES>
+__global__ __launch_bounds__(kTileThreads, (kGradLoop<GLU, VALUES> ? 2 : 4)) void k_act_grad_fp8(fp4lib::Fp8ActGradArgs a) {
   constexpr int H = GLU ? 2 : 1;          // halves of h
-  __shared__ __attribute__((aligned(16))) float cmax[H + 1][kTileThreads / 64][kTile];
-  __shared__ __attribute__((aligned(16))) uint32_t tile[H + 1][kTileWords];
+  __shared__ ColMax cmax[VALUES ? 1 : H + 1];
+  __shared__ __attribute__((aligned(16))) uint8_t code[H + 1][kTile];
+  __shared__ __attribute__((aligned(16))) uint32_t tile[VALUES ? 1 : H + 1][VALUES ? 4 : kTileWords];
   const int64_t tiles_c = (a.cols + kTile - 1) / kTile;
   const int64_t n = (a.rows + kTile - 1) / kTile * tiles_c;
   const int64_t fp = up128(a.cols), hp = H * fp, rp = up128(a.rows);
   uint32_t unused = 0;
+  constexpr bool LOOP = kGradLoop<GLU, VALUES>;
+  GradInput<GLU> next;
+  if (LOOP && blockIdx.x < n) next = load_grad<GLU>(a, tile_pos(blockIdx.x, tiles_c));
   for (int64_t id = blockIdx.x; id < n; id += gridDim.x) {
     const TilePos t = tile_pos(id, tiles_c);
     const int64_t kb = t.c0 / kTile, cols_in = a.cols - t.c0;
     float d[H][4][8], v[4][8];            // dh, a
     {
-      uint4 q[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) q[p] = load_bf16x8(a.da, t.row(p), a.rows, t.col(), a.cols, a.ld);
-      load_codes(t, a.h_codes, a.h_scales, a.rows, hp, t.col(), kb, d[0]);
-      if constexpr (GLU)
-        load_codes(t, a.h_codes, a.h_scales, a.rows, hp, fp + t.col(), fp / kTile + kb, d[1]);
+      const GradInput<GLU> in = LOOP ? next : load_grad<GLU>(a, t);
+      if (LOOP && id + gridDim.x < n) next = load_grad<GLU>(a, tile_pos(id + gridDim.x, tiles_c));
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
         float da[8];
-        unpack8(q[p], da);
+        unpack8(in.da[p], da);
+#pragma unroll
+        for (int h = 0; h < H; ++h) raw_values<false>(in.h[h], p, t.row(p) < a.rows, d[h][p]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float g = d[0][p][i];
@@ -146,52 +155,45 @@ __global__ __launch_bounds__(kTileThreads) void k_act_grad_fp8(fp4lib::Fp8ActGra
         }
       }
     }
+    if constexpr (VALUES) {
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      if (a.dh_codes) {
-        uint32_t sc[4];
-        row_scales<E5>(d[h], sc);
-        store_rows<E5, false>(t, d[h], sc, a.rows, hp, h * fp + t.col(), h * (fp / kTile) + kb,
-                              a.dh_codes, a.dh_scales, unused);
+      for (int p = 0; p < 4; ++p) {
+        if (a.a) store_bf16x8(a.a, t.row(p), a.rows, t.col(), a.cols, a.ld_a, v[p]);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          if (a.dh) store_bf16x8(a.dh + h * a.cols, t.row(p), a.rows, t.col(), a.cols, a.ld_dh, d[h][p]);
       }
-      if (a.dh) {
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-          store_bf16x8(a.dh + h * a.cols, t.row(p), a.rows, t.col(), a.cols, a.ld_dh, d[h][p]);
-      }
-    }
-    if (a.a) {
-#pragma unroll
-      for (int p = 0; p < 4; ++p) store_bf16x8(a.a, t.row(p), a.rows, t.col(), a.cols, a.ld_a, v[p]);
-    }
-    if (a.dh_t_codes || a.a_t_codes) {
+    } else {
 #pragma unroll
       for (int h = 0; h < H; ++h) col_partial(t, d[h], cmax[h]);
       col_partial(t, v, cmax[H]);
       __syncthreads();
-      if (a.dh_t_codes) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
-          float m[8];
-          uint32_t sc[8];
-          col_max(t, cmax[h], m);
+      for (int h = 0; h < H; ++h) col_codes<E5>(cmax[h], code[h], h * kTile);
+      col_codes<false>(cmax[H], code[H], H * kTile);
+      __syncthreads();
 #pragma unroll
-          for (int c = 0; c < 8; ++c) sc[c] = scale_code<E5>(m[c]);
+      for (int h = 0; h < H; ++h) {
+        if (a.dh_codes) {
+          uint32_t sc[4];
+          row_scales<E5>(d[h], sc);
+          store_rows<E5, false>(t, d[h], sc, a.rows, hp, h * fp + t.col(), h * (fp / kTile) + kb,
+                                a.dh_codes, a.dh_scales, unused);
+        }
+        if (a.dh_t_codes) {
+          const uint2 sc = *reinterpret_cast<const uint2*>(code[h] + 8 * t.l);
           // row h * cols + column of the transpose (SwiGLU: cols is a multiple
           // of 8 and 2 cols one of 16, so there is no padding)
           if (t.tr == 0 && t.col() < (GLU ? a.cols : up16(a.cols)))
-            store_scales8(sc, a.dh_t_scales + t.r0 / kTile * up16(H * a.cols) + h * a.cols + t.col());
+            *reinterpret_cast<uint2*>(a.dh_t_scales + t.r0 / kTile * up16(H * a.cols) + h * a.cols +
+                                      t.col()) = sc;
           encode_cols<E5, false>(t, d[h], sc, tile[h], unused);
         }
       }
       if (a.a_t_codes) {
-        float m[8];
-        uint32_t sc[8];
-        col_max(t, cmax[H], m);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sc[c] = scale_code<false>(m[c]);
+        const uint2 sc = *reinterpret_cast<const uint2*>(code[H] + 8 * t.l);
         if (t.tr == 0 && t.col() < up16(a.cols))
-          store_scales8(sc, a.a_t_scales + t.r0 / kTile * up16(a.cols) + t.col());
+          *reinterpret_cast<uint2*>(a.a_t_scales + t.r0 / kTile * up16(a.cols) + t.col()) = sc;
         encode_cols<false, false>(t, v, sc, tile[H], unused);
       }
       __syncthreads();
@@ -203,6 +205,18 @@ __global__ __launch_bounds__(kTileThreads) void k_act_grad_fp8(fp4lib::Fp8ActGra
       if (a.a_t_codes) store_cols(t, tile[H], cols_in, t.c0, rp, a.a_t_codes);
     }
   }
+}
+
+template <bool GLU>
+void launch_grad(const fp4lib::Fp8ActGradArgs& a, hipStream_t s) {
+  const int64_t tiles = (a.rows + kTile - 1) / kTile * ((a.cols + kTile - 1) / kTile);
+  const dim3 block(kTileThreads);
+  if (a.dh || a.a)
+    hipLaunchKernelGGL((k_act_grad_fp8<GLU, false, true>), dim3(tile_grid(tiles, kWgPerCu)), block, 0, s, a);
+  if (!a.dh_codes && !a.dh_t_codes && !a.a_t_codes) return;
+  const dim3 grid(tile_grid(tiles, kGradLoop<GLU, false> ? 1 : kWgPerCu));
+  if (a.e5m2) hipLaunchKernelGGL((k_act_grad_fp8<GLU, true, false>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((k_act_grad_fp8<GLU, false, false>), grid, block, 0, s, a);
 }
 
 }  // namespace
@@ -218,13 +232,8 @@ hipError_t launch_act_quant_fp8(const Fp8ActArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_act_grad_fp8(const Fp8ActGradArgs& a, hipStream_t s) {
-  const int64_t tiles = (a.rows + kTile - 1) / kTile * ((a.cols + kTile - 1) / kTile);
-  const dim3 grid(tile_grid(tiles, kWgPerCu)), block(kTileThreads);
-  const bool glu = a.act == FP4_ACT_SWIGLU;
-  if (glu && a.e5m2) hipLaunchKernelGGL((k_act_grad_fp8<true, true>), grid, block, 0, s, a);
-  else if (glu) hipLaunchKernelGGL((k_act_grad_fp8<true, false>), grid, block, 0, s, a);
-  else if (a.e5m2) hipLaunchKernelGGL((k_act_grad_fp8<false, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((k_act_grad_fp8<false, false>), grid, block, 0, s, a);
+  if (a.act == FP4_ACT_SWIGLU) launch_grad<true>(a, s);
+  else launch_grad<false>(a, s);
   return hipGetLastError();
 }
 

@@ -21,49 +21,53 @@ using fp4dev::bf16_to_f32;
 __host__ __device__ __forceinline__ int64_t up16(int64_t v) { return (v + 15) & ~int64_t(15); }
 __host__ __device__ __forceinline__ int64_t up128(int64_t v) { return (v + 127) & ~int64_t(127); }
 
+// Block amaxes are carried as bits: those of a nonnegative float that is no
+// NaN, which order as integers do (an integer maximum needs no
+// canonicalization, and takes its DPP operand directly).
+//
 // amax = m * 2^k, 1 <= m < 2: e = k - 8 (E5M2: k - 15) if m <= 1.75, one
 // more otherwise.  Adding 2^21 - 1 to the bits carries into the exponent
 // field exactly when the mantissa exceeds 0x600000 (m > 1.75).  Subnormal
 // amaxes and zero land below 0 and are clamped, which is e = -127; an
 // infinite amax gives the code of the largest finite one.
 template <bool E5>
-__device__ __forceinline__ uint32_t scale_code(float amax) {
-  const int e = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - (E5 ? 15 : 8);
+__device__ __forceinline__ uint32_t scale_code(uint32_t amax) {
+  const int e = static_cast<int>((amax + 0x1FFFFFu) >> 23) - (E5 ? 15 : 8);
   return static_cast<uint32_t>(e > 0 ? e : 0);
 }
 
-// 2^-e of a scale code that scale_code can give (at most 247): normal.
-__device__ __forceinline__ float enc_scale(uint32_t code) {
-  return __uint_as_float((254u - code) << 23);
-}
+// The scale 2^e of a code as the converts below take it: in the exponent
+// field (0 being 2^-127).
+__device__ __forceinline__ float code_scale(uint32_t code) { return __uint_as_float(code << 23); }
 
-// Four element codes in one word, byte k from y_k, |y_k| within the format
-// (block scales are rounded up): gfx950's packed converts at unit scale.
+// Four element codes in one word, byte k from y_k * 2^-e, which lies within the
+// format (block scales are rounded up): gfx950's packed converts divide by
+// their scale exactly.
 template <bool E5>
-__device__ __forceinline__ uint32_t pack4(float y0, float y1, float y2, float y3) {
+__device__ __forceinline__ uint32_t pack4(float y0, float y1, float y2, float y3, float scale) {
+  fp4dev::s16x2 w = {0, 0};
   if constexpr (E5) {
-    const fp4dev::s16x2 z = {0, 0};
-    const fp4dev::s16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(z, y0, y1, 1.0f, false);
-    const fp4dev::s16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(z, y2, y3, 1.0f, false);
-    return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo),
-                                 0x05040100u);
+    w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, y0, y1, scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, y2, y3, scale, true);
   } else {
-    return fp4dev::e4m3_pack4(y0, y1, y2, y3);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, y0, y1, scale, false);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, y2, y3, scale, true);
   }
+  return __builtin_bit_cast(uint32_t, w);
 }
 
 typedef float float2v __attribute__((ext_vector_type(2)));
 
-// The values of a word's four codes, unscaled (exact).
+// The values of a word's four codes times the scale (exact).
 template <bool E5>
-__device__ __forceinline__ void unpack4(uint32_t w, float* v) {
+__device__ __forceinline__ void unpack4(uint32_t w, float* v, float scale) {
   float2v lo, hi;
   if constexpr (E5) {
-    lo = __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
-    hi = __builtin_amdgcn_cvt_pk_f32_bf8(w, true);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, true);
   } else {
-    lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-    hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, false);
+    hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, true);
   }
   v[0] = lo.x;
   v[1] = lo.y;
@@ -107,21 +111,20 @@ __device__ __forceinline__ TilePos tile_pos(int64_t id, int64_t tiles_c) {
 }
 
 // 8 bf16 of row r from column c on; zeros outside [rows, cols].  The row
-// pitch is a multiple of 8 and the base 16-byte aligned; a partial group is
-// read element by element, so nothing behind column `cols` is touched.
+// pitch is a multiple of 8 and the base 16-byte aligned, so a group with one
+// valid element is an aligned 16 bytes of one allocation: it is read whole and
+// what lies behind column `cols` is masked.
 __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* __restrict__ x, int64_t r, int64_t rows,
                                              int64_t c, int64_t cols, int64_t ld) {
   uint4 q = make_uint4(0u, 0u, 0u, 0u);
   if (r < rows && c < cols) {
-    const uint16_t* p = x + r * ld + c;
-    if (c + 8 <= cols) {
-      q = *reinterpret_cast<const uint4*>(p);
-    } else {
-      uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (c + i < cols) w[i >> 1] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-      q = make_uint4(w[0], w[1], w[2], w[3]);
+    q = *reinterpret_cast<const uint4*>(x + r * ld + c);
+    if (c + 8 > cols) {
+      const int n = static_cast<int>(cols - c);          // 1 .. 7
+      auto keep = [n](uint32_t w, int k) {
+        return n >= 2 * k + 2 ? w : n == 2 * k + 1 ? w & 0xFFFFu : 0u;
+      };
+      q = make_uint4(keep(q.x, 0), keep(q.y, 1), keep(q.z, 2), keep(q.w, 3));
     }
   }
   return q;
@@ -147,22 +150,62 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* __restrict__ x, int64_t r
 // Largest over the 16 lanes of a row's block, in every one of them: the
 // rotations within a DPP row.
 template <int CTRL>
-__device__ __forceinline__ float dpp_max(float v) {
-  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true);
-  return fmaxf(v, __builtin_bit_cast(float, o));
+__device__ __forceinline__ uint32_t dpp_max(uint32_t v) {
+  const uint32_t o = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, true);
+  return v > o ? v : o;
 }
-__device__ __forceinline__ float max16(float v) {
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
   v = dpp_max<0x128>(v);   // row_ror:8
   v = dpp_max<0x124>(v);
   v = dpp_max<0x122>(v);
   return dpp_max<0x121>(v);
 }
 
-__device__ __forceinline__ float absmax8(const float (&v)[8]) {
-  float m = 0.0f;          // fmaxf passes a NaN over
+// |v| of 8 values: starting from 0, fmaxf passes a NaN over.
+__device__ __forceinline__ uint32_t absmax8(const float (&v)[8]) {
+  float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
-  return m;
+  return __float_as_uint(m);
+}
+
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Lanes' a and b in rows of 16: [max(a0, a1), max(b0, b1), max(a2, a3), max(b2, b3)].
+__device__ __forceinline__ uint32_t join_rows16(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  return umax(r[0], r[1]);
+}
+// In halves of 32: [max(a0, a1), max(b0, b1)].
+__device__ __forceinline__ uint32_t join_rows32(uint32_t a, uint32_t b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return umax(r[0], r[1]);
+}
+
+// The tile's codes from code column `col` (block kb) on, as they lie in memory:
+// 8 of each of the thread's rows, and the rows' scales.
+struct RawCodes {
+  uint2 q[4];
+  uint32_t scales;
+};
+__device__ __forceinline__ RawCodes load_raw(const TilePos& t, const uint8_t* __restrict__ codes,
+                                             const uint8_t* __restrict__ scales, int64_t rows,
+                                             int64_t pitch, int64_t col, int64_t kb) {
+  const int64_t rp = up16(rows);
+  RawCodes r = {};
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    if (t.row(p) < rows) r.q[p] = *reinterpret_cast<const uint2*>(codes + t.row(p) * pitch + col);
+  if (t.row(0) < rp) r.scales = *reinterpret_cast<const uint32_t*>(scales + kb * rp + t.row(0));
+  return r;
+}
+
+// Row p's values.  Rows outside have zero codes, and scales of any value.
+template <bool E5>
+__device__ __forceinline__ void raw_values(const RawCodes& r, int p, bool inside, float (&v)[8]) {
+  const float s = code_scale(inside ? (r.scales >> (8 * p)) & 0xFFu : 0u);
+  unpack4<E5>(r.q[p].x, v, s);
+  unpack4<E5>(r.q[p].y, v + 4, s);
 }
 
 // Nonzero values that a word of four codes holds as zero.
@@ -184,10 +227,10 @@ __device__ __forceinline__ void store_rows(const TilePos& t, const float (&v)[4]
                                            uint8_t* __restrict__ scales, uint32_t& lost) {
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const float s = enc_scale(sc[p]);
+    const float s = code_scale(sc[p]);
     uint2 w;
-    w.x = pack4<E5>(v[p][0] * s, v[p][1] * s, v[p][2] * s, v[p][3] * s);
-    w.y = pack4<E5>(v[p][4] * s, v[p][5] * s, v[p][6] * s, v[p][7] * s);
+    w.x = pack4<E5>(v[p][0], v[p][1], v[p][2], v[p][3], s);
+    w.y = pack4<E5>(v[p][4], v[p][5], v[p][6], v[p][7], s);
     if constexpr (CNT) {
       lost += lost4(w.x, [&](int i) { return v[p][i]; });
       lost += lost4(w.y, [&](int i) { return v[p][4 + i]; });
@@ -207,39 +250,31 @@ __device__ __forceinline__ void row_scales(const float (&v)[4][8], uint32_t (&sc
   for (int p = 0; p < 4; ++p) sc[p] = scale_code<E5>(max16(absmax8(v[p])));
 }
 
-// Column amaxes over the wave's 16 rows, one row of cmax[8][128] per wave;
-// the caller synchronizes, then col_max reads the whole column's.
-__device__ __forceinline__ void col_partial(const TilePos& t, const float (&v)[4][8],
-                                            float (*cmax)[kTile]) {
-  float m[8];
+// Column amaxes over the wave's 16 rows into one row of cmax[8][128] per wave:
+// the exchanges between its four row groups leave two columns' maxima in a
+// lane (8 l + q and 8 l + 4 + q, q = lane / 16).
+typedef uint32_t ColMax[kTileThreads / 64][kTile];
+__device__ __forceinline__ void col_partial(const TilePos& t, const float (&v)[4][8], ColMax& cmax) {
+  uint32_t m[8];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    m[c] = fmaxf(fmaxf(fabsf(v[0][c]), fabsf(v[1][c])), fmaxf(fabsf(v[2][c]), fabsf(v[3][c])));
-    m[c] = fmaxf(m[c], __shfl_xor(m[c], 16, 64));
-    m[c] = fmaxf(m[c], __shfl_xor(m[c], 32, 64));
-  }
-  if ((threadIdx.x & 48) == 0) {
-    float4* d = reinterpret_cast<float4*>(&cmax[threadIdx.x >> 6][8 * t.l]);
-    d[0] = make_float4(m[0], m[1], m[2], m[3]);
-    d[1] = make_float4(m[4], m[5], m[6], m[7]);
-  }
+  for (int c = 0; c < 8; ++c)
+    m[c] = __float_as_uint(fmaxf(fmaxf(fmaxf(fmaxf(0.0f, fabsf(v[0][c])), fabsf(v[1][c])),
+                                       fabsf(v[2][c])), fabsf(v[3][c])));
+  const int q = (threadIdx.x >> 4) & 3, w = threadIdx.x >> 6;
+  cmax[w][8 * t.l + q] = join_rows32(join_rows16(m[0], m[1]), join_rows16(m[2], m[3]));
+  cmax[w][8 * t.l + 4 + q] = join_rows32(join_rows16(m[4], m[5]), join_rows16(m[6], m[7]));
 }
 
-__device__ __forceinline__ void col_max(const TilePos& t, const float (*cmax)[kTile], float (&m)[8]) {
+// After a barrier: threads c0 .. c0 + 127 each make the scale code of one
+// column; after another, a thread takes those of its 8 columns.
+template <bool E5>
+__device__ __forceinline__ void col_codes(const ColMax& cmax, uint8_t (&code)[kTile], int c0) {
+  const int c = static_cast<int>(threadIdx.x) - c0;
+  if (c >= 0 && c < kTile) {
+    uint32_t m = cmax[0][c];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) m[c] = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kTileThreads / 64; ++w) {
-    const float4* s = reinterpret_cast<const float4*>(&cmax[w][8 * t.l]);
-    const float4 a = s[0], b = s[1];
-    m[0] = fmaxf(m[0], a.x);
-    m[1] = fmaxf(m[1], a.y);
-    m[2] = fmaxf(m[2], a.z);
-    m[3] = fmaxf(m[3], a.w);
-    m[4] = fmaxf(m[4], b.x);
-    m[5] = fmaxf(m[5], b.y);
-    m[6] = fmaxf(m[6], b.z);
-    m[7] = fmaxf(m[7], b.w);
+    for (int w = 1; w < kTileThreads / 64; ++w) m = umax(m, cmax[w][c]);
+    code[c] = static_cast<uint8_t>(scale_code<E5>(m));
   }
 }
 
@@ -252,24 +287,18 @@ __device__ __forceinline__ int tile_chunk(int c, int ch) {
   return (c ^ (c >> 6)) * 8 + (ch ^ ((c >> 3) & 7));
 }
 
-// Encode the thread's columns with their scale codes into the LDS tile.
+// Encode the thread's columns with their scale codes (byte c of sc: column c)
+// into the LDS tile.
 template <bool E5, bool CNT>
-__device__ __forceinline__ void encode_cols(const TilePos& t, const float (&v)[4][8],
-                                            const uint32_t (&sc)[8], uint32_t* tile,
-                                            uint32_t& lost) {
+__device__ __forceinline__ void encode_cols(const TilePos& t, const float (&v)[4][8], const uint2& sc,
+                                            uint32_t* tile, uint32_t& lost) {
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const float s = enc_scale(sc[c]);
-    const uint32_t w = pack4<E5>(v[0][c] * s, v[1][c] * s, v[2][c] * s, v[3][c] * s);
+    const float s = code_scale(((c < 4 ? sc.x : sc.y) >> (8 * (c & 3))) & 0xFFu);
+    const uint32_t w = pack4<E5>(v[0][c], v[1][c], v[2][c], v[3][c], s);
     if constexpr (CNT) lost += lost4(w, [&](int i) { return v[i][c]; });
     tile[tile_chunk(8 * t.l + c, t.tr >> 2) * 4 + (t.tr & 3)] = w;
   }
-}
-
-// The scale codes of 8 columns, consecutive in the transpose's KMAJOR scales.
-__device__ __forceinline__ void store_scales8(const uint32_t (&sc)[8], uint8_t* __restrict__ dst) {
-  *reinterpret_cast<uint2*>(dst) = make_uint2(sc[0] | (sc[1] << 8) | (sc[2] << 16) | (sc[3] << 24),
-                                              sc[4] | (sc[5] << 8) | (sc[6] << 16) | (sc[7] << 24));
 }
 
 // The LDS tile to rows col0 .. of the transpose's code matrix (pitch rp, a

@@ -18,9 +18,12 @@ namespace {
 
 constexpr int kWgPerCu = 4;
 
+// Two workgroups per CU (128 registers a thread), so that one's loads are
+// under way while the other waits at a barrier.
 template <bool E5, bool ROW, bool COL, bool TWO_D, bool CNT>
-__global__ __launch_bounds__(kTileThreads) void k_quant_fp8(fp4lib::Fp8QuantArgs a) {
-  __shared__ __attribute__((aligned(16))) float cmax[COL || TWO_D ? kTileThreads / 64 : 1][kTile];
+__global__ __launch_bounds__(kTileThreads, 4) void k_quant_fp8(fp4lib::Fp8QuantArgs a) {
+  __shared__ ColMax cmax;
+  __shared__ __attribute__((aligned(16))) uint8_t code[kTile];
   __shared__ __attribute__((aligned(16))) uint32_t tile[COL ? kTileWords : 4];
   const int64_t tiles_c = (a.cols + kTile - 1) / kTile;
   const int64_t n = (a.rows + kTile - 1) / kTile * tiles_c;
@@ -35,23 +38,28 @@ __global__ __launch_bounds__(kTileThreads) void k_quant_fp8(fp4lib::Fp8QuantArgs
 #pragma unroll
       for (int p = 0; p < 4; ++p) unpack8(q[p], v[p]);
     }
-    uint32_t sr[4], sc[8];
-    if constexpr (COL || TWO_D) {
+    uint32_t sr[4];
+    uint2 sc;
+    if constexpr (TWO_D) {
+      // one amax per tile: each wave's into LDS, the largest of the 8 in every thread
+      uint32_t m = max16(umax(umax(absmax8(v[0]), absmax8(v[1])), umax(absmax8(v[2]), absmax8(v[3]))));
+      m = join_rows16(m, m);
+      m = join_rows32(m, m);
+      uint32_t* part = cmax[0] + 8 * ((id / gridDim.x) & 1);   // two sets: the next tile's is another
+      part[threadIdx.x >> 6] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < kTileThreads / 64; ++w) m = umax(m, part[w]);
+      const uint32_t s = scale_code<E5>(m);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) sr[p] = s;
+      sc.x = sc.y = s * 0x01010101u;
+    } else if constexpr (COL) {
       col_partial(t, v, cmax);
       __syncthreads();
-      float m[8];
-      col_max(t, cmax, m);
-      if constexpr (TWO_D) {
-        const uint32_t s = scale_code<E5>(max16(absmax8(m)));
-#pragma unroll
-        for (int p = 0; p < 4; ++p) sr[p] = s;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sc[c] = s;
-        if constexpr (!COL) __syncthreads();      // cmax is read: the next tile may write it
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) sc[c] = scale_code<E5>(m[c]);
-      }
+      col_codes<E5>(cmax, code, 0);
+      __syncthreads();
+      sc = *reinterpret_cast<const uint2*>(code + 8 * t.l);
     }
     if constexpr (ROW) {
       if constexpr (!TWO_D) row_scales<E5>(v, sr);
@@ -60,7 +68,8 @@ __global__ __launch_bounds__(kTileThreads) void k_quant_fp8(fp4lib::Fp8QuantArgs
     }
     if constexpr (COL) {
       const int64_t sp = up16(a.cols);
-      if (t.tr == 0 && t.col() < sp) store_scales8(sc, a.scales_t + t.r0 / kTile * sp + t.col());
+      if (t.tr == 0 && t.col() < sp)
+        *reinterpret_cast<uint2*>(a.scales_t + t.r0 / kTile * sp + t.col()) = sc;
       encode_cols<E5, CNT>(t, v, sc, tile, lost);
       __syncthreads();
       // the next tile's first barrier separates these reads from its writes
@@ -76,42 +85,29 @@ __global__ __launch_bounds__(kTileThreads) void k_quant_fp8(fp4lib::Fp8QuantArgs
 // The columns of row codes: values code * 2^e (exact in fp32), encoded anew
 // in blocks along the rows.
 template <bool E5>
-__global__ __launch_bounds__(kTileThreads) void k_requant_t_fp8(
+__global__ __launch_bounds__(kTileThreads, 4) void k_requant_t_fp8(
     const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
     int64_t cols, uint8_t* __restrict__ codes_t, uint8_t* __restrict__ scales_t) {
-  __shared__ __attribute__((aligned(16))) float cmax[kTileThreads / 64][kTile];
+  __shared__ ColMax cmax;
+  __shared__ __attribute__((aligned(16))) uint8_t code[kTile];
   __shared__ __attribute__((aligned(16))) uint32_t tile[kTileWords];
   const int64_t tiles_c = (cols + kTile - 1) / kTile;
   const int64_t n = (rows + kTile - 1) / kTile * tiles_c;
-  const int64_t cp = up128(cols), rp = up16(rows);
   uint32_t unused = 0;
   for (int64_t id = blockIdx.x; id < n; id += gridDim.x) {
     const TilePos t = tile_pos(id, tiles_c);
     float v[4][8];
-    uint2 q[4] = {};
-    uint32_t se = 0;
+    const RawCodes raw = load_raw(t, codes, scales, rows, up128(cols), t.col(), t.c0 / kTile);
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
-      if (t.row(p) < rows) q[p] = *reinterpret_cast<const uint2*>(codes + t.row(p) * cp + t.col());
-    if (t.row(0) < rp) se = *reinterpret_cast<const uint32_t*>(scales + t.c0 / kTile * rp + t.row(0));
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      // rows outside: zero codes, and scale padding that must not turn them into NaN
-      const float s = t.row(p) < rows ? fp4dev::ue8m0_decode((se >> (8 * p)) & 0xFFu) : 0.0f;
-      unpack4<E5>(q[p].x, v[p]);
-      unpack4<E5>(q[p].y, v[p] + 4);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[p][i] *= s;
-    }
+    for (int p = 0; p < 4; ++p) raw_values<E5>(raw, p, t.row(p) < rows, v[p]);
     col_partial(t, v, cmax);
     __syncthreads();
-    float m[8];
-    col_max(t, cmax, m);
-    uint32_t sc[8];
-#pragma unroll
-    for (int c = 0; c < 8; ++c) sc[c] = scale_code<E5>(m[c]);
+    col_codes<E5>(cmax, code, 0);
+    __syncthreads();
+    const uint2 sc = *reinterpret_cast<const uint2*>(code + 8 * t.l);
     const int64_t sp = up16(cols);
-    if (t.tr == 0 && t.col() < sp) store_scales8(sc, scales_t + t.r0 / kTile * sp + t.col());
+    if (t.tr == 0 && t.col() < sp)
+      *reinterpret_cast<uint2*>(scales_t + t.r0 / kTile * sp + t.col()) = sc;
     encode_cols<E5, false>(t, v, sc, tile, unused);
     __syncthreads();
     store_cols(t, tile, cols - t.c0, t.c0, up128(rows), codes_t);
@@ -133,12 +129,10 @@ __global__ __launch_bounds__(256) void k_dequant_fp8(const uint8_t* __restrict__
     const int64_t r = static_cast<int64_t>(i / per_row);
     const int64_t c = static_cast<int64_t>(i - r * per_row) * 8;
     const uint2 q = *reinterpret_cast<const uint2*>(codes + r * cp + c);
-    const float s = fp4dev::ue8m0_decode(scales[(c >> 7) * rp + r]);
+    const float s = code_scale(scales[(c >> 7) * rp + r]);
     float v[8];
-    unpack4<E5>(q.x, v);
-    unpack4<E5>(q.y, v + 4);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= s;
+    unpack4<E5>(q.x, v, s);
+    unpack4<E5>(q.y, v + 4, s);
     if constexpr (F32) {
       float* d = static_cast<float*>(out) + r * cols + c;
       if (whole) {
@@ -155,7 +149,7 @@ __global__ __launch_bounds__(256) void k_dequant_fp8(const uint8_t* __restrict__
       uint16_t* d = static_cast<uint16_t*>(out) + r * cols + c;
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (c + k < cols) d[k] = static_cast<uint16_t>(to_bf16(v[k]));
+        if (c + k < cols) d[k] = to_bf16(v[k]);
     }
   }
 }
