@@ -207,10 +207,67 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
   }
 }
 
-// PREC: bf16 MFMA (fp32 D); else the scaled 8-bit one (bf16 D).
+// One K block on stage C.  PREC: bf16 MFMA (fp32 D); else the scaled 8-bit one.
 template <int FA, bool PREC, int MI, int NI>
+__device__ __forceinline__ void multiply(const Stage<MI, NI>& C, floatx16 (&acc)[MI][NI], uint32_t sa,
+                                         uint32_t sb, int wm, int wn, int i, int h) {
+  if constexpr (PREC) {
+    // a lane's 16 bytes of a row feed two products of 16 K values
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint4 ca[MI], cb[NI];
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const int slot = wm * 32 * MI + mi * 32 + i;
+        ca[mi] = C.a[slot * kChunks + ((2 * q + h) ^ swizzle(slot))];
+      }
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const int slot = wn * 32 * NI + ni * 32 + i;
+        cb[ni] = C.b[slot * kChunks + ((2 * q + h) ^ swizzle(slot))];
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        bf16x8 a[MI], b[NI];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+          a[mi] = widen8<FA == 1>(half ? ca[mi].z : ca[mi].x, half ? ca[mi].w : ca[mi].y, scale_of(sa, mi));
+#pragma unroll
+        for (int ni = 0; ni < NI; ++ni)
+          b[ni] = widen8<false>(half ? cb[ni].z : cb[ni].x, half ? cb[ni].w : cb[ni].y, scale_of(sb, ni));
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+          for (int ni = 0; ni < NI; ++ni)
+            acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[ni], a[mi], acc[mi][ni], 0, 0, 0);
+      }
+    }
+  } else {
+    int8v a[MI], b[NI];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int mi = 0; mi < MI; ++mi) {
+        const int slot = wm * 32 * MI + mi * 32 + i;
+        a[mi] = ks ? frag<1>(C.a, slot, h) : frag<0>(C.a, slot, h);
+      }
+#pragma unroll
+      for (int ni = 0; ni < NI; ++ni) {
+        const int slot = wn * 32 * NI + ni * 32 + i;
+        b[ni] = ks ? frag<1>(C.b, slot, h) : frag<0>(C.b, slot, h);
+      }
+      mfma_slice<FA, MI, NI>(acc, a, b, sa, sb);
+    }
+  }
+}
+
+// Tiles of 64 and 128: S stages in a ring, S - 1 blocks on their way while one
+// is multiplied, one barrier per block.  Two workgroups per CU, so the reads
+// of one are covered by the other's products.
+template <int FA, bool PREC, int MI, int NI, int S>
 __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
-  __shared__ Stage<MI, NI> s0, s1;
+  static_assert(S == 2 || S == 3, "stages");
+  __shared__ Stage<MI, NI> s0, s1, s2;
   int kb0, nkb;
   const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
   int tm, tn;
@@ -227,13 +284,13 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
   for (int j = 0; j < 2 * MI; ++j) {
     const int slot = wave * 16 * MI + 8 * j + (lane >> 3);
     const int64_t r = min(m0 + slot_row<MI>(slot), g.M - 1);
-    src.a[j] = g.codes[0] + r * g.ld[0] + kb0 * kStepBytes + 16 * ((lane & 7) ^ swizzle(slot));
+    src.a[j] = g.codes[0] + r * g.ld[0] + static_cast<int64_t>(kb0) * kStepBytes + 16 * ((lane & 7) ^ swizzle(slot));
   }
 #pragma unroll
   for (int j = 0; j < 2 * NI; ++j) {
     const int slot = wave * 16 * NI + 8 * j + (lane >> 3);
     const int64_t r = min(n0 + slot_row<NI>(slot), g.N - 1);
-    src.b[j] = g.codes[1] + r * g.ld[1] + kb0 * kStepBytes + 16 * ((lane & 7) ^ swizzle(slot));
+    src.b[j] = g.codes[1] + r * g.ld[1] + static_cast<int64_t>(kb0) * kStepBytes + 16 * ((lane & 7) ^ swizzle(slot));
   }
   // the scales' pitch is a multiple of 16 and at least the rows
   src.sa = g.scales[0] + kb0 * g.s_kblk[0] + min(m0 + wm * 32 * MI + i * MI, g.s_kblk[0] - MI);
@@ -247,82 +304,56 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx16{};
 
-  // One step on stage C: its DMA has landed for every wave, the other stage
-  // N (read in the previous step) takes block kb + 1 (the last one again at
-  // the end, unread).
-  auto step = [&](Stage<MI, NI>& C, Stage<MI, NI>& N, int kb) {
-    wait_vmcnt<0>();
+  // A block's scales are loaded before its DMA: kGroup loads a block.
+  constexpr int kGroup = 2 * MI + 2 * NI + 2;
+  uint32_t sa[S], sb[S];
+  auto fetch = [&](Stage<MI, NI>& D, int j, int kb) {
+    const int k = min(kb, nkb - 1);
+    sa[j] = load_scales<MI>(src.sa + k * src.ska);
+    sb[j] = load_scales<NI>(src.sb + k * src.skb);
+    dma(D, src, k, wave);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // Block kb on stage C (number j): it has landed for every wave, and the
+  // stage that was multiplied last (F, number f) takes block kb + S - 1 (past
+  // the end the last one again, unread).
+  auto step = [&](Stage<MI, NI>& C, int j, Stage<MI, NI>& F, int f, int kb) {
+    wait_vmcnt<(S - 2) * kGroup>();
     ring_barrier();
-    dma(N, src, min(kb + 1, nkb - 1), wave);
-    const uint32_t sa = load_scales<MI>(src.sa + kb * src.ska);
-    const uint32_t sb = load_scales<NI>(src.sb + kb * src.skb);
-    if constexpr (PREC) {
-      // a lane's 16 bytes of a row feed two products of 16 K values
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint4 ca[MI], cb[NI];
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
-          const int slot = wm * 32 * MI + mi * 32 + i;
-          ca[mi] = C.a[slot * kChunks + ((2 * q + h) ^ swizzle(slot))];
-        }
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          const int slot = wn * 32 * NI + ni * 32 + i;
-          cb[ni] = C.b[slot * kChunks + ((2 * q + h) ^ swizzle(slot))];
-        }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          bf16x8 a[MI], b[NI];
-#pragma unroll
-          for (int mi = 0; mi < MI; ++mi)
-            a[mi] = widen8<FA == 1>(half ? ca[mi].z : ca[mi].x, half ? ca[mi].w : ca[mi].y, scale_of(sa, mi));
-#pragma unroll
-          for (int ni = 0; ni < NI; ++ni)
-            b[ni] = widen8<false>(half ? cb[ni].z : cb[ni].x, half ? cb[ni].w : cb[ni].y, scale_of(sb, ni));
-#pragma unroll
-          for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-            for (int ni = 0; ni < NI; ++ni)
-              acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[ni], a[mi], acc[mi][ni], 0, 0, 0);
-        }
-      }
-    } else {
-      int8v a[MI], b[NI];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
-          const int slot = wm * 32 * MI + mi * 32 + i;
-          a[mi] = ks ? frag<1>(C.a, slot, h) : frag<0>(C.a, slot, h);
-        }
-#pragma unroll
-        for (int ni = 0; ni < NI; ++ni) {
-          const int slot = wn * 32 * NI + ni * 32 + i;
-          b[ni] = ks ? frag<1>(C.b, slot, h) : frag<0>(C.b, slot, h);
-        }
-        mfma_slice<FA, MI, NI>(acc, a, b, sa, sb);
-      }
-    }
+    const uint32_t ca = sa[j], cb = sb[j];
+    fetch(F, f, kb + S - 1);
+    multiply<FA, PREC, MI, NI>(C, acc, ca, cb, wm, wn, i, h);
   };
   if (nkb > 0) {
-    dma(s0, src, 0, wave);
+    fetch(s0, 0, 0);
+    if constexpr (S == 3) fetch(s1, 1, 1);
+    // whole turns of the ring, then what is left of one (an exit inside the
+    // loop makes the compiler move the accumulators)
     int kb = 0;
-    for (; kb + 1 < nkb; kb += 2) {
-      step(s0, s1, kb);
-      step(s1, s0, kb + 1);
+    if constexpr (S == 3) {
+      for (; kb + 2 < nkb; kb += 3) {
+        step(s0, 0, s2, 2, kb);
+        step(s1, 1, s0, 0, kb + 1);
+        step(s2, 2, s1, 1, kb + 2);
+      }
+      if (kb < nkb) step(s0, 0, s2, 2, kb);
+      if (kb + 1 < nkb) step(s1, 1, s0, 0, kb + 1);
+    } else {
+      for (; kb + 1 < nkb; kb += 2) {
+        step(s0, 0, s1, 1, kb);
+        step(s1, 1, s0, 0, kb + 1);
+      }
+      if (kb < nkb) step(s0, 0, s1, 1, kb);
     }
-    if (kb < nkb) step(s0, s1, kb);
   }
   wait_vmcnt<0>();
   ring_barrier();
-  // both stages are done with: stage 0 and 1 hold the waves' buffers
+  // the stages are done with: the first two hold the waves' buffers
   constexpr int kBuf = 32 * (32 * NI + 4);
   static_assert(2 * kBuf * sizeof(float) <= sizeof(Stage<MI, NI>), "two epilogue buffers per stage");
   float* buf = reinterpret_cast<float*>(wave < 2 ? &s0 : &s1) + (wave & 1) * kBuf;
   epilogue<MI, NI>(g, acc, m0 + wm * 32 * MI, n0 + wn * 32 * NI, lane, buf);
 }
-
 
 // ------------------------------------------------------- 256 x 256, 8-bit --
 // The same product to bf16 for large outputs: a wave's 128 x 128 part needs
@@ -709,21 +740,12 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_f32(Params p) {
   epilogue<4, 4>(g, acc, w.m0 + w.wm * 128, w.n0 + w.wn * 128, w.lane, buf);
 }
 
-template <int FA, bool PREC, int MI, int NI>
-void launch_tile(const fp4lib::Fp8GemmArgs& g, hipStream_t s) {
-  Params p{g, static_cast<int>((g.M + 64 * MI - 1) / (64 * MI)),
-           static_cast<int>((g.N + 64 * NI - 1) / (64 * NI))};
-  const dim3 grid(p.tiles_m * p.tiles_n, g.splits);
-  if constexpr (MI == 4) {
-    if constexpr (PREC) hipLaunchKernelGGL(k_gemm_fp8_wide_f32<FA>, grid, dim3(kThreads), 0, s, p);
-    else if (g.d_bf16 && !g.accumulate && g.N % 8 == 0 && g.ldd % 8 == 0 && g.splits == 1 &&
-             reinterpret_cast<uintptr_t>(g.D) % 16 == 0)
-      hipLaunchKernelGGL(k_gemm_fp8_wide_loop<FA>, dim3(std::min<int>(grid.x, fp4lib::device_cu_count())),
-                         dim3(kThreads), 0, s, p);
-    else hipLaunchKernelGGL(k_gemm_fp8_wide<FA>, grid, dim3(kThreads), 0, s, p);
-  } else {
-    hipLaunchKernelGGL((k_gemm_fp8<FA, PREC, MI, NI>), grid, dim3(kThreads), 0, s, p);
-  }
+template <typename K>
+void launch_kernel(K kernel, const fp4lib::Fp8GemmArgs& g, int bm, int bn, hipStream_t s, int max_wgs = 0) {
+  Params p{g, static_cast<int>((g.M + bm - 1) / bm), static_cast<int>((g.N + bn - 1) / bn)};
+  const int tiles = p.tiles_m * p.tiles_n;
+  hipLaunchKernelGGL(kernel, dim3(max_wgs ? std::min(tiles, max_wgs) : tiles, g.splits), dim3(kThreads), 0,
+                     s, p);
 }
 
 // D from the partial sums of `splits` workgroups per tile, in their order.
@@ -753,35 +775,83 @@ __global__ __launch_bounds__(256) void k_gemm_fp8_join(fp4lib::Fp8GemmArgs g) {
   }
 }
 
-// How a product runs: the kernel (0: few rows; 2, 4: tiles of 128, 256) and
-// the workgroups that share a tile's K.
+// How a product runs: the kernel, and the workgroups that share a tile's K.
+enum Kind { kRows, kTile64, kTile128, kTile256 };
 struct Plan {
-  int kind, splits;
+  Kind kind;
+  int splits;
 };
 
+// The kernel and split with the least estimated time.  A workgroup takes, per
+// K block, t1 us alone on its CU and t2 us beside another (256 x 256 tiles:
+// always alone); a kernel has a fixed part; joining writes and reads the fp32
+// sums.  The constants are fits of measured times on 256 CUs: bf16 (fp32) D,
+// M = 256, N = 4096, K = 21504: 64-row tiles shared by 4 48 (59) us, 128-row tiles by
+// 8 44 (56) us, unshared 78 (175); M = 1000, N = 4608, K = 12288: 256-row tiles by
+// 3 68 (108) us, unshared 101, 128-row 91 (140); M = 2048, N = K = 4096: 128-row 37
+// (61), 256-row 41 (82); M = 1024, N = 12288, K = 4608: 256-row 51 (96), 128-row 64 (103).
+//
+// Up to 16 rows of A: the kernel of gemm_fp8_rows.hip where 64 x 128 tiles would
+// leave half the CUs idle (M = 1: N = 6144, K = 2048 6.4 against 8.3 us; N = 4096,
+// K = 21504 17.5 against 20.6), tiles beyond (N = 21504, K = 4096: 18.2 against
+// 23.1 us, for every row of A is then read by far fewer workgroups).
 Plan plan_of(const fp4lib::Fp8GemmArgs& g) {
   const int64_t cus = fp4lib::device_cu_count();
-  Plan p{2, 1};
-  const int64_t wide = ((g.M + 255) / 256) * ((g.N + 255) / 256);
-  if (g.M <= kMaxRows) {
-    p.kind = 0;
-    p.splits = rows_splits(g);
-  } else if (g.nkb > 0 && wide >= cus / 2 && g.ld[0] < (1 << 23) && g.ld[1] < (1 << 23)) {
-    p.kind = 4;
-  } else {
-    const int64_t tiles = ((g.M + 127) / 128) * ((g.N + 127) / 128);
-    while (tiles * p.splits * 2 <= 2 * cus && g.nkb >= 8 * p.splits && p.splits < 16) p.splits *= 2;
+  auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
+  if (g.M <= kMaxRows && tiles(64, 128) * 2 < cus) return {kRows, 1};
+  struct Cost {
+    Kind kind;
+    int bm, bn, per_cu;
+    double t1, t2, fixed;
+  };
+  static constexpr Cost kCosts[2][3] = {
+      {{kTile64, 64, 128, 2, 0.65, 1.15, 4}, {kTile128, 128, 128, 2, 1.05, 1.8, 4}, {kTile256, 256, 256, 1, 2.4, 2.4, 8}},
+      {{kTile64, 64, 128, 2, 0.43, 0.88, 4}, {kTile128, 128, 128, 2, 0.62, 1.0, 4}, {kTile256, 256, 256, 1, 1.1, 1.1, 8}}};
+  static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
+  Plan best{kTile64, 1};
+  double least = 0.0;
+  for (const Cost& c : kCosts[g.d_bf16 ? 1 : 0]) {
+    // 32-bit offsets within a 256-row tile, and no tail test for K = 0
+    if (c.kind == kTile256 && (g.nkb == 0 || g.ld[0] >= (1 << 23) || g.ld[1] >= (1 << 23))) continue;
+    for (int splits : kSplits) {
+      if (splits > 1 && g.nkb < 4 * splits) break;
+      const int64_t n = tiles(c.bm, c.bn) * splits, slots = c.per_cu * cus, rest = n % slots;
+      const double blocks = static_cast<double>((g.nkb + splits - 1) / splits);
+      const double rounds = static_cast<double>(n / slots) * c.t2 + (rest == 0 ? 0.0 : rest <= cus ? c.t1 : c.t2);
+      const double join = splits > 1 ? 3.0 + splits * static_cast<double>(g.M) * g.N * 8.0 / 4.5e6 : 0.0;
+      const double t = rounds * blocks + c.fixed + join;
+      if (least == 0.0 || t < least) {
+        least = t;
+        best = {c.kind, splits};
+      }
+    }
   }
-  return p;
+  return best;
 }
 
 template <int FA>
-void run(const fp4lib::Fp8GemmArgs& g, int kind, hipStream_t s) {
-  if (kind == 0) launch_rows(g, s);
-  else if (kind == 4 && g.d_bf16) launch_tile<FA, false, 4, 4>(g, s);
-  else if (kind == 4) launch_tile<FA, true, 4, 4>(g, s);
-  else if (g.d_bf16) launch_tile<FA, false, 2, 2>(g, s);
-  else launch_tile<FA, true, 2, 2>(g, s);
+void run(const fp4lib::Fp8GemmArgs& g, Kind kind, hipStream_t s) {
+  const int cus = fp4lib::device_cu_count();
+  switch (kind) {
+    case kRows:
+      launch_rows(g, s);
+      break;
+    case kTile64:
+      if (g.d_bf16) launch_kernel(k_gemm_fp8<FA, false, 1, 2, 3>, g, 64, 128, s);
+      else launch_kernel(k_gemm_fp8<FA, true, 1, 2, 3>, g, 64, 128, s);
+      break;
+    case kTile128:
+      if (g.d_bf16) launch_kernel(k_gemm_fp8<FA, false, 2, 2, 2>, g, 128, 128, s);
+      else launch_kernel(k_gemm_fp8<FA, true, 2, 2, 2>, g, 128, 128, s);
+      break;
+    case kTile256:
+      if (!g.d_bf16) launch_kernel(k_gemm_fp8_wide_f32<FA>, g, 256, 256, s);
+      else if (!g.accumulate && g.N % 8 == 0 && g.ldd % 8 == 0 && g.splits == 1 &&
+               reinterpret_cast<uintptr_t>(g.D) % 16 == 0)
+        launch_kernel(k_gemm_fp8_wide_loop<FA>, g, 256, 256, s, cus);
+      else launch_kernel(k_gemm_fp8_wide<FA>, g, 256, 256, s);
+      break;
+  }
 }
 
 }  // namespace

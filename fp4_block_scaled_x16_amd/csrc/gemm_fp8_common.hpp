@@ -59,8 +59,7 @@ __device__ __forceinline__ fp4lib::Fp8GemmArgs split_args(const fp4lib::Fp8GemmA
 }
 
 // Few rows of A (gemm_fp8_rows.hip): M at most kMaxRows.
-constexpr int kMaxRows = 64;
-int rows_splits(const fp4lib::Fp8GemmArgs& g);
+constexpr int kMaxRows = 16;
 void launch_rows(const fp4lib::Fp8GemmArgs& g, hipStream_t s);
 
 }  // namespace fp8gemm
