@@ -6,4 +6,4 @@ ctypes binding over it that takes torch device tensors for memory and the
 current torch stream; importing this package does not load the library, the
 first call does, and it raises if the library is missing.
 """
-__all__ = ["api", "inputs"]
+__all__ = ["api", "ffn", "inputs", "linear"]

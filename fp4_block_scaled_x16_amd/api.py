@@ -628,6 +628,8 @@ def gemm(a: Operand, b: Operand, M, N, K, out=None, accumulate=False, device=Non
     t, dev = OUT_TYPES[out.dtype], out.device
     ws, n = None, 0
     if a.format in FP8 and b.format in FP8:
+        if qa and qb and (qa.codes.device != dev or qb.codes.device != dev):
+            raise ValueError("the operands and out are on different devices")
         n = _gemm_workspace(dev, M, N, K, t, a.format, b.format, a.ld_codes, b.ld_codes)
         if n:
             ws = torch.empty(n, dtype=torch.uint8, device=dev)

@@ -1,4 +1,4 @@
-"""A linear layer whose three GEMMs run on FP4 operands.
+"""A linear layer whose three GEMMs run on FP4 or FP8 operands.
 
 NVFP4 paper §4.1 and Fig. 5: in a linear layer Y = X W^T, the forward
 product (Fprop) and both backward products -- Dgrad (dX = dY W) and Wgrad
@@ -31,6 +31,12 @@ rounding, the same random bits for both orientations), so every operand a
 tensor contributes holds the same values in Fprop / Dgrad and in Wgrad;
 scale_round = "up" rounds block scales up (truncation-free scaling).
 
+With fmt = "fp8" (E4M3, a power-of-two scale per block of 128) X is encoded in
+1x128 blocks, W in 128x128 blocks with its transpose, dY in grad_fmt along its
+rows and its columns.  With checkpoint8 (the default) the forward pass keeps
+X's row codes alone, one byte per element, and the backward pass re-encodes them
+along the tokens for Wgrad; without it the forward pass encodes X both ways.
+
 Tensor amax: current scaling (recomputed every step, the NVFP4 recipe) or,
 with amax_interval = N > 1, recomputed every N-th step and reused in
 between (the periodic tensor scaling of the UE5M3 recipe).  The SR random
@@ -62,7 +68,7 @@ from . import api
 
 @dataclass
 class Recipe:
-    fmt: str = "nvfp4"            # "nvfp4", "ue5m3" or "mxfp4"
+    fmt: str = "nvfp4"            # "nvfp4", "ue5m3", "mxfp4" or "fp8"
     target_x: float = 448.0       # T of s_enc = 6 T / amax, per tensor
     target_w: float = 448.0
     target_dy: float = 448.0
@@ -78,10 +84,12 @@ class Recipe:
     rht_kd_n: int = 16            # its size N: 4 or 16
     rht_kd_signs: int = 0         # its N-bit sign mask
     out_dtype: str = "fp32"       # Y and dX: "fp32" or "bf16"
+    grad_fmt: str = "fp8_e5m2"    # fmt "fp8": the format of dY ("fp8" or "fp8_e5m2")
+    checkpoint8: bool = True      # fmt "fp8": keep only X's row codes for the backward pass
 
     @property
     def two_level(self):
-        return self.fmt != "mxfp4"
+        return self.fmt in ("nvfp4", "ue5m3")
 
 
 class QuantizedLinear:
@@ -99,6 +107,10 @@ class QuantizedLinear:
             raise ValueError("2D activation blocks need NVFP4 or UE5M3 and no RHT")
         if recipe.rht_kd and (not recipe.two_level or recipe.rht_kd_n not in (4, 16)):
             raise ValueError("the RHT along K needs NVFP4 or UE5M3 and N = 4 or 16")
+        if recipe.fmt not in ("nvfp4", "ue5m3", "mxfp4", "fp8"):
+            raise ValueError("fmt must be 'nvfp4', 'ue5m3', 'mxfp4' or 'fp8'")
+        if recipe.fmt == "fp8" and (recipe.rht or recipe.grad_fmt not in ("fp8", "fp8_e5m2")):
+            raise ValueError("fp8 takes no RHT, and grad_fmt 'fp8' or 'fp8_e5m2'")
         if recipe.out_dtype not in _OUT_DTYPES:
             raise ValueError("out_dtype must be 'fp32' or 'bf16'")
         self.weight = weight
@@ -168,6 +180,8 @@ class QuantizedLinear:
         r = self.recipe
         if x.dim() != 2 or x.shape[1] != self.in_features:
             raise ValueError("x must be [tokens, in_features]")
+        if r.fmt == "fp8":
+            return self._forward_fp8(x)
         am, am_t = self._amax_args(x, "x", r.rht or r.rht_kd)
         if r.act_block == "2d":
             qx2 = api.quantize(x, r.fmt, block="2d", emit_transpose=True, target=r.target_x,
@@ -207,11 +221,45 @@ class QuantizedLinear:
                      out_dtype=_OUT_DTYPES[r.out_dtype])
         return y, (xt_op, wt_op, tokens)
 
+    def _forward_fp8(self, x):
+        r = self.recipe
+        if r.checkpoint8:
+            qx = saved = api.quantize(x, "fp8", counters=self.counters)
+        else:
+            qx, saved = api.quantize_dual(x, "fp8", counters=self.counters)
+        y, qw_t = self._fprop_fp8(qx, _OUT_DTYPES[r.out_dtype])
+        return y, (saved, qw_t, x.shape[0])
+
+    def _fprop_fp8(self, qx, out_dtype):
+        """Y from X's row codes, and the codes of W^T for Dgrad."""
+        qw, qw_t = api.quantize_dual(self.weight, "fp8", block="2d", counters=self.counters)
+        return api.gemm(qx.operand(), qw.operand(), qx.rows, self.out_features, self.in_features,
+                        out_dtype=out_dtype), qw_t
+
+    def _dgrad_fp8(self, qdy, qw_t, out_dtype):
+        return api.gemm(qdy.operand(), qw_t.operand(), qdy.rows, self.in_features,
+                        self.out_features, out_dtype=out_dtype)
+
+    def _wgrad_fp8(self, qdy_t, qx_t):
+        api.gemm(qdy_t.operand(), qx_t.operand(), self.out_features, self.in_features, qdy_t.cols,
+                 out=self.main_grad, accumulate=True)
+        self.step += 1
+
+    def _backward_fp8(self, dy, saved):
+        r = self.recipe
+        qx, qw_t, tokens = saved
+        qdy, qdy_t = api.quantize_dual(dy, r.grad_fmt, counters=self.counters)
+        dx = self._dgrad_fp8(qdy, qw_t, _OUT_DTYPES[r.out_dtype])
+        self._wgrad_fp8(qdy_t, api.requantize_t(qx) if r.checkpoint8 else qx)
+        return dx
+
     def _backward(self, dy, saved):
         r = self.recipe
         xt_op, wt_op, tokens = saved
         if dy.dim() != 2 or tuple(dy.shape) != (tokens, self.out_features):
             raise ValueError("dy must be [tokens, out_features]")
+        if r.fmt == "fp8":
+            return self._backward_fp8(dy, saved)
         am, am_t = self._amax_args(dy, "dy", r.rht or r.rht_kd)
         if r.act_block == "2d":
             qdy2 = api.quantize(dy, r.fmt, block="2d", rnd="sr", seed=r.sr_seed,
