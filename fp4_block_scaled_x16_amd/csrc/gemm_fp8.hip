@@ -136,20 +136,24 @@ __device__ __forceinline__ void mfma_slice(floatx16 (&acc)[MI][NI], const int8v 
   }
 }
 
+// 16 and 8 bytes at an element's alignment (gfx950 takes them as one access).
+typedef float float4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t uint2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t uint4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // D through LDS: each wave's 32 rows of one mi (rows MI i + mi) x 32 NI
 // columns go through its own buffer, in which a lane writes NI consecutive
-// columns, and leave as whole row segments of 128 NI bytes.  Every value is
-// the fp32 sum, plus the old D if accumulating, rounded once for bf16.
+// columns, and leave as whole row segments of 128 NI bytes, whatever the
+// alignment of D's rows (the last group of a row whose length is no multiple
+// of 4 goes out element by element).  Every value is the fp32 sum, plus the old
+// D if accumulating, rounded once for bf16.
 template <int MI, int NI>
 __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 (&acc)[MI][NI],
                                          int64_t row0, int64_t col0, int lane, float* buf) {
-  constexpr int W = 32 * NI, P = W + 4;
+  constexpr int W = 32 * NI, P = W + 4, L = W / 4;      // L: lanes of a row
   const int i = lane & 31, h = lane >> 5;
-  const int64_t left = g.N - col0;           // columns of D from col0 on
-  const int es = g.d_bf16 ? 2 : 4;
-  // whole groups of 4 columns, aligned
-  const bool vec = left >= W && (g.ldd & 3) == 0 &&
-                   (reinterpret_cast<uintptr_t>(g.D) & (4 * es - 1)) == 0;
+  const int c = (lane % L) * 4;
+  const int n = static_cast<int>(min(g.N - col0 - c, int64_t(4)));     // this lane's columns inside D
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
 #pragma unroll
@@ -159,46 +163,41 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
       for (int ni = 0; ni < NI; ++ni) d[ni] = acc[mi][ni][k];
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-    if (vec) {
-      constexpr int L = W / 4;               // lanes of a row
 #pragma unroll 4
-      for (int k = 0; k < 32 * L / 64; ++k) {
-        const int r = k * (64 / L) + lane / L, c = (lane % L) * 4;
-        const int64_t row = row0 + r * MI + mi;
-        if (row >= g.M) continue;
-        float4 v = *reinterpret_cast<const float4*>(buf + r * P + c);
-        if (g.d_bf16) {
-          uint2* d = reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.D) + row * g.ldd + col0 + c);
+    for (int k = 0; k < 32 * L / 64; ++k) {
+      const int r = k * (64 / L) + lane / L;
+      const int64_t row = row0 + r * MI + mi;
+      if (row >= g.M || n <= 0) continue;
+      float4 v = *reinterpret_cast<const float4*>(buf + r * P + c);
+      if (g.d_bf16) {
+        uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col0 + c;
+        if (n == 4) {
           if (g.accumulate) {
-            const uint2 o = *d;
+            const uint2_any o = *reinterpret_cast<const uint2_any*>(d);
             v.x += __uint_as_float(o.x << 16);
             v.y += __uint_as_float(o.x & 0xFFFF0000u);
             v.z += __uint_as_float(o.y << 16);
             v.w += __uint_as_float(o.y & 0xFFFF0000u);
           }
-          *d = make_uint2(fp8dev::pack_bf16(v.x, v.y), fp8dev::pack_bf16(v.z, v.w));
+          *reinterpret_cast<uint2_any*>(d) = uint2_any{fp8dev::pack_bf16(v.x, v.y), fp8dev::pack_bf16(v.z, v.w)};
         } else {
-          float4* d = reinterpret_cast<float4*>(static_cast<float*>(g.D) + row * g.ldd + col0 + c);
-          if (g.accumulate) {
-            const float4 o = *d;
-            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-          }
-          *d = v;
+          const float e[3] = {v.x, v.y, v.z};
+#pragma unroll
+          for (int x = 0; x < 3; ++x)
+            if (x < n)
+              d[x] = fp8dev::to_bf16(g.accumulate ? e[x] + __uint_as_float(static_cast<uint32_t>(d[x]) << 16) : e[x]);
         }
-      }
-    } else {
-      for (int k = 0; k < 32 * W / 64; ++k) {
-        const int r = (k * 64 + lane) / W, c = (k * 64 + lane) % W;
-        const int64_t row = row0 + r * MI + mi;
-        if (row >= g.M || c >= left) continue;
-        float v = buf[r * P + c];
-        if (g.d_bf16) {
-          uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col0 + c;
-          if (g.accumulate) v += __uint_as_float(static_cast<uint32_t>(*d) << 16);
-          *d = fp8dev::to_bf16((v));
+      } else {
+        float* d = static_cast<float*>(g.D) + row * g.ldd + col0 + c;
+        if (n == 4) {
+          float4_any o = float4_any{v.x, v.y, v.z, v.w};
+          if (g.accumulate) o += *reinterpret_cast<const float4_any*>(d);
+          *reinterpret_cast<float4_any*>(d) = o;
         } else {
-          float* d = static_cast<float*>(g.D) + row * g.ldd + col0 + c;
-          *d = g.accumulate ? *d + v : v;
+          const float e[3] = {v.x, v.y, v.z};
+#pragma unroll
+          for (int x = 0; x < 3; ++x)
+            if (x < n) d[x] = g.accumulate ? d[x] + e[x] : e[x];
         }
       }
     }
@@ -468,8 +467,17 @@ __device__ __forceinline__ void wide_store_bf16(const fp4lib::Fp8GemmArgs& g, fl
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const uint4 v = *reinterpret_cast<const uint4*>(buf + (8 * r + (w.lane >> 3)) * kWidePitch + 8 * (w.lane & 7));
-        if (row0 + 32 * r + mi < g.M && col + 64 * half < g.N)
-          *reinterpret_cast<uint4*>(d + (32 * r + mi) * g.ldd + 64 * half) = v;
+        if (row0 + 32 * r + mi < g.M && col + 64 * half < g.N) {
+          uint16_t* o = d + (32 * r + mi) * g.ldd + 64 * half;
+          if (col + 64 * half + 8 <= g.N) {
+            *reinterpret_cast<uint4_any*>(o) = uint4_any{v.x, v.y, v.z, v.w};
+          } else {
+            const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int x = 0; x < 7; ++x)
+              if (col + 64 * half + x < g.N) o[x] = static_cast<uint16_t>(e[x >> 1] >> (16 * (x & 1)));
+          }
+        }
       }
       __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
     }
@@ -566,8 +574,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide(Params p) {
   epilogue<4, 4>(g, acc, w.m0 + w.wm * 128, w.n0 + w.wn * 128, w.lane, buf);
 }
 
-// A bf16 D with 16-byte rows (and N a multiple of 8), not accumulated: a
-// workgroup per CU takes tile after tile, the first two blocks of the next
+// A bf16 D, not accumulated: a workgroup per CU takes tile after tile, the first two blocks of the next
 // one on their way while a tile is stored.
 template <int FA>
 __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_loop(Params p) {
@@ -846,8 +853,7 @@ void run(const fp4lib::Fp8GemmArgs& g, Kind kind, hipStream_t s) {
       break;
     case kTile256:
       if (!g.d_bf16) launch_kernel(k_gemm_fp8_wide_f32<FA>, g, 256, 256, s);
-      else if (!g.accumulate && g.N % 8 == 0 && g.ldd % 8 == 0 && g.splits == 1 &&
-               reinterpret_cast<uintptr_t>(g.D) % 16 == 0)
+      else if (!g.accumulate && g.splits == 1)
         launch_kernel(k_gemm_fp8_wide_loop<FA>, g, 256, 256, s, cus);
       else launch_kernel(k_gemm_fp8_wide<FA>, g, 256, 256, s);
       break;
