@@ -755,29 +755,46 @@ void launch_kernel(K kernel, const fp4lib::Fp8GemmArgs& g, int bm, int bn, hipSt
                      s, p);
 }
 
-// D from the partial sums of `splits` workgroups per tile, in their order.
+// D from the partial sums of `splits` workgroups per tile, in their order; a
+// thread 4 columns.
 __global__ __launch_bounds__(256) void k_gemm_fp8_join(fp4lib::Fp8GemmArgs g) {
-  const int64_t np = part_pitch(g.N), per_row = np / 4, n = g.M * per_row;
+  const int64_t np = part_pitch(g.N), per_row = np / 4, n = g.M * per_row, plane = g.M * np;
   for (int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; id < n;
        id += static_cast<int64_t>(gridDim.x) * 256) {
     const int64_t row = id / per_row, col = (id - row * per_row) * 4;
-    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int k = 0; k < g.splits; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(g.part + (k * g.M + row) * np + col);
-      v = make_float4(v.x + a.x, v.y + a.y, v.z + a.z, v.w + a.w);
+    const float* src = g.part + row * np + col;
+    float4_any v = *reinterpret_cast<const float4_any*>(src);
+    int k = 1;
+    for (; k + 3 <= g.splits; k += 3) {          // three loads at a time
+      const float4_any a = *reinterpret_cast<const float4_any*>(src + k * plane),
+                       b = *reinterpret_cast<const float4_any*>(src + (k + 1) * plane),
+                       c = *reinterpret_cast<const float4_any*>(src + (k + 2) * plane);
+      v += a;
+      v += b;
+      v += c;
     }
-    const float r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (col + e >= g.N) continue;
-      if (g.d_bf16) {
-        uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col + e;
-        const float o = g.accumulate ? __uint_as_float(static_cast<uint32_t>(*d) << 16) : 0.0f;
-        *d = fp8dev::to_bf16((g.accumulate ? r[e] + o : r[e]));
-      } else {
-        float* d = static_cast<float*>(g.D) + row * g.ldd + col + e;
-        *d = g.accumulate ? *d + r[e] : r[e];
+    for (; k < g.splits; ++k) v += *reinterpret_cast<const float4_any*>(src + k * plane);
+    const bool whole = col + 4 <= g.N;
+    if (g.d_bf16) {
+      uint16_t* d = static_cast<uint16_t*>(g.D) + row * g.ldd + col;
+      if (whole && !g.accumulate) {
+        *reinterpret_cast<uint2_any*>(d) = uint2_any{fp8dev::pack_bf16(v.x, v.y), fp8dev::pack_bf16(v.z, v.w)};
+        continue;
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < g.N)
+          d[e] = fp8dev::to_bf16(g.accumulate ? v[e] + __uint_as_float(static_cast<uint32_t>(d[e]) << 16) : v[e]);
+    } else {
+      float* d = static_cast<float*>(g.D) + row * g.ldd + col;
+      if (whole) {
+        if (g.accumulate) v += *reinterpret_cast<const float4_any*>(d);
+        *reinterpret_cast<float4_any*>(d) = v;
+        continue;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < g.N) d[e] = g.accumulate ? d[e] + v[e] : v[e];
     }
   }
 }
