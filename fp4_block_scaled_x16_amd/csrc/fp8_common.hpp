@@ -280,8 +280,10 @@ __device__ __forceinline__ void col_codes(const ColMax& cmax, uint8_t (&code)[kT
 
 // Transposed code tile in LDS: 128 columns of 128 bytes.  Column c's word of
 // rows 4q .. 4q + 3 lies in row c ^ (c / 64), 16-byte chunk (q / 4) ^ (c / 8 % 8):
-// the 64 words that a wave writes at once (16 columns 8 apart, 4 row groups
-// of one chunk) are on 64 different banks, and a thread reads 16 bytes.
+// the words that a wave writes at once (16 columns 8 apart, 4 row groups of one
+// chunk) are spread over all 64 words of a row pair, and a thread reads 16
+// bytes.  Half a wave still meets two to a bank of 32; a layout without that
+// measured the same times, the memory traffic being the bound.
 constexpr int kTileWords = kTile * kTile / 4;
 __device__ __forceinline__ int tile_chunk(int c, int ch) {
   return (c ^ (c >> 6)) * 8 + (ch ^ ((c >> 3) & 7));
