@@ -110,8 +110,8 @@ def load_library(path=None):
     lib.fp4_selftest_gemm_decode.argtypes = [i32, vp, vp]
     lib.fp4_selftest_set_geometry.argtypes = [i32, i32]
     for f in ("fp4_amax", "fp4_quantize", "fp4_quantize_dual", "fp4_dequantize", "fp4_rht16",
-              "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_gemm_ws", "fp4_selftest_sweep", "fp4_selftest_gemm_decode",
-              "fp4_selftest_set_geometry"):
+              "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_gemm_ws",
+              "fp4_selftest_sweep", "fp4_selftest_gemm_decode", "fp4_selftest_set_geometry"):
         getattr(lib, f).restype = ctypes.c_int
     lib.fp4_status_string.argtypes = [ctypes.c_int]
     lib.fp4_status_string.restype = ctypes.c_char_p
@@ -257,8 +257,9 @@ def quantize(x, fmt="nvfp4", block="1d", orient="row", rnd="rne", seed=0, offset
     """Quantize a bf16 [R, C] matrix.  orient="col" quantizes X^T ([C, R]).
     scale_layout: "rowmajor" (the default) or "tiled" (1D blocks only).
     fmt "fp8" (E4M3) and "fp8_e5m2": any R and C, block "1d" (1x128) or "2d"
-    (128x128), orient "row" or "col", rnd "rne"; scales "kmajor".  rht_n: size of
-    the RHT (4, 16, 32, 64, 128); signs: its sign mask, up to 128 bits.
+    (128x128), orient "row" or "col", rnd "rne"; scales "kmajor"; x's row pitch a
+    multiple of 8, as ever.  rht_n: size of the RHT (4, 16, 32, 64, 128); signs:
+    its sign mask, up to 128 bits.
     scale_round: "rne" or "up" (truncation-free block scales).
     global_scope: "tensor" or "row" (rowwise 1D NVFP4 / UE5M3: one global
     scale per row, amax and s_dec of R entries, no separate amax pass).
@@ -400,6 +401,9 @@ def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpo
         scale_layout = SCALES_KMAJOR
     elif isinstance(scale_layout, str):
         scale_layout = SCALE_LAYOUTS[scale_layout]
+    if counters is not None and (counters.device != x.device or counters.dtype != torch.int64
+                                 or counters.shape != (5,) or not counters.is_contiguous()):
+        raise ValueError("counters must be an int64 [5] tensor on x's device (new_counters)")
     blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
     q = [_fp8_buffers(f, R, C, x.device, blk)] if row else []
     q += [_fp8_buffers(f, C, R, x.device, blk)] if col else []
@@ -576,11 +580,11 @@ def dequantize(q: Quantized, out_dtype=torch.float32, out=None):
           or not out.is_contiguous()):
         raise ValueError("out must be a contiguous %s tensor of shape (%d, %d)"
                          % (out_dtype, q.rows, q.cols))
-    lib = load_library()
-    _check(lib.fp4_dequantize(q.fmt, q.block, q.scale_layout, _ptr(q.codes), _ptr(q.scales),
-                              _ptr(q.s_dec), q.scope,
-                              q.rows, q.cols, _ptr(out), int(out_dtype == torch.float32),
-                              _stream(out.device)), "fp4_dequantize")
+    elif out.device != q.codes.device:
+        raise ValueError("out and the codes are on different devices")
+    _launch("fp4_dequantize", load_library().fp4_dequantize, out.device, q.fmt, q.block,
+            q.scale_layout, q.codes.data_ptr(), q.scales.data_ptr(), _addr(q.s_dec), q.scope,
+            q.rows, q.cols, out.data_ptr(), int(out_dtype == torch.float32))
     return out
 
 

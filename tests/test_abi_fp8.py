@@ -238,3 +238,24 @@ def test_binding_rejects():
             api.gemm(a, b, M, N, K, out=torch.zeros((8, 8)))
     with pytest.raises(ValueError):
         api.gemm(a, b, 4, 6, 130, out=torch.zeros((4, 5)))
+
+
+def test_binding_rejects_other_devices():
+    """Tensors that a kernel would reach at another device's address."""
+    x = torch.zeros((128, 128), dtype=torch.bfloat16)
+    for counters in (torch.zeros(5, dtype=torch.int64, device="meta"), torch.zeros(4, dtype=torch.int64),
+                     torch.zeros(5, dtype=torch.int32), torch.zeros(10, dtype=torch.int64)[::2]):
+        for call in (api.quantize, api.quantize_dual):
+            with pytest.raises(ValueError, match="counters"):
+                call(x, "fp8", counters=counters)
+    with pytest.raises(ValueError, match="different devices"):
+        api.dequantize(matrix(), out=torch.empty((4, 130), device="meta"))
+    with pytest.raises(ValueError, match="different devices"):
+        api.act_backward(matrix(128, 128), x.to("meta"), "relu2")
+    a = matrix().operand()
+    with pytest.raises(ValueError, match="different devices"):
+        api.gemm(a, a, 4, 4, 130, out=torch.empty((4, 4), device="meta"))
+    for call in (lambda: api.quantize(x, "fp8"), lambda: api.act_quantize(x, "relu2"),
+                 lambda: api.requantize_t(matrix()), lambda: api.dequantize(matrix())):
+        with pytest.raises(ValueError, match="on the GPU"):
+            call()
