@@ -20,13 +20,15 @@ The gradient is that of the layer at the checkpoint's h, as the linears' are
 those of their encoded operands.  X, dY, Y and dX are bf16; weight gradients
 accumulate into the two layers' fp32 main_grad.  Calling the layer runs it under
 autograd (the weights get no .grad); `forward` / `backward` are the same steps.
+Both may be captured into a graph; under autograd the captured x should be no
+leaf of an eager graph that is still alive (a leaf keeps its first stream).
 """
 from __future__ import annotations
 
 import torch
 
 from . import api
-from .linear import QuantizedLinear, Recipe
+from .linear import QuantizedLinear, Recipe, grad_alias
 
 
 class QuantizedFFN:
@@ -52,7 +54,7 @@ class QuantizedFFN:
         self._saved = None
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
-        return _FfnFunction.apply(x, self.up.weight, self.down.weight, self)
+        return _FfnFunction.apply(x, grad_alias(self.up.weight), grad_alias(self.down.weight), self)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         y, self._saved = self._forward(x)
@@ -104,5 +106,7 @@ class _FfnFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        if ctx.saved is None:
+            raise RuntimeError("a step's operands are freed by its first backward pass")
         saved, ctx.saved = ctx.saved, None
         return ctx.layer._backward(dy.contiguous(), saved), None, None, None

@@ -66,6 +66,14 @@ import torch
 from . import api
 
 
+def grad_alias(weight):
+    """The weight for one call's autograd graph, as a leaf of that graph alone.
+    A weight needs no gradient of its own there, but makes the output need
+    one; as a leaf that several graphs share it would carry the stream of the
+    first into a backward pass that is being captured on another."""
+    return weight.detach().requires_grad_(weight.requires_grad)
+
+
 @dataclass
 class Recipe:
     fmt: str = "nvfp4"            # "nvfp4", "ue5m3", "mxfp4" or "fp8"
@@ -161,7 +169,7 @@ class QuantizedLinear:
         if self.recipe.out_dtype != "bf16":
             raise ValueError("the autograd path needs Recipe(out_dtype='bf16'): its gradient "
                              "dY is quantized from bf16")
-        return _Fp4LinearFunction.apply(x, self.weight, self)
+        return _Fp4LinearFunction.apply(x, grad_alias(self.weight), self)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         """Fprop of one step; the operands Dgrad / Wgrad need are kept for
@@ -300,6 +308,8 @@ class _Fp4LinearFunction(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, dy):
+        if ctx.saved is None:
+            raise RuntimeError("a step's operands are freed by its first backward pass")
         saved, ctx.saved = ctx.saved, None
         dx = ctx.layer._backward(dy.contiguous(), saved)
         return dx, None, None

@@ -164,3 +164,62 @@ def test_a_captured_training_step():
         torch.cuda.synchronize()
         for got, ref in zip((y, dx, layer.up.main_grad, layer.down.main_grad), want[k]):
             assert torch.equal(got, ref)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_the_graph_has_no_leaf_of_the_weights(fmt):
+    """Two steps share no autograd leaf (which would carry the first step's
+    stream into the second), and weights that want gradients make the output
+    want one."""
+    leaves = []
+    up, down = (t.requires_grad_() for t in (rand(256, 128, 1, 0.1), rand(128, 128, 2, 0.1)))
+    r = Recipe(fmt=fmt, out_dtype="bf16")
+    ffn, linear = QuantizedFFN(up, down, "swiglu", r), QuantizedLinear(up, r)
+    for layer in (ffn, linear):
+        ys = [layer(rand(32, 128, k)) for k in (3, 4)]
+        leaves += [f.variable for y in ys for f, _ in y.grad_fn.next_functions if f is not None]
+    assert len(leaves) == 6 and len({id(t) for t in leaves}) == 6
+    assert all(t is not up and t is not down for t in leaves)
+    for y in ys:
+        y.backward(torch.ones_like(y))
+        with pytest.raises(RuntimeError):
+            y.grad_fn.apply(torch.ones_like(y))
+    assert up.grad is None and not QuantizedLinear(up.detach(), r)(rand(32, 128, 5)).requires_grad
+
+
+def test_autograd_captured_beside_an_eager_step():
+    """Weights that want gradients, an eager step whose graph is still alive, and
+    a captured forward and backward of the same layer."""
+    T, D, F = 64, 128, 128
+    up, down = (t.requires_grad_() for t in (rand(2 * F, D, 1, 0.1), rand(D, F, 2, 0.1)))
+    layer = QuantizedFFN(up, down, "swiglu")
+    xs, dy = [rand(T, D, k) for k in (3, 4)], rand(T, D, 5, 1e-2)
+    want = []
+    for x in xs:
+        one = QuantizedFFN(up, down, "swiglu")
+        want.append((one.forward(x), one.backward(dy), one.up.main_grad, one.down.main_grad)[0::2])
+    alive = layer(xs[0])
+    x = xs[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        y = layer(x)
+        y.backward(dy)
+    for k in (1, 0, 1):
+        x.copy_(xs[k])
+        layer.up.main_grad.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want[k][0]) and torch.equal(layer.up.main_grad, want[k][1])
+    layer.up.main_grad.zero_()
+    alive.backward(dy)
+    assert torch.equal(layer.up.main_grad, want[0][1])
+
+
+@pytest.mark.parametrize("act", ["swiglu", "relu2"])
+def test_no_tokens(act):
+    up, down = rand(256 if act == "swiglu" else 128, 128, 1), rand(64, 128, 2)
+    layer = QuantizedFFN(up, down, act)
+    x = torch.empty((0, 128), dtype=BF, device=DEV)
+    assert layer.forward(x).shape == (0, 64)
+    assert layer.backward(torch.empty((0, 64), dtype=BF, device=DEV)).shape == (0, 128)
+    assert not layer.up.main_grad.any() and not layer.down.main_grad.any()
