@@ -303,8 +303,9 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
 #pragma unroll
     for (int ni = 0; ni < NI; ++ni) acc[mi][ni] = floatx16{};
 
-  // A block's scales are loaded before its DMA: kGroup loads a block.
-  constexpr int kGroup = 2 * MI + 2 * NI + 2;
+  // A block's DMA; its scales are loaded before them, so that a wait that leaves
+  // one block's DMA under way has the block before it complete.
+  constexpr int kGroup = 2 * MI + 2 * NI;
   uint32_t sa[S], sb[S];
   auto fetch = [&](Stage<MI, NI>& D, int j, int kb) {
     const int k = min(kb, nkb - 1);
@@ -806,7 +807,8 @@ struct Plan {
   int splits;
 };
 
-// The kernel and split with the least estimated time.  A workgroup takes, per
+// The kernel and split (if the caller has a workspace: share) with the least
+// estimated time.  A workgroup takes, per
 // K block, t1 us alone on its CU and t2 us beside another (256 x 256 tiles:
 // always alone); a kernel has a fixed part; joining writes and reads the fp32
 // sums.  The constants are fits of measured times on 256 CUs: bf16 (fp32) D,
@@ -819,7 +821,7 @@ struct Plan {
 // leave half the CUs idle (M = 1: N = 6144, K = 2048 6.4 against 8.3 us; N = 4096,
 // K = 21504 17.5 against 20.6), tiles beyond (N = 21504, K = 4096: 18.2 against
 // 23.1 us, for every row of A is then read by far fewer workgroups).
-Plan plan_of(const fp4lib::Fp8GemmArgs& g) {
+Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
   const int64_t cus = fp4lib::device_cu_count();
   auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   if (g.M <= kMaxRows && tiles(64, 128) * 2 < cus) return {kRows, 1};
@@ -838,7 +840,7 @@ Plan plan_of(const fp4lib::Fp8GemmArgs& g) {
     // 32-bit offsets within a 256-row tile, and no tail test for K = 0
     if (c.kind == kTile256 && (g.nkb == 0 || g.ld[0] >= (1 << 23) || g.ld[1] >= (1 << 23))) continue;
     for (int splits : kSplits) {
-      if (splits > 1 && g.nkb < 4 * splits) break;
+      if (splits > 1 && (!share || g.nkb < 4 * splits)) break;
       const int64_t n = tiles(c.bm, c.bn) * splits, slots = c.per_cu * cus, rest = n % slots;
       const double blocks = static_cast<double>((g.nkb + splits - 1) / splits);
       const double rounds = static_cast<double>(n / slots) * c.t2 + (rest == 0 ? 0.0 : rest <= cus ? c.t1 : c.t2);
@@ -883,14 +885,13 @@ void run(const fp4lib::Fp8GemmArgs& g, Kind kind, hipStream_t s) {
 namespace fp4lib {
 
 int64_t gemm_fp8_workspace(const Fp8GemmArgs& g) {
-  const int splits = fp8gemm::plan_of(g).splits;
+  const int splits = fp8gemm::plan_of(g, true).splits;
   return splits > 1 ? splits * g.M * fp8gemm::part_pitch(g.N) * 4 : 0;
 }
 
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& args, hipStream_t s) {
   Fp8GemmArgs g = args;
-  fp8gemm::Plan p = fp8gemm::plan_of(g);
-  if (!g.part) p.splits = 1;            // without a workspace
+  const fp8gemm::Plan p = fp8gemm::plan_of(g, g.part != nullptr);
   g.splits = p.splits;
   if (g.a_e5m2) fp8gemm::run<1>(g, p.kind, s);
   else fp8gemm::run<0>(g, p.kind, s);

@@ -408,7 +408,7 @@ typedef enum fp4_out_type_e FP4_ENUM_INT { FP4_OUT_F32 = 0, FP4_OUT_BF16 = 1 } f
  * below the largest one's binade, so the value before its rounding is within
  * 1e-5 sum |a b| + 7 * 2^-13 of each group's largest |a b|, subnormal
  * elements counted as the smallest normal one (fp32 D: products and sums in
- * fp32).
+ * fp32, of operands below 2^-126 as bf16 holds them).
  * K == 0 writes zeros (or leaves D unchanged when accumulating).
  */
 fp4_status fp4_gemm(const fp4_operand* A /* host */, const fp4_operand* B /* host */,
@@ -458,7 +458,8 @@ typedef enum fp4_act_e FP4_ENUM_INT { FP4_ACT_SWIGLU = 0, FP4_ACT_RELU2 = 1 } fp
  * fp4_act_quantize -- a = act(h) of the first linear's bf16 output, encoded
  * for the second linear's product, and h itself encoded as the 8-bit
  * checkpoint from which fp4_act_backward works; both E4M3 in 1x128 blocks
- * along the rows, from one read of h.  a is formed in fp32 and rounded once.
+ * along the rows, from one read of h.  a is formed in fp32 and rounded once
+ * (silu below 2^-119 in magnitude, g under -87, may count as zero).
  *   h        [rows, 2F or F] bf16 (ld), device; F = cols.  SWIGLU: F % 8 == 0.
  *   a_codes, a_scales  codes [rows, Fp] of a, Fp = 128 ceil(F / 128), scales
  *            KMAJOR; both NULL to skip.

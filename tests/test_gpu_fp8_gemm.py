@@ -270,3 +270,20 @@ def test_captured_graph(M, K):
         api.gemm(a0.operand(), b.operand(), M, N, K)
         torch.cuda.synchronize()
         assert torch.equal(d, want[k])
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("M,N,K", [(1000, 2304, 6400), (40, 512, 9000)])
+def test_without_a_workspace(M, N, K, out):
+    """Few output tiles, through the call that has no workspace to share K in
+    (another kernel may serve it then)."""
+    import ctypes
+    lib = api.load_library()
+    a, b = operands(M, N, K, seed=3)
+    oa, ob = a.operand(), b.operand()
+    t = api.OUT_TYPES[out]
+    d = torch.empty((M, N), dtype=out, device=DEV)
+    s = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.fp4_gemm(ctypes.byref(oa), ctypes.byref(ob), M, N, K, ctypes.c_void_p(d.data_ptr()), t, N,
+                        0, s) == 0
+    close(d, *product(a, b))
