@@ -138,6 +138,7 @@ __device__ __forceinline__ void mfma_slice(floatx16 (&acc)[MI][NI], const int8v 
 
 // 16 and 8 bytes at an element's alignment (gfx950 takes them as one access).
 typedef float float4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t uint32_any __attribute__((aligned(1)));
 typedef uint32_t uint2_any __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t uint4_any __attribute__((ext_vector_type(4), aligned(2)));
 
@@ -154,8 +155,20 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
   const int i = lane & 31, h = lane >> 5;
   const int c = (lane % L) * 4;
   const int n = static_cast<int>(min(g.N - col0 - c, int64_t(4)));     // this lane's columns inside D
+  constexpr int R = 32 * L / 64;        // rows of a lane
+  const bool add_f32 = g.accumulate && !g.d_bf16 && n == 4;
 #pragma unroll
   for (int mi = 0; mi < MI; ++mi) {
+    // an fp32 D that is added to: all of its loads at once (6144 x 2048 x 8192
+    // 171 us; one before each sum 180), of D's last row for rows outside
+    float4_any old[R];
+    if (add_f32) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const int64_t row = min(row0 + (k * (64 / L) + lane / L) * MI + mi, g.M - 1);
+        old[k] = *reinterpret_cast<const float4_any*>(static_cast<float*>(g.D) + row * g.ldd + col0 + c);
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       float* d = buf + i * P + (8 * (k >> 2) + 4 * h + (k & 3)) * NI;
@@ -163,8 +176,8 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
       for (int ni = 0; ni < NI; ++ni) d[ni] = acc[mi][ni][k];
     }
     __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-#pragma unroll 4
-    for (int k = 0; k < 32 * L / 64; ++k) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
       const int r = k * (64 / L) + lane / L;
       const int64_t row = row0 + r * MI + mi;
       if (row >= g.M || n <= 0) continue;
@@ -191,7 +204,7 @@ __device__ __forceinline__ void epilogue(const fp4lib::Fp8GemmArgs& g, floatx16 
         float* d = static_cast<float*>(g.D) + row * g.ldd + col0 + c;
         if (n == 4) {
           float4_any o = float4_any{v.x, v.y, v.z, v.w};
-          if (g.accumulate) o += *reinterpret_cast<const float4_any*>(d);
+          if (add_f32) o += old[k];
           *reinterpret_cast<float4_any*>(d) = o;
         } else {
           const float e[3] = {v.x, v.y, v.z};
@@ -379,30 +392,36 @@ __device__ __forceinline__ void read_frag(const Stage<4, 4>& S, Frags& f, int wm
 
 // The tile's code rows: a uniform base and a 32-bit offset per DMA (the host
 // keeps 256 row pitches below 2^31).
+template <int MI>
 struct WideSrc {
-  const uint8_t* base[2];
-  uint32_t off[2][8];
+  const uint8_t *a, *b;
+  uint32_t off_a[2 * MI], off_b[8];
 };
 
-__device__ __forceinline__ void wide_dma(Stage<4, 4>& W, const WideSrc& s, int64_t koff, int wave, int x) {
-  dma16(s.base[x >> 3] + koff + s.off[x >> 3][x & 7],
-        (x < 8 ? W.a : W.b) + wave * 512 + (x & 7) * 64);
+// The x-th of a stage's 2 MI + 8 DMA of a wave.
+template <int MI>
+__device__ __forceinline__ void wide_dma(Stage<MI, 4>& W, const WideSrc<MI>& s, int64_t koff, int wave, int x) {
+  if (x < 2 * MI) dma16(s.a + koff + s.off_a[x], W.a + wave * 128 * MI + x * 64);
+  else dma16(s.b + koff + s.off_b[x - 2 * MI], W.b + wave * 512 + (x - 2 * MI) * 64);
 }
 
 // Where a workgroup of the wide kernels stands: its tile, the wave's part, and
 // what its lanes load.
+template <int MI>
 struct WidePos {
   int64_t m0, n0;
   int lane, wave, wm, wn, i, h;
-  WideSrc src;
-  const uint8_t *psa, *psb;      // scales of this lane's 4 rows at the first block
+  WideSrc<MI> src;
+  const uint8_t *psa, *psb;      // scales of this lane's MI and 4 rows at the first block
+  uint32_t shift;                // MI = 3: of the word at psa
 };
 
-__device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8GemmArgs& g, int id, int kb0) {
-  WidePos w;
+template <int MI>
+__device__ __forceinline__ WidePos<MI> wide_pos(const Params& p, const fp4lib::Fp8GemmArgs& g, int id, int kb0) {
+  WidePos<MI> w;
   int tm, tn;
   tile_coords(p, id, tm, tn);
-  w.m0 = static_cast<int64_t>(tm) * 256;
+  w.m0 = static_cast<int64_t>(tm) * (64 * MI);
   w.n0 = static_cast<int64_t>(tn) * 256;
   w.lane = threadIdx.x & 63;
   // per tile, not once: addresses kept over the tile loop would be spilled
@@ -412,18 +431,27 @@ __device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8Ge
   w.wn = w.wave & 1;
   w.i = w.lane & 31;
   w.h = w.lane >> 5;
-  w.src.base[0] = g.codes[0] + w.m0 * g.ld[0] + static_cast<int64_t>(kb0) * kStepBytes;
-  w.src.base[1] = g.codes[1] + w.n0 * g.ld[1] + static_cast<int64_t>(kb0) * kStepBytes;
-  const uint32_t last[2] = {static_cast<uint32_t>(min(g.M - 1 - w.m0, int64_t(255))),
-                            static_cast<uint32_t>(min(g.N - 1 - w.n0, int64_t(255)))};
+  w.src.a = g.codes[0] + w.m0 * g.ld[0] + static_cast<int64_t>(kb0) * kStepBytes;
+  w.src.b = g.codes[1] + w.n0 * g.ld[1] + static_cast<int64_t>(kb0) * kStepBytes;
+  const uint32_t last_a = static_cast<uint32_t>(min(g.M - 1 - w.m0, int64_t(64 * MI - 1)));
+  const uint32_t last_b = static_cast<uint32_t>(min(g.N - 1 - w.n0, int64_t(255)));
 #pragma unroll
-  for (int x = 0; x < 16; ++x) {
-    const int slot = w.wave * 64 + 8 * (x & 7) + (w.lane >> 3);
-    w.src.off[x >> 3][x & 7] = min(static_cast<uint32_t>(slot_row<4>(slot)), last[x >> 3]) *
-                                   static_cast<uint32_t>(g.ld[x >> 3]) +
-                               16 * ((w.lane & 7) ^ swizzle(slot));
+  for (int x = 0; x < 2 * MI; ++x) {
+    const int slot = w.wave * 16 * MI + 8 * x + (w.lane >> 3);
+    w.src.off_a[x] = min(static_cast<uint32_t>(slot_row<MI>(slot)), last_a) * static_cast<uint32_t>(g.ld[0]) +
+                     16 * ((w.lane & 7) ^ swizzle(slot));
   }
-  w.psa = g.scales[0] + kb0 * g.s_kblk[0] + min(w.m0 + w.wm * 128 + w.i * 4, g.s_kblk[0] - 4);
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    const int slot = w.wave * 64 + 8 * x + (w.lane >> 3);
+    w.src.off_b[x] = min(static_cast<uint32_t>(slot_row<4>(slot)), last_b) * static_cast<uint32_t>(g.ld[1]) +
+                     16 * ((w.lane & 7) ^ swizzle(slot));
+  }
+  // Three rows' scales are the low bytes of the word at their first one, read
+  // from before the end of the block's scales and shifted there.
+  const int64_t ra = w.m0 + w.wm * 32 * MI + w.i * MI, at = min(ra, g.s_kblk[0] - 4);
+  w.shift = static_cast<uint32_t>(min(ra - at, int64_t(3))) * 8;
+  w.psa = g.scales[0] + kb0 * g.s_kblk[0] + at;
   w.psb = g.scales[1] + kb0 * g.s_kblk[1] + min(w.n0 + w.wn * 128 + w.i * 4, g.s_kblk[1] - 4);
   return w;
 }
@@ -435,7 +463,7 @@ __device__ __forceinline__ WidePos wide_pos(const Params& p, const fp4lib::Fp8Ge
 template <int FA, int KS, bool DMA, int X = 0>
 __device__ __forceinline__ void wide_half(floatx16 (&acc)[4][4], const Frags& cur, uint32_t sa,
                                           uint32_t sb, const Stage<4, 4>& R, Frags& nxt,
-                                          Stage<4, 4>& W, int64_t koff, const WidePos& w) {
+                                          Stage<4, 4>& W, int64_t koff, const WidePos<4>& w) {
   if constexpr (X < 16) {
     mfma_one<FA, 4, 4, X / 4, X % 4>(acc, cur.a, cur.b, sa, sb);
     if constexpr (X < 8) read_frag<KS, X>(R, nxt, w.wm, w.wn, w.i, w.h);
@@ -450,7 +478,7 @@ __device__ __forceinline__ void wide_half(floatx16 (&acc)[4][4], const Frags& cu
 // 8 lanes write a row's 128 bytes.  row0, col: this lane's first row and column.
 constexpr int kWidePitch = 72;              // bf16 of a buffer row: 64 and 16 bytes of padding
 __device__ __forceinline__ void wide_store_bf16(const fp4lib::Fp8GemmArgs& g, floatx16 (&acc)[4][4],
-                                                const WidePos& w, int64_t row0, int64_t col,
+                                                const WidePos<4>& w, int64_t row0, int64_t col,
                                                 uint16_t* buf) {
   uint16_t* d = static_cast<uint16_t*>(g.D) + row0 * g.ldd + col;
 #pragma unroll
@@ -485,20 +513,27 @@ __device__ __forceinline__ void wide_store_bf16(const fp4lib::Fp8GemmArgs& g, fl
   }
 }
 
+// The scales of this lane's MI rows of A, `off` bytes on.
+template <int MI>
+__device__ __forceinline__ uint32_t wide_scales_a(const WidePos<MI>& w, int64_t off) {
+  if constexpr (MI == 4) return load_scales<4>(w.psa + off);
+  else return *reinterpret_cast<const uint32_any*>(w.psa + off) >> w.shift;
+}
+
 // The scales of the wave's rows of A and B: of the block that is multiplied,
 // and of the one after it.
 struct WideScales {
   uint32_t a, b, na, nb;
 };
 
-__device__ __forceinline__ WideScales wide_scales(const fp4lib::Fp8GemmArgs& g, const WidePos& w, int nkb) {
+__device__ __forceinline__ WideScales wide_scales(const fp4lib::Fp8GemmArgs& g, const WidePos<4>& w, int nkb) {
   const int k1 = min(1, nkb - 1);
   return WideScales{load_scales<4>(w.psa), load_scales<4>(w.psb), load_scales<4>(w.psa + k1 * g.s_kblk[0]),
                     load_scales<4>(w.psb + k1 * g.s_kblk[1])};
 }
 
 // Blocks 0 and 1 of a tile on their way into the stages.
-__device__ __forceinline__ void wide_begin(Stage<4, 4>& s0, Stage<4, 4>& s1, const WidePos& w, int nkb) {
+__device__ __forceinline__ void wide_begin(Stage<4, 4>& s0, Stage<4, 4>& s1, const WidePos<4>& w, int nkb) {
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int x = 0; x < 16; ++x) wide_dma(s0, w.src, 0, w.wave, x);
@@ -518,7 +553,7 @@ __device__ __forceinline__ void wide_begin(Stage<4, 4>& s0, Stage<4, 4>& s1, con
 template <int FA>
 __device__ __forceinline__ void wide_step(floatx16 (&acc)[4][4], Frags& f0, Frags& f1, WideScales& s,
                                           Stage<4, 4>& C, Stage<4, 4>& Nx, int kb, int nkb,
-                                          const fp4lib::Fp8GemmArgs& g, const WidePos& w) {
+                                          const fp4lib::Fp8GemmArgs& g, const WidePos<4>& w) {
   const int k2 = min(kb + 2, nkb - 1);
   wide_half<FA, 1, false>(acc, f0, s.a, s.b, C, f1, C, 0, w);
   wait_vmcnt<0>();
@@ -532,7 +567,7 @@ __device__ __forceinline__ void wide_step(floatx16 (&acc)[4][4], Frags& f0, Frag
   s.nb = pb;
 }
 
-__device__ __forceinline__ void wide_first_frags(const Stage<4, 4>& s0, Frags& f0, const WidePos& w) {
+__device__ __forceinline__ void wide_first_frags(const Stage<4, 4>& s0, Frags& f0, const WidePos<4>& w) {
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     f0.a[t] = frag<0>(s0.a, w.wm * 128 + t * 32 + w.i, w.h);
@@ -553,7 +588,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide(Params p) {
   __shared__ Stage<4, 4> s0, s1;
   int kb0, nkb;
   const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
-  const WidePos w = wide_pos(p, g, blockIdx.x, kb0);
+  const WidePos<4> w = wide_pos<4>(p, g, blockIdx.x, kb0);
   floatx16 acc[4][4];
   wide_zero(acc);
   if (nkb > 0) {
@@ -584,7 +619,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_loop(Params p) {
   const fp4lib::Fp8GemmArgs& g = p.g;
   const int nkb = static_cast<int>(g.nkb), tiles = p.tiles_m * p.tiles_n;
   int id = blockIdx.x;
-  WidePos w = wide_pos(p, g, id, 0);
+  WidePos<4> w = wide_pos<4>(p, g, id, 0);
   WideScales sc = wide_scales(g, w, nkb);
   wide_begin(s0, s1, w, nkb);
   for (;;) {
@@ -601,7 +636,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_loop(Params p) {
     id += gridDim.x;
     const int64_t row0 = w.m0 + w.wm * 128 + (w.lane >> 3) * 4, col = w.n0 + w.wn * 128 + 8 * (w.lane & 7);
     if (id < tiles) {
-      w = wide_pos(p, g, id, 0);
+      w = wide_pos<4>(p, g, id, 0);
       sc = wide_scales(g, w, nkb);
     }
     wait_vmcnt<0>();
@@ -613,36 +648,39 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_loop(Params p) {
 }
 
 // ------------------------------------------------------ 256 x 256, bf16 ---
-// The product to fp32 for large outputs: the wide tile with its codes widened
+// The product to fp32 for large outputs: the wide tile, of 256 or (where that
+// leaves fewer CUs idle) 192 rows, with its codes widened
 // to bf16 in registers, two converts beside each MFMA.  A step is four
 // quarters of 32 K values; a lane's 16 bytes of each row in a quarter are two
 // products' operands (halves).  While a half is multiplied the next one is
 // widened, from bytes read from LDS a quarter ahead; the barrier stands before
 // the last quarter, whose bytes are then in registers, so the DMA of the
 // stage that it frees has most of a step to land.
+template <int MI>
 struct Raw {
-  uint4 a[4], b[4];
+  uint4 a[MI], b[4];
 };
+template <int MI>
 struct Wide {
-  uint32_t a[4][4], b[4][4];
+  uint32_t a[MI][4], b[4][4];
 };
 
-// Tile t (0..3 B, 4..7 A) of quarter Q.
-template <int Q>
-__device__ __forceinline__ void read_raw(const Stage<4, 4>& S, Raw& r, int t, const WidePos& w) {
+// Tile t (0..3 B, then A) of quarter Q.
+template <int Q, int MI>
+__device__ __forceinline__ void read_raw(const Stage<MI, 4>& S, Raw<MI>& r, int t, const WidePos<MI>& w) {
   const int q = 2 * Q + w.h;
   if (t < 4) {
     const int slot = w.wn * 128 + t * 32 + w.i;
     r.b[t] = S.b[slot * kChunks + (q ^ swizzle(slot))];
   } else {
-    const int slot = w.wm * 128 + (t - 4) * 32 + w.i;
+    const int slot = w.wm * 32 * MI + (t - 4) * 32 + w.i;
     r.a[t - 4] = S.a[slot * kChunks + (q ^ swizzle(slot))];
   }
 }
 
 // Word w (0, 1) of tile t's half HALF as four bf16.
-template <int FA, int HALF>
-__device__ __forceinline__ void widen_word(const Raw& r, Wide& f, int t, int w, const float (&s)[8]) {
+template <int FA, int HALF, int MI>
+__device__ __forceinline__ void widen_word(const Raw<MI>& r, Wide<MI>& f, int t, int w, const float (&s)[4 + MI]) {
   const uint4& c = t < 4 ? r.b[t & 3] : r.a[t & 3];
   const uint32_t x = HALF ? (w ? c.w : c.z) : (w ? c.y : c.x);
   uint32_t* d = t < 4 ? f.b[t & 3] : f.a[t & 3];
@@ -662,54 +700,59 @@ __device__ __forceinline__ bf16x8 as_bf16(const uint32_t (&w)[4]) {
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// One half: 16 MFMAs on `cur`; beside MFMA x the widening of a word of half
-// NHALF of `raw` into `nxt`; if READ, beside the first 8 the bytes of quarter RQ
-// of stage R; if DMA, beside each the x-th DMA of block koff into stage W.
-template <int FA, int NHALF, bool READ, int RQ, bool DMA>
-__device__ __forceinline__ void prec_half(floatx16 (&acc)[4][4], const Wide& cur, Wide& nxt,
-                                          const Raw& raw, const float (&s)[8], const Stage<4, 4>& R,
-                                          Raw& rnext, Stage<4, 4>& W, int64_t koff, const WidePos& w) {
+// One half: 4 MI MFMAs on `cur`; beside MFMA x the widening of word x of half
+// NHALF of `raw` into `nxt`; if READ, beside the first ones the bytes of quarter RQ
+// of stage R; if DMA, beside each the x-th DMA of block koff into stage W.  (MI =
+// 3: two words and DMA are left for the first two.)
+template <int FA, int NHALF, bool READ, int RQ, bool DMA, int MI>
+__device__ __forceinline__ void prec_half(floatx16 (&acc)[MI][4], const Wide<MI>& cur, Wide<MI>& nxt,
+                                          const Raw<MI>& raw, const float (&s)[4 + MI], const Stage<MI, 4>& R,
+                                          Raw<MI>& rnext, Stage<MI, 4>& W, int64_t koff, const WidePos<MI>& w) {
+  constexpr int kMfma = 4 * MI, kWords = 2 * (4 + MI);
 #pragma unroll
-  for (int x = 0; x < 16; ++x) {
+  for (int x = 0; x < kMfma; ++x) {
     acc[x / 4][x % 4] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16(cur.b[x % 4]), as_bf16(cur.a[x / 4]),
                                                                 acc[x / 4][x % 4], 0, 0, 0);
-    widen_word<FA, NHALF>(raw, nxt, x >> 1, x & 1, s);
-    if constexpr (READ) {
-      if (x < 8) read_raw<RQ>(R, rnext, x, w);
+#pragma unroll
+    for (int y = x; y < kWords; y += kMfma) {
+      widen_word<FA, NHALF>(raw, nxt, y >> 1, y & 1, s);
+      if constexpr (DMA) wide_dma(W, w.src, koff, w.wave, y);
     }
-    if constexpr (DMA) wide_dma(W, w.src, koff, w.wave, x);
+    if constexpr (READ) {
+      if (x < 4 + MI) read_raw<RQ>(R, rnext, x, w);
+    }
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-template <int FA>
+// MI = 4: 256 x 256 tiles; 3: 192 x 256.
+template <int FA, int MI>
 __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_f32(Params p) {
-  __shared__ Stage<4, 4> s0, s1;
+  __shared__ Stage<MI, 4> s0, s1;
   int kb0, nkb;
   const fp4lib::Fp8GemmArgs g = split_args(p.g, kb0, nkb);
-  const WidePos w = wide_pos(p, g, blockIdx.x, kb0);
+  const WidePos<MI> w = wide_pos<MI>(p, g, blockIdx.x, kb0);
 
-  floatx16 acc[4][4];
+  floatx16 acc[MI][4];
 #pragma unroll
-  for (int mi = 0; mi < 4; ++mi)
+  for (int mi = 0; mi < MI; ++mi)
 #pragma unroll
     for (int ni = 0; ni < 4; ++ni) acc[mi][ni] = floatx16{};
 
-  Raw r0, r1;
-  Wide f0, f1;
-  float s[8];                 // block scales of B's and A's four tiles
+  Raw<MI> r0, r1;
+  Wide<MI> f0, f1;
+  float s[4 + MI];            // block scales of B's and A's tiles
   auto set_scales = [&](uint32_t wa, uint32_t wb) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      s[t] = scale_of(wb, t);
-      s[4 + t] = scale_of(wa, t);
-    }
+    for (int t = 0; t < 4; ++t) s[t] = scale_of(wb, t);
+#pragma unroll
+    for (int t = 0; t < MI; ++t) s[4 + t] = scale_of(wa, t);
   };
   // Step kb on stage C: the bytes of its quarter 0 and its first half widened
   // are in registers, with its scales; then as in k_gemm_fp8_wide.
-  auto step = [&](Stage<4, 4>& C, Stage<4, 4>& Nx, int kb) {
+  auto step = [&](Stage<MI, 4>& C, Stage<MI, 4>& Nx, int kb) {
     const int k1 = min(kb + 1, nkb - 1), k2 = min(kb + 2, nkb - 1);
-    const uint32_t na = load_scales<4>(w.psa + k1 * g.s_kblk[0]);
+    const uint32_t na = wide_scales_a(w, k1 * g.s_kblk[0]);
     const uint32_t nb = load_scales<4>(w.psb + k1 * g.s_kblk[1]);
     const int64_t koff = static_cast<int64_t>(k2) * kStepBytes;
     prec_half<FA, 1, true, 1, false>(acc, f0, f1, r0, s, C, r1, C, 0, w);
@@ -726,16 +769,16 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_f32(Params p) {
   };
   if (nkb > 0) {
 #pragma unroll
-    for (int x = 0; x < 16; ++x) wide_dma(s0, w.src, 0, w.wave, x);
-    set_scales(load_scales<4>(w.psa), load_scales<4>(w.psb));
+    for (int x = 0; x < 2 * MI + 8; ++x) wide_dma(s0, w.src, 0, w.wave, x);
+    set_scales(wide_scales_a(w, 0), load_scales<4>(w.psb));
     wait_vmcnt<0>();
     ring_barrier();
 #pragma unroll
-    for (int x = 0; x < 16; ++x) wide_dma(s1, w.src, nkb > 1 ? kStepBytes : 0, w.wave, x);
+    for (int x = 0; x < 2 * MI + 8; ++x) wide_dma(s1, w.src, nkb > 1 ? kStepBytes : 0, w.wave, x);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) read_raw<0>(s0, r0, t, w);
+    for (int t = 0; t < 4 + MI; ++t) read_raw<0>(s0, r0, t, w);
 #pragma unroll
-    for (int t = 0; t < 16; ++t) widen_word<FA, 0>(r0, f0, t >> 1, t & 1, s);
+    for (int t = 0; t < 2 * (4 + MI); ++t) widen_word<FA, 0>(r0, f0, t >> 1, t & 1, s);
     for (int kb = 0; kb < nkb; kb += 2) {
       step(s0, s1, kb);
       step(s1, s0, kb + 1);
@@ -745,7 +788,8 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_f32(Params p) {
   ring_barrier();
   constexpr int kBuf = 32 * (32 * 4 + 4);
   float* buf = reinterpret_cast<float*>(w.wave < 2 ? &s0 : &s1) + (w.wave & 1) * kBuf;
-  epilogue<4, 4>(g, acc, w.m0 + w.wm * 128, w.n0 + w.wn * 128, w.lane, buf);
+  static_assert(2 * kBuf * sizeof(float) <= sizeof(s0), "two epilogue buffers per stage");
+  epilogue<MI, 4>(g, acc, w.m0 + w.wm * 32 * MI, w.n0 + w.wn * 128, w.lane, buf);
 }
 
 template <typename K>
@@ -801,21 +845,24 @@ __global__ __launch_bounds__(256) void k_gemm_fp8_join(fp4lib::Fp8GemmArgs g) {
 }
 
 // How a product runs: the kernel, and the workgroups that share a tile's K.
-enum Kind { kRows, kTile64, kTile128, kTile256 };
+enum Kind { kRows, kTile64, kTile128, kTile192, kTile256 };
 struct Plan {
   Kind kind;
   int splits;
 };
 
 // The kernel and split (if the caller has a workspace: share) with the least
-// estimated time.  A workgroup takes, per
-// K block, t1 us alone on its CU and t2 us beside another (256 x 256 tiles:
-// always alone); a kernel has a fixed part; joining writes and reads the fp32
-// sums.  The constants are fits of measured times on 256 CUs: bf16 (fp32) D,
-// M = 256, N = 4096, K = 21504: 64-row tiles shared by 4 48 (59) us, 128-row tiles by
-// 8 44 (56) us, unshared 78 (175); M = 1000, N = 4608, K = 12288: 256-row tiles by
-// 3 68 (108) us, unshared 101, 128-row 91 (140); M = 2048, N = K = 4096: 128-row 37
-// (61), 256-row 41 (82); M = 1024, N = 12288, K = 4608: 256-row 51 (96), 128-row 64 (103).
+// estimated time.  A workgroup takes t1 us per K block while at most half of the
+// chip's places for such workgroups are taken, and up to t2 when all are (two
+// workgroups share a CU; the clock falls with the power drawn); a round of
+// workgroups has a fixed part (the persistent bf16 kernel once); joining reads
+// the fp32 sums that the parts wrote.  The constants are fits of times on 256 CUs,
+// measured / estimated in us, bf16 D: M = N = K = 4096: 256-row tiles 55 / 56,
+// 128-row 78 / 72; M = 2048: 128-row 37 / 36, 256-row 41 / 42; M = 1000, N = 4608,
+// K = 12288: 256-row tiles by 3 67 / 64, 128-row unshared 91 / 70.  fp32 D: M =
+// 6144, N = 2048, K = 8192: 192-row 164 / 164, 256-row 167 / 171, 128-row 210 / 205; M
+// = 8192, N = K = 4096: 256-row 200 / 208, 128-row 239 / 246, 192-row 249 / 246; M =
+// N = 2048, K = 8192: 128-row 68 / 71, 192-row 128 / 126.
 //
 // Up to 16 rows of A: the kernel of gemm_fp8_rows.hip where 64 x 128 tiles would
 // leave half the CUs idle (M = 1: N = 6144, K = 2048 6.4 against 8.3 us; N = 4096,
@@ -827,25 +874,31 @@ Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
   if (g.M <= kMaxRows && tiles(64, 128) * 2 < cus) return {kRows, 1};
   struct Cost {
     Kind kind;
-    int bm, bn, per_cu;
+    int bf16, bm, bn, per_cu;
     double t1, t2, fixed;
   };
-  static constexpr Cost kCosts[2][3] = {
-      {{kTile64, 64, 128, 2, 0.65, 1.15, 4}, {kTile128, 128, 128, 2, 1.05, 1.8, 4}, {kTile256, 256, 256, 1, 2.4, 2.4, 8}},
-      {{kTile64, 64, 128, 2, 0.43, 0.88, 4}, {kTile128, 128, 128, 2, 0.62, 1.0, 4}, {kTile256, 256, 256, 1, 1.1, 1.1, 8}}};
+  static constexpr Cost kCosts[] = {
+      {kTile64, 0, 64, 128, 2, 0.65, 1.15, 4},   {kTile128, 0, 128, 128, 2, 1.05, 1.8, 4},
+      {kTile192, 0, 192, 256, 1, 1.85, 2.44, 8}, {kTile256, 0, 256, 256, 1, 2.1, 3.0, 8},
+      {kTile64, 1, 64, 128, 2, 0.43, 0.88, 4},   {kTile128, 1, 128, 128, 2, 0.62, 1.0, 4},
+      {kTile256, 1, 256, 256, 1, 1.05, 1.5, 8}};
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   Plan best{kTile64, 1};
   double least = 0.0;
-  for (const Cost& c : kCosts[g.d_bf16 ? 1 : 0]) {
-    // 32-bit offsets within a 256-row tile, and no tail test for K = 0
-    if (c.kind == kTile256 && (g.nkb == 0 || g.ld[0] >= (1 << 23) || g.ld[1] >= (1 << 23))) continue;
+  for (const Cost& c : kCosts) {
+    if (c.bf16 != (g.d_bf16 != 0)) continue;
+    // 32-bit offsets within a tile's 256 rows, and no tail test for K = 0
+    if (c.bn == 256 && (g.nkb == 0 || g.ld[0] >= (1 << 23) || g.ld[1] >= (1 << 23))) continue;
     for (int splits : kSplits) {
       if (splits > 1 && (!share || g.nkb < 4 * splits)) break;
-      const int64_t n = tiles(c.bm, c.bn) * splits, slots = c.per_cu * cus, rest = n % slots;
+      const int64_t n = tiles(c.bm, c.bn) * splits, slots = c.per_cu * cus, whole = n / slots, rest = n % slots;
+      const double full = static_cast<double>(rest) / static_cast<double>(slots);
+      const double last = rest == 0 ? 0.0 : c.t1 + (c.t2 - c.t1) * std::max(0.0, 2.0 * full - 1.0);
       const double blocks = static_cast<double>((g.nkb + splits - 1) / splits);
-      const double rounds = static_cast<double>(n / slots) * c.t2 + (rest == 0 ? 0.0 : rest <= cus ? c.t1 : c.t2);
-      const double join = splits > 1 ? 3.0 + splits * static_cast<double>(g.M) * g.N * 8.0 / 4.5e6 : 0.0;
-      const double t = rounds * blocks + c.fixed + join;
+      const bool once = c.kind == kTile256 && c.bf16 && splits == 1;
+      const double starts = once ? 1.0 : static_cast<double>(whole + (rest != 0));
+      const double join = splits > 1 ? 3.0 + (4 * splits + (c.bf16 ? 2 : 4)) * static_cast<double>(g.M) * g.N / 6.5e6 : 0.0;
+      const double t = (static_cast<double>(whole) * c.t2 + last) * blocks + starts * c.fixed + join;
       if (least == 0.0 || t < least) {
         least = t;
         best = {c.kind, splits};
@@ -870,8 +923,11 @@ void run(const fp4lib::Fp8GemmArgs& g, Kind kind, hipStream_t s) {
       if (g.d_bf16) launch_kernel(k_gemm_fp8<FA, false, 2, 2, 2>, g, 128, 128, s);
       else launch_kernel(k_gemm_fp8<FA, true, 2, 2, 2>, g, 128, 128, s);
       break;
+    case kTile192:
+      launch_kernel(k_gemm_fp8_wide_f32<FA, 3>, g, 192, 256, s);
+      break;
     case kTile256:
-      if (!g.d_bf16) launch_kernel(k_gemm_fp8_wide_f32<FA>, g, 256, 256, s);
+      if (!g.d_bf16) launch_kernel(k_gemm_fp8_wide_f32<FA, 4>, g, 256, 256, s);
       else if (!g.accumulate && g.splits == 1)
         launch_kernel(k_gemm_fp8_wide_loop<FA>, g, 256, 256, s, cus);
       else launch_kernel(k_gemm_fp8_wide<FA>, g, 256, 256, s);

@@ -287,3 +287,15 @@ def test_without_a_workspace(M, N, K, out):
     assert lib.fp4_gemm(ctypes.byref(oa), ctypes.byref(ob), M, N, K, ctypes.c_void_p(d.data_ptr()), t, N,
                         0, s) == 0
     close(d, *product(a, b))
+
+
+@pytest.mark.parametrize("fa", ["fp8", "fp8_e5m2"])
+@pytest.mark.parametrize("M,N,K", [(6100, 2010, 300), (5953, 1793, 129), (4100, 3000, 640), (8000, 4010, 300)])
+def test_fp32_by_large_tiles(M, N, K, fa):
+    """Enough outputs for 192 and 256 rows a tile; last tiles of every length
+    around the scales' words."""
+    a, b = operands(M, N, K, fa)
+    d = torch.full((M, N), 0.5, device=DEV)
+    api.gemm(a.operand(), b.operand(), M, N, K, out=d, accumulate=True)
+    ref, bound, cut = product(a, b)
+    close(d, ref + 0.5, bound + 0.5, cut)
