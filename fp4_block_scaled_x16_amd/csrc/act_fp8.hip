@@ -28,6 +28,13 @@ __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.0f + t);      // t = inf: 0
 }
 
+// The same bits, of which the compiler knows nothing (it would keep what it
+// has unpacked from them).
+__device__ __forceinline__ uint4 reread(uint4 q) {
+  asm volatile("" : "+v"(q.x), "+v"(q.y), "+v"(q.z), "+v"(q.w));
+  return q;
+}
+
 template <bool GLU>
 __global__ __launch_bounds__(kTileThreads, 4) void k_act_fp8(fp4lib::Fp8ActArgs a) {
   const int64_t tiles_c = (a.cols + kTile - 1) / kTile;
@@ -36,32 +43,28 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_act_fp8(fp4lib::Fp8ActArgs 
   uint32_t unused = 0;
   for (int64_t id = blockIdx.x; id < n; id += gridDim.x) {
     const TilePos t = tile_pos(id, tiles_c);
-    float g[4][8], u[4][8], v[4][8];
-    {
-      uint4 q[4], w[4];
+    // h stays as it was read, and is unpacked again for its own codes: with three
+    // fp32 tiles in 128 registers it spills (8192 x 6144: 71.3 us, 72; three
+    // workgroups per CU in 80 registers: 101)
+    uint4 q[4], w[4];
+    load_tile(q, a.h, t, a.rows, a.cols, a.ld);
+    if constexpr (GLU) load_tile(w, a.h + a.cols, t, a.rows, a.cols, a.ld);
+    float v[4][8];
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        q[p] = load_bf16x8(a.h, t.row(p), a.rows, t.col(), a.cols, a.ld);
-        if constexpr (GLU)
-          w[p] = load_bf16x8(a.h + a.cols, t.row(p), a.rows, t.col(), a.cols, a.ld);
-      }
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        unpack8(q[p], g[p]);
-        if constexpr (GLU) unpack8(w[p], u[p]);
-      }
-    }
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
+    for (int p = 0; p < 4; ++p) {
+      float g[8], u[8];
+      unpack8(q[p], g);
+      if constexpr (GLU) unpack8(w[p], u);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         if constexpr (GLU) {
-          v[p][i] = g[p][i] * sigmoid(g[p][i]) * u[p][i];
+          v[p][i] = g[i] * sigmoid(g[i]) * u[i];
         } else {
-          const float r = g[p][i] < 0.0f ? 0.0f : g[p][i];     // keeps a NaN
+          const float r = g[i] < 0.0f ? 0.0f : g[i];     // keeps a NaN
           v[p][i] = r * r;
         }
       }
+    }
     uint32_t sc[4];
     const int64_t kb = t.c0 / kTile;
     if (a.a_codes) {
@@ -74,11 +77,15 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_act_fp8(fp4lib::Fp8ActArgs 
     }
     if (a.h_codes) {
       const int64_t hp = GLU ? 2 * fp : fp;
-      row_scales<false>(g, sc);
-      store_rows<false, false>(t, g, sc, a.rows, hp, t.col(), kb, a.h_codes, a.h_scales, unused);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) unpack8(reread(q[p]), v[p]);
+      row_scales<false>(v, sc);
+      store_rows<false, false>(t, v, sc, a.rows, hp, t.col(), kb, a.h_codes, a.h_scales, unused);
       if constexpr (GLU) {
-        row_scales<false>(u, sc);
-        store_rows<false, false>(t, u, sc, a.rows, hp, fp + t.col(), fp / kTile + kb, a.h_codes,
+#pragma unroll
+        for (int p = 0; p < 4; ++p) unpack8(reread(w[p]), v[p]);
+        row_scales<false>(v, sc);
+        store_rows<false, false>(t, v, sc, a.rows, hp, fp + t.col(), fp / kTile + kb, a.h_codes,
                                  a.h_scales, unused);
       }
     }
@@ -95,8 +102,7 @@ template <bool GLU>
 __device__ __forceinline__ GradInput<GLU> load_grad(const fp4lib::Fp8ActGradArgs& a, const TilePos& t) {
   const int64_t fp = up128(a.cols), hp = (GLU ? 2 : 1) * fp, kb = t.c0 / kTile;
   GradInput<GLU> in;
-#pragma unroll
-  for (int p = 0; p < 4; ++p) in.da[p] = load_bf16x8(a.da, t.row(p), a.rows, t.col(), a.cols, a.ld);
+  load_tile(in.da, a.da, t, a.rows, a.cols, a.ld);
   in.h[0] = load_raw(t, a.h_codes, a.h_scales, a.rows, hp, t.col(), kb);
   if constexpr (GLU) in.h[1] = load_raw(t, a.h_codes, a.h_scales, a.rows, hp, fp + t.col(), fp / kTile + kb);
   return in;
@@ -106,10 +112,10 @@ __device__ __forceinline__ GradInput<GLU> load_grad(const fp4lib::Fp8ActGradArgs
 //
 // SwiGLU to codes holds three fp32 tiles, 96 registers a thread and as many
 // again around them: one workgroup fits on a CU, so it loops over tiles and
-// loads the next one's input before it computes (8192 x 6144: 102 us, 4.5 TB/s;
+// loads the next one's input before it computes (8192 x 6144: 95 us, 4.8 TB/s;
 // two workgroups of 128 registers spill: 217 us).  The others fit twice, and
-// overlap each other better than a loop does (squared ReLU, 8192 x 21504: 219
-// us, 4.8 TB/s; 241 with the loop).
+// overlap each other better than a loop does (squared ReLU, 8192 x 21504: 216
+// us, 4.9 TB/s; the loop took a tenth more).
 template <bool GLU, bool VALUES>
 constexpr bool kGradLoop = GLU && !VALUES;
 
@@ -138,14 +144,14 @@ __global__ __launch_bounds__(kTileThreads, (kGradLoop<GLU, VALUES> ? 2 : 4)) voi
         float da[8];
         unpack8(in.da[p], da);
 #pragma unroll
-        for (int h = 0; h < H; ++h) raw_values<false>(in.h[h], p, t.row(p) < a.rows, d[h][p]);
+        for (int h = 0; h < H; ++h) raw_values<false>(in.h[h], p, d[h][p]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float g = d[0][p][i];
           if constexpr (GLU) {
             const float u = d[1][p][i], s = sigmoid(g), silu = g * s;
             v[p][i] = silu * u;
-            d[0][p][i] = da[i] * u * (s * (1.0f + g * (1.0f - s)));
+            d[0][p][i] = da[i] * u * __builtin_fmaf(silu, 1.0f - s, s);
             d[1][p][i] = da[i] * silu;
           } else {
             const float r = g < 0.0f ? 0.0f : g;

@@ -45,7 +45,8 @@ __device__ __forceinline__ float code_scale(uint32_t code) { return __uint_as_fl
 // their scale exactly.
 template <bool E5>
 __device__ __forceinline__ uint32_t pack4(float y0, float y1, float y2, float y3, float scale) {
-  fp4dev::s16x2 w = {0, 0};
+  fp4dev::s16x2 w;
+  w = __builtin_nondeterministic_value(w);       // both halves are written
   if constexpr (E5) {
     w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, y0, y1, scale, false);
     w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, y2, y3, scale, true);
@@ -100,11 +101,13 @@ struct TilePos {
   __device__ __forceinline__ int64_t col() const { return c0 + 8 * l; }
 };
 
+// (Tiles are fewer than 2^31: each holds a 128-byte run at least, and only a
+// matrix of one tile row or column as little.)
 __device__ __forceinline__ TilePos tile_pos(int64_t id, int64_t tiles_c) {
   TilePos t;
-  const int64_t tr = id / tiles_c;
-  t.r0 = tr * kTile;
-  t.c0 = (id - tr * tiles_c) * kTile;
+  const uint32_t i = static_cast<uint32_t>(id), n = static_cast<uint32_t>(tiles_c), tr = i / n;
+  t.r0 = static_cast<int64_t>(tr) * kTile;
+  t.c0 = static_cast<int64_t>(i - tr * n) * kTile;
   t.l = threadIdx.x & 15;
   t.tr = threadIdx.x >> 4;
   return t;
@@ -128,6 +131,18 @@ __device__ __forceinline__ uint4 load_bf16x8(const uint16_t* __restrict__ x, int
     }
   }
   return q;
+}
+
+// The thread's part of a bf16 tile; a tile inside the matrix without tests.
+__device__ __forceinline__ void load_tile(uint4 (&q)[4], const uint16_t* __restrict__ x, const TilePos& t,
+                                          int64_t rows, int64_t cols, int64_t ld) {
+  if (t.r0 + kTile <= rows && t.c0 + kTile <= cols) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) q[p] = *reinterpret_cast<const uint4*>(x + t.row(p) * ld + t.col());
+  } else {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) q[p] = load_bf16x8(x, t.row(p), rows, t.col(), cols, ld);
+  }
 }
 
 // 8 values as bf16 into row r, columns c ..; a partial group element by
@@ -192,18 +207,28 @@ __device__ __forceinline__ RawCodes load_raw(const TilePos& t, const uint8_t* __
                                              const uint8_t* __restrict__ scales, int64_t rows,
                                              int64_t pitch, int64_t col, int64_t kb) {
   const int64_t rp = up16(rows);
-  RawCodes r = {};
+  const uint8_t *c = codes + t.row(0) * pitch + col, *s = scales + kb * rp + t.row(0);
+  RawCodes r;
+  if (t.r0 + kTile <= rows) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p)
-    if (t.row(p) < rows) r.q[p] = *reinterpret_cast<const uint2*>(codes + t.row(p) * pitch + col);
-  if (t.row(0) < rp) r.scales = *reinterpret_cast<const uint32_t*>(scales + kb * rp + t.row(0));
+    for (int p = 0; p < 4; ++p) r.q[p] = *reinterpret_cast<const uint2*>(c + p * pitch);
+    r.scales = *reinterpret_cast<const uint32_t*>(s);
+  } else {
+    // rows outside: zero codes and, their own being of any value, zero scales
+    const int64_t n = rows - t.row(0);
+    r = {};
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      if (p < n) r.q[p] = *reinterpret_cast<const uint2*>(c + p * pitch);
+    if (n > 0) r.scales = *reinterpret_cast<const uint32_t*>(s) & (n < 4 ? (1u << (8 * n)) - 1u : ~0u);
+  }
   return r;
 }
 
-// Row p's values.  Rows outside have zero codes, and scales of any value.
+// Row p's values.
 template <bool E5>
-__device__ __forceinline__ void raw_values(const RawCodes& r, int p, bool inside, float (&v)[8]) {
-  const float s = code_scale(inside ? (r.scales >> (8 * p)) & 0xFFu : 0u);
+__device__ __forceinline__ void raw_values(const RawCodes& r, int p, float (&v)[8]) {
+  const float s = code_scale((r.scales >> (8 * p)) & 0xFFu);
   unpack4<E5>(r.q[p].x, v, s);
   unpack4<E5>(r.q[p].y, v + 4, s);
 }

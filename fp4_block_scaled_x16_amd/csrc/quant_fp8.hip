@@ -33,8 +33,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_quant_fp8(fp4lib::Fp8QuantA
     float v[4][8];
     {
       uint4 q[4];
-#pragma unroll
-      for (int p = 0; p < 4; ++p) q[p] = load_bf16x8(a.x, t.row(p), a.rows, t.col(), a.cols, a.ld);
+      load_tile(q, a.x, t, a.rows, a.cols, a.ld);
 #pragma unroll
       for (int p = 0; p < 4; ++p) unpack8(q[p], v[p]);
     }
@@ -99,7 +98,7 @@ __global__ __launch_bounds__(kTileThreads, 4) void k_requant_t_fp8(
     float v[4][8];
     const RawCodes raw = load_raw(t, codes, scales, rows, up128(cols), t.col(), t.c0 / kTile);
 #pragma unroll
-    for (int p = 0; p < 4; ++p) raw_values<E5>(raw, p, t.row(p) < rows, v[p]);
+    for (int p = 0; p < 4; ++p) raw_values<E5>(raw, p, v[p]);
     col_partial(t, v, cmax);
     __syncthreads();
     col_codes<E5>(cmax, code, 0);
