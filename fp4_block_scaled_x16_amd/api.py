@@ -161,9 +161,7 @@ def _addr(t):
 
 
 def _as_bf16_bits(x):
-    if x.dtype == torch.bfloat16:
-        x = x.view(torch.int16)
-    if x.dtype not in (torch.int16, torch.uint16):
+    if x.dtype not in (torch.bfloat16, torch.int16, torch.uint16):
         raise TypeError("x must be bfloat16 (or its int16 bit view)")
     if x.dim() != 2 or x.stride(1) != 1:
         raise ValueError("x must be a 2-D row-major tensor")
@@ -383,13 +381,16 @@ def _up(v, to):
     return -(-v // to) * to
 
 
-def _fp8_buffers(fmt, rows, cols, device, block=BLOCK_1D):
-    """An FP8 code matrix [rows, cols] whose contents a kernel writes."""
-    kb = -(-cols // 128)
-    codes = torch.empty((rows, 128 * kb), dtype=torch.uint8, device=device)
-    scales = torch.empty((kb, _up(rows, 16)), dtype=torch.uint8, device=device)
-    return Quantized(fmt, block, rows, cols, codes, scales, None, None,
-                     scale_layout=SCALES_KMAJOR)
+def _fp8_buffers(fmt, rows, cols, near, block=BLOCK_1D):
+    """An FP8 code matrix [rows, cols] whose contents a kernel writes, on the
+    device of `near` (new_empty of a uint8 tensor is the cheapest allocation)."""
+    kb = (cols + 127) >> 7
+    if near.dtype is torch.uint8:
+        codes = near.new_empty(rows, kb << 7)
+    else:
+        codes = near.new_empty((rows, kb << 7), dtype=torch.uint8)
+    scales = codes.new_empty(kb, (rows + 15) & -16)
+    return Quantized(fmt, block, rows, cols, codes, scales, None, None, None, SCALES_KMAJOR)
 
 
 def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpose, counters,
@@ -405,8 +406,8 @@ def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpo
                                  or counters.shape != (5,) or not counters.is_contiguous()):
         raise ValueError("counters must be an int64 [5] tensor on x's device (new_counters)")
     blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
-    q = [_fp8_buffers(f, R, C, x.device, blk)] if row else []
-    q += [_fp8_buffers(f, C, R, x.device, blk)] if col else []
+    q = [_fp8_buffers(f, R, C, x, blk)] if row else []
+    q += [_fp8_buffers(f, C, R, q[0].codes if q else x, blk)] if col else []
     d = [ctypes.byref(_fp8_desc(f, blk, o, SR if rnd == "sr" else RNE, bool(rht),
                                 amax_in is not None, bool(emit_transpose), int(scale_layout),
                                 GLOBAL_SCOPES[global_scope], COUNT_LEVELS[count]))
@@ -462,7 +463,7 @@ def requantize_t(q: Quantized):
     was kept as its 8-bit Fprop operand alone.  Exact but for elements below the
     normal range of their new block."""
     _fp8_only(q, "requantize_t")
-    t = _fp8_buffers(q.fmt, q.cols, q.rows, q.codes.device)
+    t = _fp8_buffers(q.fmt, q.cols, q.rows, q.codes)
     _launch("fp4_requantize_t", load_library().fp4_requantize_t, q.codes.device, q.fmt,
             q.codes.data_ptr(), q.scales.data_ptr(), q.rows, q.cols, t.codes.data_ptr(),
             t.scales.data_ptr())
@@ -514,9 +515,10 @@ def act_quantize(h, act="swiglu", a="fp8", checkpoint=True):
             raise ValueError("h must be [tokens, 2F] for 'swiglu'")
         cols //= 2
     dev = h.device
-    qa = _fp8_buffers(FP8_E4M3, rows, cols, dev) if a == "fp8" else None
+    qa = _fp8_buffers(FP8_E4M3, rows, cols, h) if a == "fp8" else None
     av = _bf16_rows(rows, cols, dev) if a == "bf16" else None
-    qh = _fp8_buffers(FP8_E4M3, rows, _checkpoint_cols(act, cols), dev) if checkpoint else None
+    qh = (_fp8_buffers(FP8_E4M3, rows, _checkpoint_cols(act, cols), qa.codes if qa else h)
+          if checkpoint else None)
     _launch("fp4_act_quantize", load_library().fp4_act_quantize, dev, ACTS[act], h.data_ptr(), rows,
             cols, _ld(h), qa and qa.codes.data_ptr(), qa and qa.scales.data_ptr(), _addr(av),
             0 if av is None else _ld(av), qh and qh.codes.data_ptr(), qh and qh.scales.data_ptr())
@@ -550,14 +552,15 @@ def act_backward(qh: Quantized, da, act="swiglu", fmt="fp8", out="fp8"):
     o = [None] * 6
     dh = av = None
     if out == "fp8":
-        q = (_fp8_buffers(f, rows, qh.cols, dev), _fp8_buffers(f, halves * cols, rows, dev),
-             _fp8_buffers(FP8_E4M3, cols, rows, dev))
-        o = [t for p in q for t in (p.codes, p.scales)]
+        near = qh.codes
+        q = (_fp8_buffers(f, rows, qh.cols, near), _fp8_buffers(f, halves * cols, rows, near),
+             _fp8_buffers(FP8_E4M3, cols, rows, near))
+        o = [t.data_ptr() for p in q for t in (p.codes, p.scales)]
     else:
         dh, av = _bf16_rows(rows, halves * cols, dev), _bf16_rows(rows, cols, dev)
     _launch("fp4_act_backward", load_library().fp4_act_backward, dev, ACTS[act],
             qh.codes.data_ptr(), qh.scales.data_ptr(), da.data_ptr(), rows, cols, _ld(da), f,
-            *[_addr(t) for t in o], _addr(dh), 0 if dh is None else _ld(dh), _addr(av),
+            *o, _addr(dh), 0 if dh is None else _ld(dh), _addr(av),
             0 if av is None else _ld(av))
     return q if out == "fp8" else (dh, av)
 
