@@ -28,7 +28,7 @@ from __future__ import annotations
 import torch
 
 from . import api
-from .linear import QuantizedLinear, Recipe, grad_alias
+from .linear import Kept, QuantizedLinear, Recipe, grad_alias
 
 
 class QuantizedFFN:
@@ -57,13 +57,14 @@ class QuantizedFFN:
         return _FfnFunction.apply(x, grad_alias(self.up.weight), grad_alias(self.down.weight), self)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
-        y, self._saved = self._forward(x)
+        y, saved = self._forward(x)
+        self._saved = Kept(saved, x.device)
         return y
 
     def backward(self, dy: torch.Tensor) -> torch.Tensor:
         if self._saved is None:
             raise RuntimeError("backward() needs a preceding forward()")
-        saved, self._saved = self._saved, None
+        saved, self._saved = self._saved.take(), None
         return self._backward(dy, saved)
 
     def _forward(self, x):

@@ -74,6 +74,35 @@ def grad_alias(weight):
     return weight.detach().requires_grad_(weight.requires_grad)
 
 
+class Kept:
+    """What a forward step keeps for its backward step.  A backward step on
+    another stream tells the allocator so: the tensors' memory belongs to the
+    stream of the forward step, and is let go while the other one may still be
+    reading."""
+
+    def __init__(self, saved, device):
+        self.saved, self.device = saved, device
+        self.stream = torch.cuda.current_stream(device)
+
+    def take(self):
+        now = torch.cuda.current_stream(self.device)
+        if now != self.stream:
+            _record(self.saved, now)
+        return self.saved
+
+
+def _record(saved, stream):
+    if isinstance(saved, torch.Tensor):
+        saved.record_stream(stream)
+    elif isinstance(saved, api.Quantized):
+        _record((saved.codes, saved.scales, saved.s_dec, saved.amax, saved.codes_t), stream)
+    elif isinstance(saved, api.Operand):
+        _record(saved._owner, stream)
+    elif isinstance(saved, tuple):
+        for s in saved:
+            _record(s, stream)
+
+
 @dataclass
 class Recipe:
     fmt: str = "nvfp4"            # "nvfp4", "ue5m3", "mxfp4" or "fp8"
@@ -174,14 +203,15 @@ class QuantizedLinear:
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         """Fprop of one step; the operands Dgrad / Wgrad need are kept for
         the next `backward`."""
-        y, self._saved = self._forward(x)
+        y, saved = self._forward(x)
+        self._saved = Kept(saved, x.device)
         return y
 
     def backward(self, dy: torch.Tensor) -> torch.Tensor:
         """Dgrad (returned) and Wgrad (added to main_grad) of the last forward."""
         if self._saved is None:
             raise RuntimeError("backward() needs a preceding forward()")
-        saved, self._saved = self._saved, None
+        saved, self._saved = self._saved.take(), None
         return self._backward(dy, saved)
 
     def _forward(self, x):

@@ -223,3 +223,32 @@ def test_no_tokens(act):
     assert layer.forward(x).shape == (0, 64)
     assert layer.backward(torch.empty((0, 64), dtype=BF, device=DEV)).shape == (0, 128)
     assert not layer.up.main_grad.any() and not layer.down.main_grad.any()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "nvfp4"])
+def test_backward_on_another_stream(fmt):
+    """The forward pass on one stream, the backward pass on another that waits
+    for it, and the first stream filling new memory meanwhile: what the step
+    kept is not handed out while it is read."""
+    T, D, F = 2048, 512, 512
+    up, down = rand(2 * F, D, 1, 0.05), rand(D, F, 2, 0.05)
+    x, dy = rand(T, D, 3), rand(T, D, 4, 1e-2)
+    r = Recipe(fmt=fmt, out_dtype="bf16")
+    one = QuantizedFFN(up, down, "swiglu", r)
+    one.forward(x)
+    want = one.backward(dy), one.up.main_grad, one.down.main_grad
+    layer = QuantizedFFN(up, down, "swiglu", r)
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(a):
+        layer.forward(x)
+    b.wait_stream(a)
+    with torch.cuda.stream(b):
+        torch.cuda._sleep(1_000_000)             # the first stream is ahead
+        dx = layer.backward(dy)
+    with torch.cuda.stream(a):
+        junk = [torch.full((T, n), 0xFF, dtype=torch.uint8, device=DEV) for n in (512, 512, 1024, 2048) * 4]
+    torch.cuda.synchronize()
+    for got, ref in zip((dx, layer.up.main_grad, layer.down.main_grad), want):
+        assert torch.equal(got, ref)
+    del junk
