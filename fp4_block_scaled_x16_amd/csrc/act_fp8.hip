@@ -8,7 +8,8 @@
 // Both are bound by HBM: per element of a, SwiGLU forward reads 4 bytes and
 // writes 3, backward reads 4 and writes 5; in values instead of codes the two
 // linears' quantizers would read and write another 16.  The 128 x 128 tile of
-// fp8_common.hpp, on the halves of h at once.
+// fp8_common.hpp, on the halves of h at once.  SwiGLU at 8192 x 6144: 71 us (5.0
+// TB/s) forward, 95 (4.8) backward.
 //
 // sigmoid is 1 / (1 + 2^(-g log2 e)) on the hardware exp2 and reciprocal (1 ulp
 // each; the argument's rounding makes |g| 2^-24 of relative error in the

@@ -377,6 +377,9 @@ __global__ __launch_bounds__(kThreads) void k_gemm_fp8(Params p) {
 // between two halves whose operands are in registers.  sched_barrier(0) pins
 // one MFMA and its share of LDS reads and DMA together: left to the scheduler
 // the DMA sinks to the next barrier.
+//
+// 8192 x 21504 x 4096: 600 us, 2.41 PFLOP/s, at the card's power limit (1.6 GHz);
+// the MFMAs alone, on registers, take 496, and 515 with their LDS reads.
 struct Frags {
   int8v a[4], b[4];
 };
@@ -656,6 +659,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_gemm_fp8_wide_loop(Params p) {
 // widened, from bytes read from LDS a quarter ahead; the barrier stands before
 // the last quarter, whose bytes are then in registers, so the DMA of the
 // stage that it frees has most of a step to land.
+//
+// 6144 x 2048 x 8192: 164 us, 1.26 PFLOP/s (171 added to D).  15 us (22) of it are
+// the first blocks' latency and D's own traffic, which nothing covers in a
+// single round of tiles; the MFMAs alone take 130.
 template <int MI>
 struct Raw {
   uint4 a[MI], b[4];

@@ -8,6 +8,10 @@
 // 128 x 128 tile per workgroup step: a block of either orientation lies in
 // one tile, so every scale is known after one read, and the tile is the unit
 // of the transposition through LDS (fp8_common.hpp).
+//
+// Measured: 8192 x 4096 along rows or columns 16.4 us (6.2 TB/s, part of it in
+// the last-level cache), both 24.2 (5.5), 12288 x 4608 in 2D both ways 40.4
+// (5.6), codes along the columns 8192 x 4096 12.3 (5.5); a large copy reaches 5.16.
 #include "fp8_common.hpp"
 
 using namespace fp8dev;
