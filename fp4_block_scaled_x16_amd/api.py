@@ -396,37 +396,40 @@ def _fp8_buffers(fmt, rows, cols, near, block=BLOCK_1D):
 def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpose, counters,
                   scale_layout, global_scope, count):
     R, C = x.shape
-    if block not in ("1d", "2d") or orient not in ("row", "col"):
-        raise ValueError("block must be '1d' or '2d' and orient 'row' or 'col'")
-    if scale_layout is None:
-        scale_layout = SCALES_KMAJOR
-    elif isinstance(scale_layout, str):
-        scale_layout = SCALE_LAYOUTS[scale_layout]
+    blk, d, d_t = _fp8_descs(f, block, orient, rnd, bool(rht), amax_in is not None,
+                             bool(emit_transpose), scale_layout, global_scope, count)
     if counters is not None and (counters.device != x.device or counters.dtype != torch.int64
                                  or counters.shape != (5,) or not counters.is_contiguous()):
         raise ValueError("counters must be an int64 [5] tensor on x's device (new_counters)")
-    blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
-    q = [_fp8_buffers(f, R, C, x, blk)] if row else []
-    q += [_fp8_buffers(f, C, R, q[0].codes if q else x, blk)] if col else []
-    d = [ctypes.byref(_fp8_desc(f, blk, o, SR if rnd == "sr" else RNE, bool(rht),
-                                amax_in is not None, bool(emit_transpose), int(scale_layout),
-                                GLOBAL_SCOPES[global_scope], COUNT_LEVELS[count]))
-         for o, on in ((ROWWISE, row), (COLWISE, col)) if on]
     lib = load_library()
     if row and col:
-        _launch("fp4_quantize_dual", lib.fp4_quantize_dual, x.device, d[0], d[1], x.data_ptr(), R,
-                C, _ld(x), q[0].codes.data_ptr(), q[0].scales.data_ptr(), q[1].codes.data_ptr(),
-                q[1].scales.data_ptr(), None, None, None, None, _addr(counters))
-    else:
-        _launch("fp4_quantize", lib.fp4_quantize, x.device, d[0], x.data_ptr(), R, C, _ld(x),
-                q[0].codes.data_ptr(), q[0].scales.data_ptr(), None, None, None, _addr(counters))
-    return tuple(q)
+        q = _fp8_buffers(f, R, C, x, blk)
+        q_t = _fp8_buffers(f, C, R, q.codes, blk)
+        _launch("fp4_quantize_dual", lib.fp4_quantize_dual, x.device, d, d_t, x.data_ptr(), R, C,
+                _ld(x), q.codes.data_ptr(), q.scales.data_ptr(), q_t.codes.data_ptr(),
+                q_t.scales.data_ptr(), None, None, None, None, _addr(counters))
+        return q, q_t
+    q = _fp8_buffers(f, R, C, x, blk) if row else _fp8_buffers(f, C, R, x, blk)
+    _launch("fp4_quantize", lib.fp4_quantize, x.device, d if row else d_t, x.data_ptr(), R, C,
+            _ld(x), q.codes.data_ptr(), q.scales.data_ptr(), None, None, None, _addr(counters))
+    return q,
 
 
 @functools.lru_cache(maxsize=64)
-def _fp8_desc(f, block, orient, rnd, rht, amax_given, emit_transpose, layout, scope, count):
-    return QuantDesc(f, block, orient, rnd, 0, 0, int(rht), 0, 448.0, int(amax_given),
-                     int(emit_transpose), layout, 0, (ctypes.c_uint32 * 3)(), 0, scope, count)
+def _fp8_descs(f, block, orient, rnd, rht, amax_given, emit_transpose, scale_layout, scope, count):
+    """The block's code and the (never written) descriptors of either orientation."""
+    if block not in ("1d", "2d") or orient not in ("row", "col"):
+        raise ValueError("block must be '1d' or '2d' and orient 'row' or 'col'")
+    if scale_layout is None:
+        layout = SCALES_KMAJOR
+    else:
+        layout = SCALE_LAYOUTS[scale_layout] if isinstance(scale_layout, str) else int(scale_layout)
+    blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
+    return blk, *(ctypes.byref(QuantDesc(f, blk, o, SR if rnd == "sr" else RNE, 0, 0, int(rht), 0,
+                                         448.0, int(amax_given), int(emit_transpose), layout, 0,
+                                         (ctypes.c_uint32 * 3)(), 0, GLOBAL_SCOPES[scope],
+                                         COUNT_LEVELS[count]))
+                  for o in (ROWWISE, COLWISE))
 
 
 def fp8_matrix(codes, scales, rows, cols, fmt="fp8"):
