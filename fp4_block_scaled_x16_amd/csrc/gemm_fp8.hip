@@ -20,6 +20,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "fp4_internal.hpp"
 #include "fp8_common.hpp"
@@ -861,15 +862,20 @@ struct Plan {
 // The kernel and split (if the caller has a workspace: share) with the least
 // estimated time.  A workgroup takes t1 us per K block while at most half of the
 // chip's places for such workgroups are taken, and up to t2 when all are (two
-// workgroups share a CU; the clock falls with the power drawn); a round of
-// workgroups has a fixed part (the persistent bf16 kernel once); joining reads
-// the fp32 sums that the parts wrote.  The constants are fits of times on 256 CUs,
-// measured / estimated in us, bf16 D: M = N = K = 4096: 256-row tiles 55 / 56,
-// 128-row 78 / 72; M = 2048: 128-row 37 / 36, 256-row 41 / 42; M = 1000, N = 4608,
-// K = 12288: 256-row tiles by 3 67 / 64, 128-row unshared 91 / 70.  fp32 D: M =
-// 6144, N = 2048, K = 8192: 192-row 164 / 164, 256-row 167 / 171, 128-row 210 / 205; M
-// = 8192, N = K = 4096: 256-row 200 / 208, 128-row 239 / 246, 192-row 249 / 246; M =
-// N = 2048, K = 8192: 128-row 68 / 71, 192-row 128 / 126.
+// workgroups share a CU as soon as there are more than CUs; the clock falls with
+// the power drawn); a round of workgroups has a fixed part (the persistent bf16
+// kernel once); the codes come from HBM at 5 TB/s, which hides behind the work
+// or hides it (a fourth-power mean joins the two); joining writes and reads the
+// parts' fp32 sums.  The constants are a least-squares fit of the times of every
+// kernel and split at 61 sizes (fp32 D: 63; M 17 .. 16384, N 320 .. 21504, K 1024 ..
+// 21504; 256 CUs): by them the chosen one takes 1 % more than the best on average.
+// Measured / estimated in us, bf16 D: M = N = K = 4096: 256-row tiles 55 / 60,
+// 128-row 78 / 67; M = 1000, N = 4608, K = 12288: 256-row tiles by 3 67 / 76, 128-row
+// unshared 91 / 89; M = 1160, N = 512, K = 6016: 64-row by 3 14.7 / 15.5, 128-row by 6
+// 19.2 / 17.3; M = 32, N = 4096, K = 21504: 64-row by 8 21.3 / 27.0, by 3 32.7 / 31.7.
+// fp32 D: M = 6144, N = 2048, K = 8192: 192-row 164 / 164, 256-row 167 / 166, 128-row
+// 210 / 174; M = 8192, N = K = 4096: 256-row 200 / 195, 192-row 249 / 249, 128-row
+// 239 / 223.
 //
 // Up to 16 rows of A: the kernel of gemm_fp8_rows.hip where 64 x 128 tiles would
 // leave half the CUs idle (M = 1: N = 6144, K = 2048 6.4 against 8.3 us; N = 4096,
@@ -885,10 +891,12 @@ Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
     double t1, t2, fixed;
   };
   static constexpr Cost kCosts[] = {
-      {kTile64, 0, 64, 128, 2, 0.65, 1.15, 4},   {kTile128, 0, 128, 128, 2, 1.05, 1.8, 4},
-      {kTile192, 0, 192, 256, 1, 1.85, 2.44, 8}, {kTile256, 0, 256, 256, 1, 2.1, 3.0, 8},
-      {kTile64, 1, 64, 128, 2, 0.43, 0.88, 4},   {kTile128, 1, 128, 128, 2, 0.62, 1.0, 4},
-      {kTile256, 1, 256, 256, 1, 1.05, 1.5, 8}};
+      {kTile64, 0, 64, 128, 2, 0.58, 1.05, 3.3}, {kTile128, 0, 128, 128, 2, 0.98, 1.63, 3.5},
+      {kTile192, 0, 192, 256, 1, 2.0, 2.43, 8},  {kTile256, 0, 256, 256, 1, 2.15, 2.73, 10},
+      {kTile64, 1, 64, 128, 2, 0.38, 0.69, 3.3}, {kTile128, 1, 128, 128, 2, 0.66, 0.94, 3.5},
+      {kTile256, 1, 256, 256, 1, 1.04, 1.6, 9}};
+  const double size = static_cast<double>(g.M) * static_cast<double>(g.N);
+  const double bytes = 4.0 + (static_cast<double>(g.M) + static_cast<double>(g.N)) * g.nkb * 128 / 5e6;
   static constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
   Plan best{kTile64, 1};
   double least = 0.0;
@@ -900,12 +908,14 @@ Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
       if (splits > 1 && (!share || g.nkb < 4 * splits)) break;
       const int64_t n = tiles(c.bm, c.bn) * splits, slots = c.per_cu * cus, whole = n / slots, rest = n % slots;
       const double full = static_cast<double>(rest) / static_cast<double>(slots);
-      const double last = rest == 0 ? 0.0 : c.t1 + (c.t2 - c.t1) * std::max(0.0, 2.0 * full - 1.0);
+      const double more = full <= 0.5 ? 0.0 : c.per_cu == 2 ? 0.8 + 0.2 * (2.0 * full - 1.0) : 2.0 * full - 1.0;
+      const double last = rest == 0 ? 0.0 : c.t1 + (c.t2 - c.t1) * more;
       const double blocks = static_cast<double>((g.nkb + splits - 1) / splits);
       const bool once = c.kind == kTile256 && c.bf16 && splits == 1;
       const double starts = once ? 1.0 : static_cast<double>(whole + (rest != 0));
-      const double join = splits > 1 ? 3.0 + (4 * splits + (c.bf16 ? 2 : 4)) * static_cast<double>(g.M) * g.N / 6.5e6 : 0.0;
-      const double t = (static_cast<double>(whole) * c.t2 + last) * blocks + starts * c.fixed + join;
+      const double join = splits > 1 ? 3.5 + splits * size * 1.28e-6 : 0.0;
+      const double work = (static_cast<double>(whole) * c.t2 + last) * blocks + starts * c.fixed;
+      const double t = std::sqrt(std::hypot(work * work, bytes * bytes)) + join;
       if (least == 0.0 || t < least) {
         least = t;
         best = {c.kind, splits};
