@@ -64,7 +64,8 @@ struct Fp8GemmArgs {
   int64_t ldd;
   int d_bf16, accumulate;
   int a_e5m2;            // operand A is E5M2 (B is E4M3)
-  float* part;           // the caller's workspace (gemm_fp8_workspace bytes), or null
+  float* part;           // the caller's workspace, or null
+  int64_t part_bytes;    // its size: less than gemm_fp8_workspace runs the product unshared
   int splits;            // set by the launcher
 };
 

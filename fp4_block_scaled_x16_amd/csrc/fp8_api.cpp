@@ -222,8 +222,8 @@ fp4_status gemm_fp8(const fp4_operand* A, const fp4_operand* B, int64_t M, int64
   g.D = D;
   g.ldd = ldd;
   g.accumulate = accumulate != 0;
-  if (workspace && workspace_bytes >= fp4lib::gemm_fp8_workspace(g))
-    g.part = static_cast<float*>(workspace);
+  g.part = static_cast<float*>(workspace);
+  g.part_bytes = workspace ? workspace_bytes : 0;
   return device_status(fp4lib::launch_gemm_fp8(g, static_cast<hipStream_t>(stream)),
                        "fp4_gemm launch");
 }

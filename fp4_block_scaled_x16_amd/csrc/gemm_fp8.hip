@@ -915,7 +915,7 @@ Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
       const double starts = once ? 1.0 : static_cast<double>(whole + (rest != 0));
       const double join = splits > 1 ? 3.5 + splits * size * 1.28e-6 : 0.0;
       const double work = (static_cast<double>(whole) * c.t2 + last) * blocks + starts * c.fixed;
-      const double t = std::sqrt(std::hypot(work * work, bytes * bytes)) + join;
+      const double t = std::sqrt(std::sqrt(work * work * work * work + bytes * bytes * bytes * bytes)) + join;
       if (least == 0.0 || t < least) {
         least = t;
         best = {c.kind, splits};
@@ -957,14 +957,16 @@ void run(const fp4lib::Fp8GemmArgs& g, Kind kind, hipStream_t s) {
 
 namespace fp4lib {
 
-int64_t gemm_fp8_workspace(const Fp8GemmArgs& g) {
-  const int splits = fp8gemm::plan_of(g, true).splits;
+static int64_t part_bytes(const Fp8GemmArgs& g, int splits) {
   return splits > 1 ? splits * g.M * fp8gemm::part_pitch(g.N) * 4 : 0;
 }
 
+int64_t gemm_fp8_workspace(const Fp8GemmArgs& g) { return part_bytes(g, fp8gemm::plan_of(g, true).splits); }
+
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& args, hipStream_t s) {
   Fp8GemmArgs g = args;
-  const fp8gemm::Plan p = fp8gemm::plan_of(g, g.part != nullptr);
+  fp8gemm::Plan p = fp8gemm::plan_of(g, g.part != nullptr);
+  if (part_bytes(g, p.splits) > g.part_bytes) p = fp8gemm::plan_of(g, false);
   g.splits = p.splits;
   if (g.a_e5m2) fp8gemm::run<1>(g, p.kind, s);
   else fp8gemm::run<0>(g, p.kind, s);
