@@ -299,3 +299,29 @@ def test_fp32_by_large_tiles(M, N, K, fa):
     api.gemm(a.operand(), b.operand(), M, N, K, out=d, accumulate=True)
     ref, bound, cut = product(a, b)
     close(d, ref + 0.5, bound + 0.5, cut)
+
+
+def test_two_threads():
+    """Products that share K, from two threads on streams of their own: each has
+    its own workspace."""
+    import threading
+    M, N, K = 24, 264, 9000
+    pairs = [operands(M, N, K, seed=s) for s in (1, 5)]
+    want = [api.gemm(a.operand(), b.operand(), M, N, K) for a, b in pairs]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(k):
+        a, b = pairs[k]
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got[k].append(api.gemm(a.operand(), b.operand(), M, N, K))
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for k in (0, 1):
+        assert len(got[k]) == 20 and all(torch.equal(d, want[k]) for d in got[k])
