@@ -878,13 +878,18 @@ struct Plan {
 // 239 / 223.
 //
 // Up to 16 rows of A: the kernel of gemm_fp8_rows.hip where 64 x 128 tiles would
-// leave half the CUs idle (M = 1: N = 6144, K = 2048 6.4 against 8.3 us; N = 4096,
-// K = 21504 17.5 against 20.6), tiles beyond (N = 21504, K = 4096: 18.2 against
-// 23.1 us, for every row of A is then read by far fewer workgroups).
+// leave half the CUs idle (M = 1: N = 6144, K = 2048 6.4 against 8.8 us; N = 4096,
+// K = 21504 17.0 against 19.4), tiles beyond (N = 21504, K = 4096: 19.0 against
+// 22.8 us, for every row of A is then read by far fewer workgroups).  With more
+// than 8 rows that reading counts where B is long enough to hide the tiles' second
+// launch (M = 16: N = 4096, K = 21504 tiles 20.0, rows 23.0; N = 12288, K = 4608
+// 14.5, 15.4; N = 2048, K = 6144 9.8, 7.9; M = 8: N = 4096, K = 21504 19.5, 19.7).
 Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
   const int64_t cus = fp4lib::device_cu_count();
   auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
-  if (g.M <= kMaxRows && tiles(64, 128) * 2 < cus) return {kRows, 1};
+  if (g.M <= kMaxRows && tiles(64, 128) * 2 < cus &&
+      (g.M <= 8 || !share || static_cast<double>(g.N) * g.nkb * 128 < 48e6))
+    return {kRows, 1};
   struct Cost {
     Kind kind;
     int bf16, bm, bn, per_cu;

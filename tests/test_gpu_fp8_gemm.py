@@ -325,3 +325,31 @@ def test_two_threads():
     torch.cuda.synchronize()
     for k in (0, 1):
         assert len(got[k]) == 20 and all(torch.equal(d, want[k]) for d in got[k])
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("out,M,N,K", [
+    # bf16, 256 rows a tile: one to four blocks of K, and K shared
+    (torch.bfloat16, 1989, 8201, 128), (torch.bfloat16, 2003, 8195, 250), (torch.bfloat16, 1999, 8199, 300),
+    (torch.bfloat16, 997, 8203, 500), (torch.bfloat16, 500, 8201, 8300),
+    # fp32, 192 rows: three and four blocks, K shared; 256 rows: five, K shared
+    (torch.float32, 997, 8203, 300), (torch.float32, 997, 8203, 500), (torch.float32, 2999, 1001, 12300),
+    (torch.float32, 1500, 8201, 640), (torch.float32, 500, 8201, 8300)])
+def test_few_blocks_and_shared_k_by_large_tiles(out, M, N, K, accumulate):
+    a, b = operands(M, N, K, seed=2)
+    ref, bound, cut = product(a, b)
+    if not accumulate:
+        close(api.gemm(a.operand(), b.operand(), M, N, K, out_dtype=out), ref, bound, cut)
+        return
+    d = torch.full((M, N + 3), 0.5, dtype=out, device=DEV)
+    api.gemm(a.operand(), b.operand(), M, N, K, out=d[:, 1:N + 1], accumulate=True)
+    close(d[:, 1:N + 1], ref + 0.5, bound + 0.5, cut)
+    assert bool((d[:, :1] == 0.5).all()) and bool((d[:, N + 1:] == 0.5).all())
+
+
+@pytest.mark.parametrize("M", [8, 9, 16])
+def test_a_batch_of_decoding_requests(M):
+    """More than 8 rows and a long B leave the kernel for few rows."""
+    N, K = 3000, 17000
+    a, b = operands(M, N, K, seed=4)
+    close(api.gemm(a.operand(), b.operand(), M, N, K, out_dtype=torch.bfloat16), *product(a, b))
