@@ -1,7 +1,7 @@
 // FP8 block-128 GEMM with few rows of A (a token, a batch of decoding
 // requests): D[M, N] for M <= 16.
 //
-// Bound by reading B once: at M = 1, N = 4096, K = 21504 its 88 MB (17.5 us, 5.0
+// Bound by reading B once: at M = 1, N = 4096, K = 21504 its 88 MB (16.9 us, 5.2
 // TB/s).  No LDS staging, since no byte of B is used twice: every lane loads its
 // own operands of v_mfma_f32_16x16x32_bf16 from global memory (the codes widened
 // exactly, as for an fp32 D in gemm_fp8.hip; the arithmetic is free here, so bf16
