@@ -66,12 +66,62 @@ import torch
 from . import api
 
 
+_MARK = "fp4_mi355x"
+
+
+def _listened(weight):
+    """Whether hooks of the weight may be waiting for a backward pass: those of
+    the tensor, or those of the node that accumulates its gradient.  That node
+    lives only while somebody holds it (a program that put hooks on it, or another
+    graph), so a mark on it outlasts this function's own hold only then."""
+    if weight._backward_hooks or weight._post_accumulate_grad_hooks:
+        return True
+    edge = torch.autograd.graph.get_gradient_edge
+    edge(weight).node.metadata[_MARK] = True
+    return _MARK in edge(weight).node.metadata
+
+
+class _Reached(torch.autograd.Function):
+    """A graph whose backward pass reaches the weight without a gradient."""
+
+    @staticmethod
+    def forward(ctx, weight):
+        return weight.new_empty(())
+
+    @staticmethod
+    def backward(ctx, _):
+        return None
+
+
+def _capturing(weight):
+    return weight.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
 def grad_alias(weight):
-    """The weight for one call's autograd graph, as a leaf of that graph alone.
-    A weight needs no gradient of its own there, but makes the output need
-    one; as a leaf that several graphs share it would carry the stream of the
-    first into a backward pass that is being captured on another."""
-    return weight.detach().requires_grad_(weight.requires_grad)
+    """The weight for one call's autograd graph.  It needs no gradient of its own
+    there, but makes the output need one, and its hooks run in the backward pass
+    (with None: the gradient is in main_grad by then).
+
+    Where no hook is waiting it is an alias that is a leaf of that graph alone: as
+    a leaf that several graphs share, the weight would carry the stream of the
+    first into a backward pass that is being captured on another.  A hook that is
+    registered between the two passes is reached from the alias.  A step that is
+    captured has the alias in any case, and runs no hooks: they would run once,
+    while it is recorded, and not when it is replayed."""
+    if not weight.requires_grad or not torch.is_grad_enabled():
+        return weight
+    if not _capturing(weight) and _listened(weight):
+        return weight
+    alias = weight.detach().requires_grad_()
+
+    def reached(_):
+        if not _capturing(weight) and _listened(weight):
+            with torch.enable_grad():
+                root = _Reached.apply(weight)
+            torch.autograd.backward(root, retain_graph=True)
+
+    alias.register_post_accumulate_grad_hook(reached)
+    return alias
 
 
 class Kept:
