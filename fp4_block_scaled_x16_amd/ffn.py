@@ -28,7 +28,7 @@ from __future__ import annotations
 import torch
 
 from . import api
-from .linear import Kept, QuantizedLinear, Recipe, grad_alias
+from .linear import Kept, QuantizedLinear, Recipe, grad_alias, grad_rows
 
 
 class QuantizedFFN:
@@ -110,4 +110,4 @@ class _FfnFunction(torch.autograd.Function):
         if ctx.saved is None:
             raise RuntimeError("a step's operands are freed by its first backward pass")
         saved, ctx.saved = ctx.saved, None
-        return ctx.layer._backward(dy.contiguous(), saved), None, None, None
+        return ctx.layer._backward(grad_rows(dy), saved), None, None, None

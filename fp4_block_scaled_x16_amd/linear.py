@@ -124,6 +124,15 @@ def grad_alias(weight):
     return alias
 
 
+def grad_rows(dy):
+    """A gradient as the quantizers take it: row-major, its rows 16-byte aligned
+    (autograd's may be of any layout, and a dense one of any width)."""
+    if dy.stride(1) == 1 and dy.data_ptr() % 16 == 0 and (
+            dy.shape[0] < 2 or (dy.stride(0) >= dy.shape[1] and dy.stride(0) % 8 == 0)):
+        return dy
+    return api._bf16_rows(*dy.shape, dy.device).copy_(dy)
+
+
 class Kept:
     """What a forward step keeps for its backward step.  A backward step on
     another stream tells the allocator so: the tensors' memory belongs to the
@@ -391,5 +400,5 @@ class _Fp4LinearFunction(torch.autograd.Function):
         if ctx.saved is None:
             raise RuntimeError("a step's operands are freed by its first backward pass")
         saved, ctx.saved = ctx.saved, None
-        dx = ctx.layer._backward(dy.contiguous(), saved)
+        dx = ctx.layer._backward(grad_rows(dy), saved)
         return dx, None, None
