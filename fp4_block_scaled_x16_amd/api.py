@@ -432,18 +432,26 @@ def _fp8_descs(f, block, orient, rnd, rht, amax_given, emit_transpose, scale_lay
                   for o in (ROWWISE, COLWISE))
 
 
+def _bytes(t, dtype, name):
+    """uint8 t, or the bytes of one of the dtype."""
+    if t.dtype == torch.uint8:
+        return t
+    if t.dtype != dtype:
+        raise ValueError("%s must be uint8 or %s, not %s" % (name, dtype, t.dtype))
+    return t.view(torch.uint8)
+
+
 def fp8_matrix(codes, scales, rows, cols, fmt="fp8"):
     """A Quantized of FP8 codes and scales that exist already (a checkpoint's
-    weights): codes uint8 (or a float8 dtype) [rows, cols up to 128], zeros from
-    cols on; scales uint8 [blocks of cols, rows up to 16], the byte of (block j,
-    row r) being e + 127 of the scale 2^e."""
+    weights): codes uint8 (or fmt's torch dtype, float8_e4m3fn or float8_e5m2)
+    [rows, cols up to 128], zeros from cols on; scales uint8 (or float8_e8m0fnu)
+    [blocks of cols, rows up to 16], the byte of (block j, row r) being e + 127 of
+    the scale 2^e."""
     f = _fmt(fmt)
     if f not in FP8:
         raise ValueError("fmt must be 'fp8' or 'fp8_e5m2'")
-    if codes.dtype != torch.uint8:
-        codes = codes.view(torch.uint8)
-    if scales.dtype != torch.uint8:
-        scales = scales.view(torch.uint8)
+    codes = _bytes(codes, torch.float8_e4m3fn if f == FP8_E4M3 else torch.float8_e5m2, "codes")
+    scales = _bytes(scales, torch.float8_e8m0fnu, "scales")
     kb = -(-cols // 128)
     if codes.shape != (rows, 128 * kb) or not codes.is_contiguous():
         raise ValueError("codes must be a contiguous [%d, %d] tensor" % (rows, 128 * kb))
