@@ -332,11 +332,9 @@ def quantize_dual(x, fmt="nvfp4", rnd="rne", seed=0, offset=0, offset_t=None, rh
     x = _as_bf16_bits(x)
     f = _fmt(fmt)
     if f in FP8:
-        if scale_layout_t is not None and scale_layout is None:
-            scale_layout = scale_layout_t
         return _quantize_fp8(x, f, block, "row", True, True, rnd, rht or rht_row,
                              amax_in if amax_in is not None else amax_t_in, False, counters,
-                             scale_layout, "tensor", count)
+                             scale_layout, "tensor", count, scale_layout_t)
     if block != "1d":
         raise ValueError("2D dual quantization needs an FP8 format (NVFP4, UE5M3: quantize with "
                          "emit_transpose)")
@@ -394,10 +392,11 @@ def _fp8_buffers(fmt, rows, cols, near, block=BLOCK_1D):
 
 
 def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpose, counters,
-                  scale_layout, global_scope, count):
+                  scale_layout, global_scope, count, scale_layout_t=None):
     R, C = x.shape
     blk, d, d_t = _fp8_descs(f, block, orient, rnd, bool(rht), amax_in is not None,
-                             bool(emit_transpose), scale_layout, global_scope, count)
+                             bool(emit_transpose), scale_layout, scale_layout_t, global_scope,
+                             count)
     if counters is not None and (counters.device != x.device or counters.dtype != torch.int64
                                  or counters.shape != (5,) or not counters.is_contiguous()):
         raise ValueError("counters must be an int64 [5] tensor on x's device (new_counters)")
@@ -416,20 +415,25 @@ def _quantize_fp8(x, f, block, orient, row, col, rnd, rht, amax_in, emit_transpo
 
 
 @functools.lru_cache(maxsize=64)
-def _fp8_descs(f, block, orient, rnd, rht, amax_given, emit_transpose, scale_layout, scope, count):
+def _fp8_descs(f, block, orient, rnd, rht, amax_given, emit_transpose, scale_layout, scale_layout_t,
+               scope, count):
     """The block's code and the (never written) descriptors of either orientation."""
     if block not in ("1d", "2d") or orient not in ("row", "col"):
         raise ValueError("block must be '1d' or '2d' and orient 'row' or 'col'")
-    if scale_layout is None:
-        layout = SCALES_KMAJOR
-    else:
-        layout = SCALE_LAYOUTS[scale_layout] if isinstance(scale_layout, str) else int(scale_layout)
+
+    def layout_of(layout):
+        return SCALE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+
+    layout = SCALES_KMAJOR
+    if scale_layout is not None or scale_layout_t is not None:
+        layout = layout_of(scale_layout_t if scale_layout is None else scale_layout)
+    layout_t = layout if scale_layout_t is None else layout_of(scale_layout_t)
     blk = BLOCK_2D128 if block == "2d" else BLOCK_1D
     return blk, *(ctypes.byref(QuantDesc(f, blk, o, SR if rnd == "sr" else RNE, 0, 0, int(rht), 0,
-                                         448.0, int(amax_given), int(emit_transpose), layout, 0,
+                                         448.0, int(amax_given), int(emit_transpose), lay, 0,
                                          (ctypes.c_uint32 * 3)(), 0, GLOBAL_SCOPES[scope],
                                          COUNT_LEVELS[count]))
-                  for o in (ROWWISE, COLWISE))
+                  for o, lay in ((ROWWISE, layout), (COLWISE, layout_t)))
 
 
 def _bytes(t, dtype, name):
