@@ -183,6 +183,11 @@ class Recipe:
     grad_fmt: str = "fp8_e5m2"    # fmt "fp8": the format of dY ("fp8" or "fp8_e5m2")
     checkpoint8: bool = True      # fmt "fp8": keep only X's row codes for the backward pass
 
+    def __post_init__(self):
+        # formats may be given by the library's numbers, as `api.quantize` takes them
+        names = {number: name for name, number in api.FORMATS.items()}
+        self.fmt, self.grad_fmt = names.get(self.fmt, self.fmt), names.get(self.grad_fmt, self.grad_fmt)
+
     @property
     def two_level(self):
         return self.fmt in ("nvfp4", "ue5m3")
