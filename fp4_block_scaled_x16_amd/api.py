@@ -109,9 +109,11 @@ def load_library(path=None):
     lib.fp4_selftest_sweep.argtypes = [i32, vp, i32, vp, vp]
     lib.fp4_selftest_gemm_decode.argtypes = [i32, vp, vp]
     lib.fp4_selftest_set_geometry.argtypes = [i32, i32]
+    lib.fp4_selftest_set_fp8_plan.argtypes = [i32, i32]
     for f in ("fp4_amax", "fp4_quantize", "fp4_quantize_dual", "fp4_dequantize", "fp4_rht16",
               "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_gemm_ws",
-              "fp4_selftest_sweep", "fp4_selftest_gemm_decode", "fp4_selftest_set_geometry"):
+              "fp4_selftest_sweep", "fp4_selftest_gemm_decode", "fp4_selftest_set_geometry",
+              "fp4_selftest_set_fp8_plan"):
         getattr(lib, f).restype = ctypes.c_int
     lib.fp4_status_string.argtypes = [ctypes.c_int]
     lib.fp4_status_string.restype = ctypes.c_char_p
@@ -704,3 +706,10 @@ def selftest_set_geometry(max_workgroups=0, gemm_tile_rows=0):
     """Launch-geometry controls for race guards (0, 0: the defaults)."""
     _check(load_library().fp4_selftest_set_geometry(int(max_workgroups), int(gemm_tile_rows)),
            "fp4_selftest_set_geometry")
+
+
+def selftest_set_fp8_plan(tile_rows=0, splits=1):
+    """The kernel of the FP8 products (0: chosen by size)."""
+    _check(load_library().fp4_selftest_set_fp8_plan(int(tile_rows), int(splits)),
+           "fp4_selftest_set_fp8_plan")
+    _gemm_workspace.cache_clear()

@@ -510,6 +510,15 @@ FP4_EXPORT fp4_status fp4_selftest_set_geometry(int max_workgroups, int gemm_til
   return ok();
 }
 
+FP4_EXPORT fp4_status fp4_selftest_set_fp8_plan(int tile_rows, int splits) {
+  if (tile_rows != 0 && tile_rows != 16 && tile_rows != 64 && tile_rows != 128 && tile_rows != 192 &&
+      tile_rows != 256)
+    return fail(FP4_ERR_ARG, "tile_rows must be 0, 16, 64, 128, 192 or 256");
+  if (splits < 1) return fail(FP4_ERR_ARG, "splits must be >= 1");
+  fp4lib::set_fp8_plan(tile_rows, splits);
+  return ok();
+}
+
 FP4_EXPORT fp4_status fp4_selftest_sweep(int kind, const uint32_t* thresholds, int n,
                                          uint64_t* result, void* stream) {
   static const int kLen[5] = {7, 126, 255, 7, 126};

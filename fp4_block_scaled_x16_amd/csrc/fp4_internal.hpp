@@ -148,6 +148,7 @@ hipError_t launch_act_quant_fp8(const Fp8ActArgs& a, hipStream_t s);
 hipError_t launch_act_grad_fp8(const Fp8ActGradArgs& a, hipStream_t s);
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& g, hipStream_t s);
 int64_t gemm_fp8_workspace(const Fp8GemmArgs& g);
+void set_fp8_plan(int tile_rows, int splits);      // fp4_selftest_set_fp8_plan
 // Exhaustive conversion checks (selftest.hip).
 hipError_t launch_selftest_sweep(int kind, const uint32_t* thresholds, int n, uint64_t* result,
                                  hipStream_t s);

@@ -20,6 +20,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "fp4_internal.hpp"
@@ -853,11 +854,25 @@ __global__ __launch_bounds__(256) void k_gemm_fp8_join(fp4lib::Fp8GemmArgs g) {
 }
 
 // How a product runs: the kernel, and the workgroups that share a tile's K.
-enum Kind { kRows, kTile64, kTile128, kTile192, kTile256 };
+enum Kind { kRows, kTile64, kTile128, kTile192, kTile256, kNone };
 struct Plan {
   Kind kind;
   int splits;
 };
+
+// A plan that a test asks for (fp4_selftest_set_fp8_plan): rows of a tile, 16 for
+// the kernel for few rows; 0: none.  kNone where the kernel cannot run the product.
+std::atomic<int> g_rows{0}, g_splits{1};
+
+Plan asked_plan(const fp4lib::Fp8GemmArgs& g, int rows) {
+  const int splits = g_splits.load();
+  const Plan none{kNone, 1};
+  if (splits > 1 && splits > g.nkb) return none;
+  if (rows == 16) return g.M <= kMaxRows && splits == 1 ? Plan{kRows, 1} : none;
+  if (rows >= 192 && (g.nkb == 0 || g.ld[0] >= (1 << 23) || g.ld[1] >= (1 << 23))) return none;
+  if (rows == 192 && g.d_bf16) return none;
+  return {rows == 64 ? kTile64 : rows == 128 ? kTile128 : rows == 192 ? kTile192 : kTile256, splits};
+}
 
 // The kernel and split (if the caller has a workspace: share) with the least
 // estimated time.  A workgroup takes t1 us per K block while at most half of the
@@ -885,6 +900,7 @@ struct Plan {
 // launch (M = 16: N = 4096, K = 21504 tiles 20.0, rows 23.0; N = 12288, K = 4608
 // 14.5, 15.4; N = 2048, K = 6144 9.8, 7.9; M = 8: N = 4096, K = 21504 19.5, 19.7).
 Plan plan_of(const fp4lib::Fp8GemmArgs& g, bool share) {
+  if (const int rows = g_rows.load()) return asked_plan(g, rows);
   const int64_t cus = fp4lib::device_cu_count();
   auto tiles = [&](int64_t bm, int64_t bn) { return ((g.M + bm - 1) / bm) * ((g.N + bn - 1) / bn); };
   if (g.M <= kMaxRows && tiles(64, 128) * 2 < cus &&
@@ -954,6 +970,8 @@ void run(const fp4lib::Fp8GemmArgs& g, Kind kind, hipStream_t s) {
         launch_kernel(k_gemm_fp8_wide_loop<FA>, g, 256, 256, s, cus);
       else launch_kernel(k_gemm_fp8_wide<FA>, g, 256, 256, s);
       break;
+    case kNone:
+      break;
   }
 }
 
@@ -968,10 +986,17 @@ static int64_t part_bytes(const Fp8GemmArgs& g, int splits) {
 
 int64_t gemm_fp8_workspace(const Fp8GemmArgs& g) { return part_bytes(g, fp8gemm::plan_of(g, true).splits); }
 
+void set_fp8_plan(int tile_rows, int splits) {
+  fp8gemm::g_rows.store(tile_rows);
+  fp8gemm::g_splits.store(splits);
+}
+
 hipError_t launch_gemm_fp8(const Fp8GemmArgs& args, hipStream_t s) {
   Fp8GemmArgs g = args;
   fp8gemm::Plan p = fp8gemm::plan_of(g, g.part != nullptr);
   if (part_bytes(g, p.splits) > g.part_bytes) p = fp8gemm::plan_of(g, false);
+  // (an asked plan alone can be neither of the two)
+  if (p.kind == fp8gemm::kNone || part_bytes(g, p.splits) > g.part_bytes) return hipErrorInvalidValue;
   g.splits = p.splits;
   if (g.a_e5m2) fp8gemm::run<1>(g, p.kind, s);
   else fp8gemm::run<0>(g, p.kind, s);

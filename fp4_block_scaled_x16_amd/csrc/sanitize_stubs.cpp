@@ -55,6 +55,7 @@ hipError_t launch_act_quant_fp8(const Fp8ActArgs&, hipStream_t) { return hipErro
 hipError_t launch_act_grad_fp8(const Fp8ActGradArgs&, hipStream_t) { return hipErrorNoDevice; }
 hipError_t launch_gemm_fp8(const Fp8GemmArgs&, hipStream_t) { return hipErrorNoDevice; }
 int64_t gemm_fp8_workspace(const Fp8GemmArgs&) { return 0; }
+void set_fp8_plan(int, int) {}
 hipError_t launch_selftest_sweep(int, const uint32_t*, int, uint64_t*, hipStream_t) {
   return hipErrorNoDevice;
 }

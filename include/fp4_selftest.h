@@ -97,6 +97,21 @@ fp4_status fp4_selftest_gemm_decode(fp4_format format, uint16_t* out, void* stre
  */
 fp4_status fp4_selftest_set_geometry(int max_workgroups, int gemm_tile_rows);
 
+/*
+ * fp4_selftest_set_fp8_plan -- which kernel the FP8 products run on, so that a
+ * test reaches each of them at any size (otherwise a cost model chooses).
+ *   tile_rows  16: the kernel for up to 16 rows of A; 64, 128, 192 (fp32 D) or
+ *              256: tiles of that many rows; 0: chosen per product.
+ *   splits     >= 1: workgroups that share a tile's K, at most its blocks (1
+ *              with 16 rows); ignored with tile_rows 0.
+ * While one is set, fp4_gemm_workspace returns what it needs, and a product that
+ * it cannot run (too many rows, a bf16 D on 192 rows, K = 0 on 192 or 256, more
+ * splits than K has blocks, a workspace that is too small) fails with
+ * FP4_ERR_DEVICE and enqueues nothing.  Process-wide, as fp4_selftest_set_geometry.
+ * Rejects other values (FP4_ERR_ARG).
+ */
+fp4_status fp4_selftest_set_fp8_plan(int tile_rows, int splits);
+
 #ifdef __cplusplus
 }
 #endif
