@@ -28,7 +28,7 @@ from __future__ import annotations
 import torch
 
 from . import api
-from .linear import Kept, QuantizedLinear, Recipe, grad_alias, grad_rows
+from .linear import Kept, QuantizedLinear, Recipe, grad_alias, grad_rows, reach_hooks
 
 
 class QuantizedFFN:
@@ -102,7 +102,7 @@ class _FfnFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, up, down, layer):
         y, ctx.saved = layer._forward(x)
-        ctx.layer = layer
+        ctx.layer, ctx.weights = layer, ((layer.up.weight, up), (layer.down.weight, down))
         return y
 
     @staticmethod
@@ -110,4 +110,7 @@ class _FfnFunction(torch.autograd.Function):
         if ctx.saved is None:
             raise RuntimeError("a step's operands are freed by its first backward pass")
         saved, ctx.saved = ctx.saved, None
-        return ctx.layer._backward(grad_rows(dy), saved), None, None, None
+        dx = ctx.layer._backward(grad_rows(dy), saved)
+        for weight, alias in ctx.weights:
+            reach_hooks(weight, alias)
+        return dx, None, None, None

@@ -104,24 +104,28 @@ def grad_alias(weight):
 
     Where no hook is waiting it is an alias that is a leaf of that graph alone: as
     a leaf that several graphs share, the weight would carry the stream of the
-    first into a backward pass that is being captured on another.  A hook that is
-    registered between the two passes is reached from the alias.  A step that is
+    first into a backward pass that is being captured on another.  A step that is
     captured has the alias in any case, and runs no hooks: they would run once,
     while it is recorded, and not when it is replayed."""
     if not weight.requires_grad or not torch.is_grad_enabled():
         return weight
     if not _capturing(weight) and _listened(weight):
         return weight
-    alias = weight.detach().requires_grad_()
+    return weight.detach().requires_grad_()
+
+
+def reach_hooks(weight, alias):
+    """In the backward pass, before it comes to the alias: hooks that have been
+    registered since the forward pass run when it does."""
+    if alias is weight or not alias.requires_grad or _capturing(weight) or not _listened(weight):
+        return
 
     def reached(_):
-        if not _capturing(weight) and _listened(weight):
-            with torch.enable_grad():
-                root = _Reached.apply(weight)
-            torch.autograd.backward(root, retain_graph=True)
+        with torch.enable_grad():
+            root = _Reached.apply(weight)
+        torch.autograd.backward(root, retain_graph=True)
 
     alias.register_post_accumulate_grad_hook(reached)
-    return alias
 
 
 def grad_rows(dy):
@@ -397,7 +401,7 @@ class _Fp4LinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, layer):
         y, ctx.saved = layer._forward(x)
-        ctx.layer = layer
+        ctx.layer, ctx.weights = layer, (layer.weight, weight)
         return y
 
     @staticmethod
@@ -406,4 +410,5 @@ class _Fp4LinearFunction(torch.autograd.Function):
             raise RuntimeError("a step's operands are freed by its first backward pass")
         saved, ctx.saved = ctx.saved, None
         dx = ctx.layer._backward(grad_rows(dy), saved)
+        reach_hooks(*ctx.weights)
         return dx, None, None
