@@ -258,7 +258,8 @@ def quantize(x, fmt="nvfp4", block="1d", orient="row", rnd="rne", seed=0, offset
     scale_layout: "rowmajor" (the default) or "tiled" (1D blocks only).
     fmt "fp8" (E4M3) and "fp8_e5m2": any R and C, block "1d" (1x128) or "2d"
     (128x128), orient "row" or "col", rnd "rne"; scales "kmajor"; x's row pitch a
-    multiple of 8, as ever.  rht_n: size of the RHT (4, 16, 32, 64, 128); signs:
+    multiple of 8, as ever; their scales are always rounded up and depend on x
+    alone, so scale_round and target mean nothing there.  rht_n: size of the RHT (4, 16, 32, 64, 128); signs:
     its sign mask, up to 128 bits.
     scale_round: "rne" or "up" (truncation-free block scales).
     global_scope: "tensor" or "row" (rowwise 1D NVFP4 / UE5M3: one global
@@ -634,7 +635,9 @@ def gemm(a: Operand, b: Operand, M, N, K, out=None, accumulate=False, device=Non
          out_dtype=torch.float32):
     """D[M, N] (+)= s_A s_B sum_k a[m, k] b[n, k], written as fp32 or bf16
     (the dtype of `out` when given, else out_dtype).  FP8: a is "fp8" or
-    "fp8_e5m2" and b "fp8"; K is their code matrices' cols, whole."""
+    "fp8_e5m2" and b "fp8"; K is their code matrices' cols, whole.  A row's bf16
+    result may differ in its last bit with the number of rows beside it: up to 16
+    rows are summed in fp32 throughout, more by the 8-bit matrix instructions."""
     if a.format in FP8 and b.format in FP8:
         qa, qb = getattr(a, "_owner", None), getattr(b, "_owner", None)
         if qa and qb and (qa.cols != K or qb.cols != K or M > qa.rows or N > qb.rows):

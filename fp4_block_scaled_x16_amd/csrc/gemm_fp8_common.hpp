@@ -13,7 +13,8 @@ namespace fp8gemm {
 using fp8dev::bf16x2;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// 8 codes (two words) with their block's scale as bf16, exact.
+// 8 codes (two words) with their block's scale as bf16: exact from 2^-126 to below
+// 2^128 (a code of 2^-9 with the scale 2^-127 is below bf16's subnormals).
 template <bool E5>
 __device__ __forceinline__ bf16x8 widen8(uint32_t w0, uint32_t w1, float s) {
   bf16x2 a, b, c, d;

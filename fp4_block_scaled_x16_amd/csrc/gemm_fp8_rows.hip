@@ -4,8 +4,8 @@
 // Bound by reading B once: at M = 1, N = 4096, K = 21504 its 88 MB (16.9 us, 5.2
 // TB/s).  No LDS staging, since no byte of B is used twice: every lane loads its
 // own operands of v_mfma_f32_16x16x32_bf16 from global memory (the codes widened
-// exactly, as for an fp32 D in gemm_fp8.hip; the arithmetic is free here, so bf16
-// outputs have it too).  A workgroup owns 16 rows of B; its waves take turns
+// as for an fp32 D in gemm_fp8.hip; the arithmetic is free here, so bf16 outputs
+// have it too).  A workgroup owns 16 rows of B; its waves take turns
 // along K, so that a few rows of B still put 16 waves of loads in flight on a CU,
 // and their sums meet in LDS in a fixed order.
 #include <hip/hip_runtime.h>

@@ -51,8 +51,10 @@ Calling the layer (`layer(x)`) runs it under autograd: a torch.autograd.
 Function whose forward is Fprop and whose backward is Dgrad (the gradient
 of x) and Wgrad (added to main_grad; the weight gets no .grad).  Its
 gradient dY is quantized from bf16, so the autograd path takes bf16 x and
-writes bf16 Y and dX (out_dtype "bf16").  `forward` / `backward` are the
-same steps called explicitly, one backward per forward.
+writes bf16 Y and dX (out_dtype "bf16").  Hooks on the weight run in that
+backward pass, when main_grad has the step's gradient (but not in a step that is
+captured into a graph).  `forward` / `backward` are the same steps called
+explicitly, one backward per forward.
 
 Every computation runs in the library's kernels; this module only
 allocates outputs and passes pointers (through `api`).
@@ -176,10 +178,10 @@ class Recipe:
     rht_n: int = 16               # RHT size N: 4, 16, 32, 64 or 128
     rht_signs: int = 0            # N-bit sign mask D_r
     sr_seed: int = 1              # Philox key of the stochastic rounding of dY
-    amax_interval: int = 1        # recompute each tensor amax every this many steps
-    scale_layout: str = "tiled"   # storage of the 1D block scales
+    amax_interval: int = 1        # recompute each tensor amax every this many steps (two-level)
+    scale_layout: str = "tiled"   # storage of the FP4 formats' 1D block scales
     act_block: str = "1d"         # "1d" (1x16 / 1x32) or "2d" (16x16) for X and dY
-    scale_round: str = "rne"      # block scales: "rne" or "up" (truncation-free)
+    scale_round: str = "rne"      # two-level block scales: "rne" or "up" (truncation-free)
     rht_kd: bool = False          # RHT along K on the Fprop / Dgrad operands too
     rht_kd_n: int = 16            # its size N: 4 or 16
     rht_kd_signs: int = 0         # its N-bit sign mask

@@ -85,7 +85,9 @@ extern "C" {
  *   repeated for each of its rows).
  *   A NaN element becomes a NaN code, an infinite one a NaN (E4M3) or an
  *   infinity (E5M2); a block's NaNs do not count towards amax_B, and a block
- *   with an infinity has the scale of the largest finite fp32 value. */
+ *   with an infinity has the scale of the largest finite fp32 value.
+ *   Magnitudes from 248 * 2^120 (E5M2: 240 * 2^120) round up to 2^128, which is
+ *   an infinity in fp32 and bf16 (fp4_dequantize, the products' fp32 form). */
 typedef enum fp4_format_e FP4_ENUM_INT {
   FP4_NVFP4 = 0, FP4_UE5M3 = 1, FP4_MXFP4 = 2, FP4_MXFP8 = 3, FP4_FP8_E4M3 = 5, FP4_FP8_E5M2 = 6
 } fp4_format;
@@ -408,7 +410,9 @@ typedef enum fp4_out_type_e FP4_ENUM_INT { FP4_OUT_F32 = 0, FP4_OUT_BF16 = 1 } f
  * below the largest one's binade, so the value before its rounding is within
  * 1e-5 sum |a b| + 7 * 2^-13 of each group's largest |a b|, subnormal
  * elements counted as the smallest normal one (fp32 D: products and sums in
- * fp32, of operands below 2^-126 as bf16 holds them).
+ * fp32, of operands below 2^-126 as bf16 holds them).  Up to 16 rows of A may
+ * have the fp32 form for a bf16 D too, so the same row of A can differ in the
+ * last bit of its outputs between a short batch and a long one.
  * K == 0 writes zeros (or leaves D unchanged when accumulating).
  */
 fp4_status fp4_gemm(const fp4_operand* A /* host */, const fp4_operand* B /* host */,
