@@ -111,15 +111,17 @@ def grad_alias(weight):
     while it is recorded, and not when it is replayed."""
     if not weight.requires_grad or not torch.is_grad_enabled():
         return weight
-    if not _capturing(weight) and _listened(weight):
+    if weight.is_leaf and not _capturing(weight) and _listened(weight):
         return weight
     return weight.detach().requires_grad_()
 
 
 def reach_hooks(weight, alias):
     """In the backward pass, before it comes to the alias: hooks that have been
-    registered since the forward pass run when it does."""
-    if alias is weight or not alias.requires_grad or _capturing(weight) or not _listened(weight):
+    registered since the forward pass, and those of a weight that is itself computed
+    (whose graph outlasts the step's), run when it does."""
+    if (alias is weight or not alias.requires_grad or not weight.requires_grad
+            or _capturing(weight) or not _listened(weight)):
         return
 
     def reached(_):

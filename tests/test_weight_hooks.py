@@ -133,6 +133,28 @@ def test_weights_without_gradients_and_steps_without_a_graph():
 
 
 @pytest.mark.parametrize("kind", ["linear", "ffn"])
+def test_weights_that_are_frozen_between_the_passes(kind):
+    layer, weights = make(kind)
+    y = layer(torch.ones((4, 16), dtype=BF))
+    for w, _ in weights:
+        w.requires_grad_(False)
+    y.backward(torch.ones_like(y))
+    assert all(float(o.main_grad.sum()) > 0 for _, o in weights)
+
+
+def test_a_weight_that_is_computed():
+    """Its graph is reached without a gradient, step after step, as its hooks are."""
+    base = leaf(8, 16)
+    w = base * 1
+    layer, log = PlainLinear(w, R), []
+    w.register_hook(lambda g: log.append(g))
+    for n in (1, 2):
+        y = layer(torch.ones((4, 16), dtype=BF))
+        y.backward(torch.ones_like(y))
+        assert log == [None] * n and base.grad is None
+
+
+@pytest.mark.parametrize("kind", ["linear", "ffn"])
 def test_a_weight_that_nobody_listens_to_shares_no_leaf(kind):
     """Its graphs hold leaves of their own, so one that is alive does not tie a
     step that is captured on another stream to its own."""
