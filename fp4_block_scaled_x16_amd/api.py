@@ -69,10 +69,35 @@ class Operand(ctypes.Structure):
                 ("s_dec_scope", ctypes.c_int)]
 
 
+class Heads(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("heads", ctypes.c_int64)]
+
+
+class QKNormDesc(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("weight_f32", ctypes.c_int), ("eps", ctypes.c_float), ("table", ctypes.c_void_p),
+                ("table_rows", ctypes.c_int64), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("pages", ctypes.c_int64),
+                ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("scale_block_stride", ctypes.c_int64),
+                ("amax", ctypes.c_void_p), ("target", ctypes.c_float)]
+
+
 _lib = None
 EXPORTS = ("fp4_amax", "fp4_quantize", "fp4_dequantize", "fp4_rht16", "fp4_gemm",
            "fp4_gemm_ws", "fp4_gemm_workspace", "fp4_requantize_t", "fp4_act_quantize",
-           "fp4_act_backward",
+           "fp4_act_backward", "fp4_qk_norm_rope", "fp4_qk_norm_rope_backward",
+           "fp4_qk_norm_workspace", "fp4_kv_cache_write", "fp4_kv_cache_read",
+           "fp4_attention_decode", "fp4_attention_workspace",
            "fp4_status_string", "fp4_last_error")
 
 
@@ -106,6 +131,18 @@ def load_library(path=None):
     lib.fp4_gemm_workspace.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), i64, i64,
                                        i64, i32]
     lib.fp4_gemm_workspace.restype = i64
+    heads, norm, cache = (ctypes.POINTER(t) for t in (Heads, QKNormDesc, KVCacheDesc))
+    lib.fp4_qk_norm_rope.argtypes = [norm, heads, heads, vp, i64, i64, heads, heads, vp]
+    lib.fp4_qk_norm_rope_backward.argtypes = [norm, heads, heads, vp, i64, i64, heads, heads, heads,
+                                              heads, vp, vp, i32, vp, i64, vp]
+    lib.fp4_qk_norm_workspace.argtypes = [i64]
+    lib.fp4_kv_cache_write.argtypes = [cache, heads, heads, vp, i64, norm, vp, heads, heads, vp]
+    lib.fp4_kv_cache_read.argtypes = [cache, vp, i64, vp, vp, i32, vp]
+    lib.fp4_attention_decode.argtypes = [cache, heads, vp, i64, i64, vp, i64, ctypes.c_float, vp, i32,
+                                         vp, vp, i64, vp]
+    lib.fp4_attention_workspace.argtypes = [cache, i64, i64, i64]
+    lib.fp4_qk_norm_workspace.restype = lib.fp4_attention_workspace.restype = i64
+    lib.fp4_selftest_set_attention_splits.argtypes = [i32]
     lib.fp4_selftest_sweep.argtypes = [i32, vp, i32, vp, vp]
     lib.fp4_selftest_gemm_decode.argtypes = [i32, vp, vp]
     lib.fp4_selftest_set_geometry.argtypes = [i32, i32]
@@ -113,7 +150,9 @@ def load_library(path=None):
     for f in ("fp4_amax", "fp4_quantize", "fp4_quantize_dual", "fp4_dequantize", "fp4_rht16",
               "fp4_requantize_t", "fp4_act_quantize", "fp4_act_backward", "fp4_gemm", "fp4_gemm_ws",
               "fp4_selftest_sweep", "fp4_selftest_gemm_decode", "fp4_selftest_set_geometry",
-              "fp4_selftest_set_fp8_plan"):
+              "fp4_selftest_set_fp8_plan", "fp4_qk_norm_rope", "fp4_qk_norm_rope_backward",
+              "fp4_kv_cache_write", "fp4_kv_cache_read", "fp4_attention_decode",
+              "fp4_selftest_set_attention_splits"):
         getattr(lib, f).restype = ctypes.c_int
     lib.fp4_status_string.argtypes = [ctypes.c_int]
     lib.fp4_status_string.restype = ctypes.c_char_p
@@ -675,6 +714,330 @@ def _gemm_workspace(device, M, N, K, out_type, fmt_a, fmt_b, ld_a, ld_b):
                                                  out_type)
 
 
+# ------------------------------------------------- attention on a cache --
+HEAD_DIMS = (64, 128, 256)
+CACHE_FORMATS = (FP8_E4M3, MXFP8, MXFP4, NVFP4, UE5M3)
+PAIRINGS = {"half": 0, "interleaved": 1}
+
+
+def _heads(x, name, tokens=None, heads=None, head_dim=None):
+    """A bf16 [tokens, heads, head_dim] tensor, of any strides but the last, as
+    the library takes it."""
+    if x.dtype is not torch.bfloat16 or x.dim() != 3:
+        raise ValueError("%s must be a 3-D bfloat16 tensor [tokens, heads, head_dim]" % name)
+    t, h, d = x.shape
+    if (tokens is not None and t != tokens or heads is not None and h != heads
+            or head_dim is not None and d != head_dim):
+        raise ValueError("%s must be [%s, %s, %s], not %s" % (name, tokens, heads, head_dim, tuple(x.shape)))
+    st, sh, sd = x.stride()
+    if sd != 1:
+        raise ValueError("%s: the elements of a head must be contiguous" % name)
+    return Heads(x.data_ptr(), st if t > 1 else 0, sh if h > 1 else 0, h)
+
+
+def _index(x, name, n, device, dtype=torch.int64):
+    if x.dtype is not dtype or x.shape != (n,) or x.device != device or (n > 1 and x.stride(0) != 1):
+        raise ValueError("%s must be a contiguous %s [%d] tensor on %s" % (name, dtype, n, device))
+    return x.data_ptr()
+
+
+class QKNorm:
+    """RMS norm of each head of queries and keys, a weight, and the rotation of
+    their positions; either may be left out.
+
+    q_weight, k_weight: [head_dim], both bfloat16 or both float32 (None: no norm).
+    table: float32 [positions, rotary_dim], each row the cosines and then the sines
+    of rotary_dim / 2 angles (`attention.rotary_table`; None: no rotation); the first
+    rotary_dim elements of a head are turned.  style: which elements make a pair,
+    "half" (i and i + rotary_dim / 2) or "interleaved" (2 i and 2 i + 1).
+    """
+
+    def __init__(self, q_weight=None, k_weight=None, table=None, eps=1e-6, style="half"):
+        if style not in PAIRINGS:
+            raise ValueError("style must be one of %s" % (tuple(PAIRINGS),))
+        if (q_weight is None) != (k_weight is None):
+            raise ValueError("q_weight and k_weight are given together or not at all")
+        if q_weight is None and table is None:
+            raise ValueError("neither weights nor a table")
+        self.head_dim = None
+        for w in (q_weight, k_weight) if q_weight is not None else ():
+            if (w.dim() != 1 or w.dtype not in (torch.bfloat16, torch.float32) or w.dtype != q_weight.dtype
+                    or w.shape != q_weight.shape or w.device != q_weight.device or not w.is_contiguous()):
+                raise ValueError("the weights must be contiguous bfloat16 or float32 [head_dim] "
+                                 "tensors, alike")
+            self.head_dim = w.shape[0]
+        if table is not None and (table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous()
+                                  or table.shape[1] % 2):
+            raise ValueError("table must be a contiguous float32 [positions, rotary_dim] tensor")
+        if table is not None and q_weight is not None and table.device != q_weight.device:
+            raise ValueError("the weights and the table are on different devices")
+        self.q_weight, self.k_weight, self.table = q_weight, k_weight, table
+        self.eps, self.style = float(eps), style
+        self.device = (table if q_weight is None else q_weight).device
+        rows, dim = (0, 0) if table is None else table.shape
+        self._desc = QKNormDesc(_addr(q_weight), _addr(k_weight),
+                                int(q_weight is not None and q_weight.dtype == torch.float32), self.eps,
+                                _addr(table), rows, dim, PAIRINGS[style])
+        self._ref = ctypes.byref(self._desc)
+
+    def _check(self, x, positions, tokens):
+        """The address of the positions that rows x [tokens, heads, head_dim] have."""
+        if x.device != self.device or (self.head_dim is not None and x.shape[2] != self.head_dim):
+            raise ValueError("the norm is for heads of %s on %s" % (self.head_dim, self.device))
+        if self.table is None:
+            return None
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        return _index(positions, "positions", tokens, x.device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
+
+
+def _out_heads(out, like, name):
+    """(tensor, Heads) of an output for `like`: `out`, or a new dense one."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
+    elif out.device != like.device:
+        raise ValueError("%s is on %s, not on %s" % (name, out.device, like.device))
+    return out, _heads(out, name, *like.shape)
+
+
+def _ref(h):
+    return None if h is None else ctypes.byref(h)
+
+
+def qk_norm_rope(norm: QKNorm, q, k, positions=None, out=(None, None)):
+    """(q, k) normed and rotated, bf16 [tokens, heads, head_dim] each; either may
+    be None.  The inputs may be parts of one projection's output.  positions:
+    int64 [tokens], rows of the norm's table (one outside it gives NaN).
+    out: tensors to write, of any strides but the last, for q and k (the inputs
+    themselves, too)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are None")
+    tokens, _, d = first.shape if first.dim() == 3 else (None, None, None)
+    hq = None if q is None else _heads(q, "q", tokens, None, d)
+    hk = None if k is None else _heads(k, "k", tokens, None, d)
+    _same_device(first.device, k=k)
+    pos = norm._check(first, positions, tokens)
+    yq = yk = oq = ok = None
+    if q is not None:
+        yq, oq = _out_heads(out[0], q, "out[0]")
+    if k is not None:
+        yk, ok = _out_heads(out[1], k, "out[1]")
+    _launch("fp4_qk_norm_rope", load_library().fp4_qk_norm_rope, first.device, norm._ref, _ref(hq), _ref(hk),
+            pos, tokens, d, _ref(oq), _ref(ok))
+    return yq, yk
+
+
+def qk_norm_rope_backward(norm: QKNorm, q, k, positions, dq, dk, out=(None, None), weight_grads=True):
+    """The gradients (of q, of k, of q_weight, of k_weight) of `qk_norm_rope` at its
+    inputs q and k, for dq and dk, those of its outputs (bf16, like them).  Weight
+    gradients are float32 [head_dim], summed in a fixed order (None without a norm).
+    weight_grads: False for none, or a dense float32 [2, head_dim] tensor to which q's
+    and k's are added (its rows are what is returned)."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are None")
+    tokens, _, d = first.shape if first.dim() == 3 else (None, None, None)
+    hq = hk = hdq = hdk = gq = gk = oq = ok = None
+    if q is not None:
+        hq, hdq = _heads(q, "q", tokens, None, d), _heads(dq, "dq", *q.shape)
+        gq, oq = _out_heads(out[0], q, "out[0]")
+    if k is not None:
+        hk, hdk = _heads(k, "k", tokens, None, d), _heads(dk, "dk", *k.shape)
+        gk, ok = _out_heads(out[1], k, "out[1]")
+    dev = first.device
+    _same_device(dev, k=k, dq=dq if q is not None else None, dk=dk if k is not None else None)
+    pos = norm._check(first, positions, tokens)
+    wq = wk = ws = None
+    n = 0
+    add = isinstance(weight_grads, torch.Tensor)
+    if (add or weight_grads) and norm.q_weight is not None:
+        w = weight_grads if add else torch.empty((2, d), dtype=torch.float32, device=dev)
+        if w.dtype != torch.float32 or w.shape != (2, d) or not w.is_contiguous() or w.device != dev:
+            raise ValueError("weight_grads must be a dense float32 [2, %d] tensor on %s" % (d, dev))
+        wq, wk = w[0] if q is not None else None, w[1] if k is not None else None
+        n = _norm_workspace(dev, d)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    _launch("fp4_qk_norm_rope_backward", load_library().fp4_qk_norm_rope_backward, dev, norm._ref, _ref(hq),
+            _ref(hk), pos, tokens, d, _ref(hdq), _ref(hdk), _ref(oq), _ref(ok), _addr(wq), _addr(wk),
+            int(add), _addr(ws), n)
+    return gq, gk, wq, wk
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_workspace(device, head_dim):
+    with torch.cuda.device(device):
+        return load_library().fp4_qk_norm_workspace(head_dim)
+
+
+class KVCache:
+    """A paged cache of keys and values in one of the library's formats.
+
+    fmt: "fp8" (E4M3, a scale per 128 elements of a row), "mxfp8", "mxfp4" (per 32),
+    "nvfp4" or "ue5m3" (per 16, with tensor scales).  k_codes, v_codes: uint8
+    [pages, heads, page_size, bytes of a row]; k_scales, v_scales: uint8 [pages,
+    heads, blocks of a row, page_size]; V's strides those of K, and the last
+    dimension contiguous.  amax: float32 [2] on the device, of K and of V, from which
+    the tensor scales of "nvfp4" and "ue5m3" are made (fixed while the cache is in
+    use); target: their T.  Slot s is place s % page_size of page s // page_size.
+    """
+
+    def __init__(self, fmt, k_codes, k_scales, v_codes, v_scales, amax=None, target=448.0):
+        f = _fmt(fmt)
+        if f not in CACHE_FORMATS:
+            raise ValueError("a cache is 'fp8', 'mxfp8', 'mxfp4', 'nvfp4' or 'ue5m3'")
+        if k_codes.dim() != 4 or k_scales.dim() != 4:
+            raise ValueError("codes must be [pages, heads, page_size, bytes] and scales [pages, heads, "
+                             "blocks, page_size]")
+        pages, heads, page, width = k_codes.shape
+        d = width if f in (FP8_E4M3, MXFP8) else 2 * width
+        if d not in HEAD_DIMS:
+            raise ValueError("head_dim must be one of %s, not %d" % (HEAD_DIMS, d))
+        blocks = -(-d // BLOCK_LEN[f])
+        for name, t, shape, strides in (
+                ("k_codes", k_codes, k_codes.shape, k_codes), ("v_codes", v_codes, k_codes.shape, k_codes),
+                ("k_scales", k_scales, (pages, heads, blocks, page), k_scales),
+                ("v_scales", v_scales, (pages, heads, blocks, page), k_scales)):
+            if (t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape) or t.stride() != strides.stride()
+                    or t.stride(3) != 1 or t.device != k_codes.device):
+                raise ValueError("%s must be uint8 %s on %s, its last dimension contiguous and K's and "
+                                 "V's strides alike" % (name, tuple(shape), k_codes.device))
+        if f in (NVFP4, UE5M3):
+            if (amax is None or amax.dtype != torch.float32 or amax.shape != (2,) or not amax.is_contiguous()
+                    or amax.device != k_codes.device):
+                raise ValueError("amax must be a contiguous float32 [2] tensor on %s" % k_codes.device)
+        else:
+            amax = None
+        self.fmt, self.heads, self.head_dim, self.pages, self.page_size = f, heads, d, pages, page
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.amax, self.target, self.device = amax, float(target), k_codes.device
+
+        def strides(t, row):          # of a dimension of one entry: any that is valid
+            return [s if n > 1 else row for s, n in zip(t.stride()[:3], t.shape)]
+
+        self._desc = KVCacheDesc(f, heads, d, page, pages, k_codes.data_ptr(), k_scales.data_ptr(),
+                                 v_codes.data_ptr(), v_scales.data_ptr(), *strides(k_codes, width),
+                                 *strides(k_scales, page), _addr(amax), self.target)
+        self._ref = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, pages, page_size, heads, head_dim, fmt="mxfp8", device="cuda", amax=None, target=448.0):
+        """A cache whose pages are yet to be written."""
+        f = _fmt(fmt)
+        if f not in CACHE_FORMATS:
+            raise ValueError("a cache is 'fp8', 'mxfp8', 'mxfp4', 'nvfp4' or 'ue5m3'")
+        if head_dim not in HEAD_DIMS:
+            raise ValueError("head_dim must be one of %s, not %d" % (HEAD_DIMS, head_dim))
+        width = head_dim if f in (FP8_E4M3, MXFP8) else head_dim // 2
+        codes = (torch.empty((pages, heads, page_size, width), dtype=torch.uint8, device=device)
+                 for _ in range(2))
+        scales = (torch.empty((pages, heads, -(-head_dim // BLOCK_LEN[f]), page_size), dtype=torch.uint8,
+                              device=device) for _ in range(2))
+        k, v = codes
+        ks, vs = scales
+        return cls(f, k, ks, v, vs, amax, target)
+
+
+def kv_cache_write(cache: KVCache, k, v, slots, q=None, norm: QKNorm = None, positions=None, q_out=None):
+    """Encode the rows k and v (bf16 [tokens, heads, head_dim]) of new tokens into
+    their slots (int64 [tokens]; a negative one, or one behind the last page, is not
+    written; the others are distinct).
+
+    norm: k goes through it first, in the same pass, without a rounding between; with
+    q, q does too and comes back (bf16; into q_out, if given).  positions as in
+    `qk_norm_rope`.  Returns q's result, or None.
+    """
+    hk = _heads(k, "k", None, cache.heads, cache.head_dim)
+    tokens = k.shape[0]
+    hv = _heads(v, "v", tokens, cache.heads, cache.head_dim)
+    dev = cache.device
+    _same_device(dev, k=k, v=v, q=q)
+    at = _index(slots, "slots", tokens, dev)
+    if norm is None:
+        if q is not None:
+            raise ValueError("q needs a norm")
+        _launch("fp4_kv_cache_write", load_library().fp4_kv_cache_write, dev, cache._ref, ctypes.byref(hk),
+                ctypes.byref(hv), at, tokens, None, None, None, None)
+        return None
+    pos = norm._check(k, positions, tokens)
+    hq = oq = None
+    if q is not None:
+        hq = _heads(q, "q", tokens, None, cache.head_dim)
+        q_out, oq = _out_heads(q_out, q, "q_out")
+    _launch("fp4_kv_cache_write", load_library().fp4_kv_cache_write, dev, cache._ref, ctypes.byref(hk),
+            ctypes.byref(hv), at, tokens, norm._ref, pos, _ref(hq), _ref(oq))
+    return q_out if q is not None else None
+
+
+def kv_cache_read(cache: KVCache, slots, out_dtype=torch.bfloat16):
+    """(k, v): the values of slots (int64 [n], any order), [n, heads, head_dim] each,
+    bf16 or fp32; zeros for what is no slot of the cache."""
+    if out_dtype not in OUT_TYPES:
+        raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+    if slots.dim() != 1:
+        raise ValueError("slots must be an int64 [n] tensor")
+    n = slots.shape[0]
+    at = _index(slots, "slots", n, cache.device)
+    k, v = (torch.empty((n, cache.heads, cache.head_dim), dtype=out_dtype, device=cache.device)
+            for _ in range(2))
+    _launch("fp4_kv_cache_read", load_library().fp4_kv_cache_read, cache.device, cache._ref, at, n,
+            k.data_ptr(), v.data_ptr(), int(out_dtype == torch.float32))
+    return k, v
+
+
+def attention_decode(q, cache: KVCache, page_table, lens, scale=None, out=None, out_dtype=torch.bfloat16,
+                     return_lse=False):
+    """Attention of one new token per request over its cached tokens (its own
+    written first): q bf16 [requests, heads, head_dim], heads a multiple of the
+    cache's; page_table int32 [requests, width], entry i the page of tokens
+    i * page_size ..; lens int32 [requests].  scale: 1 / sqrt(head_dim) if None.
+
+    Returns [requests, heads, head_dim] (bf16, or float32 by out_dtype or `out`, which
+    is dense); zeros where a request has no tokens.  With return_lse also the float32
+    [requests, heads] log of each softmax's denominator (-inf without tokens).  Tokens
+    on a page that the cache does not have are left out.
+    """
+    hq = _heads(q, "q", None, None, cache.head_dim)
+    n, heads, d = q.shape
+    dev = cache.device
+    _same_device(dev, q=q, page_table=page_table)
+    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n
+            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 [%d, width] tensor, contiguous along its rows" % n)
+    at = _index(lens, "lens", n, dev, torch.int32)
+    if out is None:
+        out = torch.empty((n, heads, d), dtype=out_dtype, device=dev)
+    elif out.shape != q.shape or not out.is_contiguous() or out.device != dev:
+        raise ValueError("out must be a contiguous tensor of q's shape on its device")
+    if out.dtype not in OUT_TYPES:
+        raise ValueError("the output is float32 or bfloat16")
+    lse = torch.empty((n, heads), dtype=torch.float32, device=dev) if return_lse else None
+    width = page_table.shape[1]
+    size = _attention_workspace(dev, cache.fmt, cache.heads, d, cache.page_size, heads, n, width)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    _launch("fp4_attention_decode", load_library().fp4_attention_decode, dev, cache._ref, ctypes.byref(hq),
+            page_table.data_ptr(), page_table.stride(0) if n > 1 else 0, width, at, n,
+            d ** -0.5 if scale is None else float(scale), out.data_ptr(), OUT_TYPES[out.dtype], _addr(lse),
+            _addr(ws), size)
+    return (out, lse) if return_lse else out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_workspace(device, fmt, heads, head_dim, page_size, q_heads, requests, width):
+    """Bytes of workspace that a call of these sizes can use."""
+    some = 4096                        # any aligned address: none is read
+    c = KVCacheDesc(fmt, heads, head_dim, page_size, 1, some, some, some, some, 4096, 4096, 4096, 1024, 1024,
+                    1024, some, 448.0)
+    with torch.cuda.device(device):
+        return load_library().fp4_attention_workspace(ctypes.byref(c), q_heads, requests, width)
+
+
 # ------------------------------------------------------------- self-test --
 SWEEPS = {"e2m1_rne": 0, "e4m3_scale": 1, "ue5m3_scale": 2, "e2m1_sr": 3, "e4m3_elem": 4}
 
@@ -716,3 +1079,10 @@ def selftest_set_fp8_plan(tile_rows=0, splits=1):
     _check(load_library().fp4_selftest_set_fp8_plan(int(tile_rows), int(splits)),
            "fp4_selftest_set_fp8_plan")
     _gemm_workspace.cache_clear()
+
+
+def selftest_set_attention_splits(splits=0):
+    """Parts that attention shares a request's tokens among (0: chosen by size)."""
+    _check(load_library().fp4_selftest_set_attention_splits(int(splits)),
+           "fp4_selftest_set_attention_splits")
+    _attention_workspace.cache_clear()

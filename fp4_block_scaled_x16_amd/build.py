@@ -22,8 +22,9 @@ LIB_NAME = "libfp4_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 # (source, object name, extra flags): gemm_nv.hip is built once per
-# block-scale format and gemm_nv_dma.hip once per format and tile height, so
-# the kernel families compile in parallel
+# block-scale format, gemm_nv_dma.hip once per format and tile height and
+# attention.hip once per format of the cache, so the kernel families compile in
+# parallel
 SOURCES = [("quant.hip", "quant", []), ("quant_rowscope.hip", "quant_rowscope", []),
            ("quant_mxfp8.hip", "quant_mxfp8", []),
            ("gemm.hip", "gemm", [])] + [
@@ -33,6 +34,9 @@ SOURCES = [("quant.hip", "quant", []), ("quant_rowscope.hip", "quant_rowscope", 
     ("quant_fp8.hip", "quant_fp8", []), ("act_fp8.hip", "act_fp8", []),
     ("gemm_fp8.hip", "gemm_fp8", []), ("gemm_fp8_rows.hip", "gemm_fp8_rows", []),
     ("fp8_api.cpp", "fp8_api", []),
+    ("qk_rows.hip", "qk_rows", []), ("kv_cache.hip", "kv_cache", []),
+    ("attention_join.hip", "attention_join", []), ("kv_api.cpp", "kv_api", [])] + [
+    ("attention.hip", "attention_%d" % f, ["-DFP4_KV_FMT=%d" % f]) for f in range(5)] + [
     ("gemm_mx.hip", "gemm_mx", []), ("gemm_mx_dma.hip", "gemm_mx_dma", []),
     ("selftest.hip", "selftest", []), ("fp4_api.cpp", "fp4_api", [])]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -88,7 +92,7 @@ SANITIZED_LIB = os.path.join(BUILD, "sanitize", "libfp4_mi355x_sanitized.so")
 
 
 def build_sanitized():
-    """The C ABI's host code (fp4_api.cpp, fp8_api.cpp: every argument check) built as
+    """The C ABI's host code (fp4_api.cpp, fp8_api.cpp, kv_api.cpp: every argument check) built as
     plain host C++ with AddressSanitizer and UndefinedBehaviorSanitizer
     (every UB report fatal), linked against host-only stand-ins for the
     kernel launchers (csrc/sanitize_stubs.cpp).  Loaded in place of the real
@@ -100,7 +104,7 @@ def build_sanitized():
              "-fsanitize=address,undefined", "-fno-sanitize-recover=undefined",
              "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I" + os.path.join(ROOT, "include")]
     objs = []
-    for src in ("fp4_api.cpp", "fp8_api.cpp", "sanitize_stubs.cpp"):
+    for src in ("fp4_api.cpp", "fp8_api.cpp", "kv_api.cpp", "sanitize_stubs.cpp"):
         obj = os.path.join(out_dir, src.replace(".cpp", ".o"))
         _run([CLANG] + flags + ["-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)

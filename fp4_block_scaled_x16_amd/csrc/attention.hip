@@ -1,0 +1,453 @@
+// Attention of one new token per request over its pages of a quantized
+// key-value cache:  out = softmax(scale q K^T) V  over the request's tokens.
+//
+// Bound by reading the codes once.  A workgroup of four waves has one request,
+// one key head, up to 16 of the query heads that share it, and a part of the
+// request's tokens; its waves take turns at tiles of 32 tokens, each with a
+// running maximum and sum of its own, and meet in LDS at the end.  Where a
+// request has several parts, their sums go to the caller's workspace and
+// k_attention_join brings them together in order (no atomics: the same bits
+// every time).
+//
+// Codes go from global memory into registers and, widened, straight into MFMA
+// operands: no byte of the cache is used twice, so nothing is staged in LDS.
+//   scores^T [token, head] = K q^T.  Lane (c, g) (c = lane % 16, g = lane / 16)
+//     has token c of each half tile, elements g D/4 .. of its row; q's operand
+//     is laid out to match.  It gets back tokens 4 g .. 4 g + 3 of head c.
+//   out^T [element, head] += V^T p^T.  The four scores of each half are the
+//     lane's own part of p's operand: p never leaves its lane.  V^T's operand
+//     holds elements of 8 tokens (4 g .. of each half), so a lane loads elements
+//     c D/16 .. of those 8 rows and pairs tokens with byte permutes.
+// FP8, MXFP8 and MXFP4 are widened to bf16, their power-of-two scales applied by
+// the same convert; NVFP4 and UE5M3 to fp16, in which code times block scale is
+// exact (UE5M3 times 2^-5), q's row being scaled into fp16's range by a power of
+// two.  Either way the operands are exact.  p is split into a rounded part and
+// what that leaves (bf16: 2^-17 of p; fp16: 2^-22), since rounding it once would
+// add as much error as the output's own: for up to 8 heads the second part takes
+// the other 8 of the matrix's 16 columns, for more a second MFMA.
+#include "attention_common.hpp"
+
+using namespace kvdev;
+using namespace fp4attn;
+
+namespace {
+
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 halfx8 __attribute__((ext_vector_type(8)));
+typedef _Float16 halfx2 __attribute__((ext_vector_type(2)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+// A running maximum is raised only when a score exceeds it by this many powers
+// of two: what it guards against is overflow, and until then nothing has to be
+// rescaled.
+constexpr float kSlack = 8.0f;
+
+template <bool F16>
+__device__ __forceinline__ floatx4 mfma(uintx4 a, uintx4 b, floatx4 c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(halfx8, a),
+                                                  __builtin_bit_cast(halfx8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Two floats as bf16 (fp16), to nearest even.
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (F16)
+    return __builtin_bit_cast(uint32_t, halfx2{static_cast<_Float16>(x), static_cast<_Float16>(y)});
+  else
+    return fp8dev::pack_bf16(x, y);
+}
+template <bool F16>
+__device__ __forceinline__ float unpack_lo(uint32_t w) {
+  if constexpr (F16) return static_cast<float>(__builtin_bit_cast(halfx2, w)[0]);
+  return __uint_as_float(w << 16);
+}
+template <bool F16>
+__device__ __forceinline__ float unpack_hi(uint32_t w) {
+  if constexpr (F16) return static_cast<float>(__builtin_bit_cast(halfx2, w)[1]);
+  return __uint_as_float(w & 0xFFFF0000u);
+}
+
+// Codes of pair P of a word (8-bit: 0, 1; 4-bit: 0 .. 3) widened: `s` is the
+// block scale, as a float (bf16) or as an fp16 pair of which HALF is it.
+template <int FMT, int P, int HALF>
+__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t s) {
+  using F = KvTraits<FMT>;
+  if constexpr (F::kTwoLevel) {
+    const halfx2 sp = __builtin_bit_cast(halfx2, s);
+    const halfx2 v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, P);
+    return __builtin_bit_cast(uint32_t, v * (HALF ? halfx2{sp[1], sp[1]} : halfx2{sp[0], sp[0]}));
+  } else if constexpr (F::kBits == 8) {
+    return __builtin_bit_cast(uint32_t,
+                              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, __uint_as_float(s), P == 1));
+  } else {
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, __uint_as_float(s), P));
+  }
+}
+
+// Scale B of a word of four scale codes as widen2 takes it: a float's bits, or
+// the fp16 pair that holds it in half B % 2.
+template <int FMT, int B>
+__device__ __forceinline__ uint32_t scale_for(uint32_t word) {
+  if constexpr (KvTraits<FMT>::kTwoLevel)
+    return fp4gemm::scale_pair_f16<KvTraits<FMT>::kDev, B & 2>(word);
+  else
+    return ((word >> (8 * B)) & 0xFFu) << 23;
+}
+
+// N bytes (2, 4, 8 or a multiple of 16) into words.
+template <int N>
+struct Raw {
+  uint32_t w[N < 4 ? 1 : N / 4];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (N == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (N == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) {
+        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+      }
+    }
+  }
+};
+
+template <int FMT, int D>
+struct Shape {
+  using F = KvTraits<FMT>;
+  static constexpr int kSteps = D / 32;                       // MFMAs over a row of K
+  static constexpr int kKBytes = D / 4 * F::kBits / 8;        // of a lane's part of a row of K
+  static constexpr int kKBlocks = D / 4 <= F::kBlock ? 1 : D / 4 / F::kBlock;
+  static constexpr int kElems = D / 16;                       // of a lane's part of a row of V
+  static constexpr int kVBytes = kElems * F::kBits / 8;
+};
+
+// One half (16 tokens) of a tile of K as a lane loads it.
+template <int FMT, int D>
+struct KHalf {
+  using S = Shape<FMT, D>;
+  Raw<S::kKBytes> w;
+  uint32_t s[S::kKBlocks];
+};
+template <int FMT, int D>
+struct VHalf {
+  using S = Shape<FMT, D>;
+  Raw<S::kVBytes> w[4];
+  uint32_t s;                   // scale codes of the four tokens
+};
+
+// Page and first place of a half, and how many of its tokens there are.
+struct HalfPos {
+  int64_t page;
+  int place, n;
+};
+
+template <int FMT, int D, int NP>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4lib::AttnArgs a) {
+  using F = KvTraits<FMT>;
+  using S = Shape<FMT, D>;
+  constexpr bool kF16 = F::kTwoLevel;
+  constexpr int kHeads = NP == 1 ? 8 : 16;                   // query heads of a workgroup
+  // fp16 holds p down to 2^-24: its largest, 2^kSlack, is moved up by 2^7
+  constexpr float kShift = kF16 ? 7.0f : 0.0f;
+  __shared__ float meet[kWaves - 1][S::kElems * 4 + 2][64];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int group = a.q.heads / a.cache.heads;               // query heads of a key head
+  const int tiles = (group + kHeads - 1) / kHeads;
+  int id = blockIdx.x;
+  const int split = id % a.splits;
+  id /= a.splits;
+  const int tile = id % tiles;
+  id /= tiles;
+  const int kv = id % a.cache.heads, request = id / a.cache.heads;
+
+  const int len = tokens_of(a, request), per = part_tokens(len, a.splits);
+  const int begin = split * per, end = min(len, begin + per);
+  const int first = kv * group + tile * kHeads, heads = min(kHeads, group - tile * kHeads);
+  if (begin >= end && split > 0) return;
+  const int col = NP == 1 ? c & 7 : c;
+  const bool mine = col < heads;
+  const int64_t row = static_cast<int64_t>(request) * a.q.heads + first + (mine ? col : 0);
+
+  // q, elements g D/4 .. of the lane's head: the operand of each step.
+  uintx4 q[S::kSteps];
+  float factor = a.scale * kLog2e;
+  {
+    const uint16_t* p = a.q.x + request * a.q.token + static_cast<int64_t>(first + (mine ? col : 0)) * a.q.head +
+                        g * (D / 4);
+#pragma unroll
+    for (int k = 0; k < S::kSteps; ++k) {
+      const uint4 w = *reinterpret_cast<const uint4*>(p + 8 * k);
+      q[k] = uintx4{w.x, w.y, w.z, w.w};
+    }
+    if constexpr (kF16) {
+      float s_enc, s_dec;
+      tensor_scales<FMT>(a.cache, 0, s_enc, s_dec);
+      uint32_t big = 0;
+#pragma unroll
+      for (int k = 0; k < S::kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          big = fp8dev::umax(big, fp8dev::umax((q[k][i] << 16) & 0x7FFFFFFFu, q[k][i] & 0x7FFF0000u));
+      big = fp8dev::umax(big, __shfl_xor(big, 16, 64));
+      big = fp8dev::umax(big, __shfl_xor(big, 32, 64));
+      const int e = 14 - (static_cast<int>(big >> 23) - 127);      // largest element to 2^14 .. 2^15
+#pragma unroll
+      for (int k = 0; k < S::kSteps; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          q[k][i] = pack2<true>(__builtin_ldexpf(unpack_lo<false>(q[k][i]), e),
+                                __builtin_ldexpf(unpack_hi<false>(q[k][i]), e));
+      factor = __builtin_ldexpf(factor * s_dec, (FMT == kKvUe4 ? 5 : 0) - e);
+    }
+  }
+
+  floatx4 acc[S::kElems];
+#pragma unroll
+  for (int i = 0; i < S::kElems; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+  float top = -__builtin_inff(), total = 0.0f;
+
+  const int32_t* table = a.table + request * a.table_stride;
+  const int mask = (1 << a.cache.page_shift) - 1;
+  auto half_at = [&](int t) {
+    HalfPos h{0, t & mask, end - t < 0 ? 0 : end - t > 16 ? 16 : end - t};
+    if (h.n > 0) {
+      const int page = table[t >> a.cache.page_shift];
+      if (page >= 0 && page < a.cache.pages) h.page = page;
+      else h.n = 0;                                           // no such page: its tokens are masked
+    }
+    return h;
+  };
+  const uint8_t* kc = a.cache.codes[0] + kv * a.cache.head + g * S::kKBytes;
+  const uint8_t* vc = a.cache.codes[1] + kv * a.cache.head + c * S::kVBytes;
+  const uint8_t* ks = a.cache.scales[0] + kv * a.cache.s_head + (g * (D / 4) / F::kBlock) * a.cache.s_block;
+  const uint8_t* vs = a.cache.scales[1] + kv * a.cache.s_head + (c * S::kElems / F::kBlock) * a.cache.s_block;
+  auto load_k = [&](KHalf<FMT, D>& k, const HalfPos& h) {
+    k.w.load(kc + h.page * a.cache.page + (h.place + c) * a.cache.token);
+#pragma unroll
+    for (int b = 0; b < S::kKBlocks; ++b)
+      k.s[b] = ks[h.page * a.cache.s_page + h.place + c + b * a.cache.s_block];
+  };
+  auto load_v = [&](VHalf<FMT, D>& v, const HalfPos& h) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v.w[j].load(vc + h.page * a.cache.page + (h.place + 4 * g + j) * a.cache.token);
+    v.s = *reinterpret_cast<const uint32_t*>(vs + h.page * a.cache.s_page + h.place + 4 * g);
+    // what is not there: zero codes and scales, whatever the memory holds
+    if (h.n < 16) {
+      const int n = h.n - 4 * g;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j >= n)
+#pragma unroll
+          for (auto& w : v.w[j].w) w = 0;
+      v.s &= n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
+    }
+  };
+
+  for (int t = begin + wave * kTile; t < end; t += kWaves * kTile) {
+    const HalfPos h[2] = {half_at(t), half_at(t + 16)};
+    KHalf<FMT, D> k[2];
+    VHalf<FMT, D> v[2];
+    load_k(k[0], h[0]);
+    load_k(k[1], h[1]);
+    load_v(v[0], h[0]);
+    load_v(v[1], h[1]);
+
+    float x[8];
+    float best = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < S::kSteps; ++n) {
+        // elements 8 n .. of the lane's part lie in one block
+        const uint32_t sc = scale_for<FMT, 0>(k[i].s[8 * n / F::kBlock < S::kKBlocks ? 8 * n / F::kBlock : 0]);
+        uintx4 w;
+        if constexpr (F::kBits == 8)
+          w = uintx4{widen2<FMT, 0, 0>(k[i].w.w[2 * n], sc), widen2<FMT, 1, 0>(k[i].w.w[2 * n], sc),
+                     widen2<FMT, 0, 0>(k[i].w.w[2 * n + 1], sc), widen2<FMT, 1, 0>(k[i].w.w[2 * n + 1], sc)};
+        else
+          w = uintx4{widen2<FMT, 0, 0>(k[i].w.w[n], sc), widen2<FMT, 1, 0>(k[i].w.w[n], sc),
+                     widen2<FMT, 2, 0>(k[i].w.w[n], sc), widen2<FMT, 3, 0>(k[i].w.w[n], sc)};
+        s = mfma<kF16>(w, q[n], s);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[4 * i + j] = 4 * g + j < h[i].n ? s[j] * factor : -__builtin_inff();
+        best = fmaxf(best, x[4 * i + j]);
+      }
+    }
+
+    if (__any(best > top + kSlack)) {
+      best = fmaxf(best, __shfl_xor(best, 16, 64));
+      best = fmaxf(best, __shfl_xor(best, 32, 64));
+      const float to = fmaxf(top, best);
+      const float by = to == top ? 1.0f : __builtin_amdgcn_exp2f(top - to);
+      top = to;
+      total *= by;
+#pragma unroll
+      for (int i = 0; i < S::kElems; ++i) acc[i] *= by;
+    }
+    const float from = top == -__builtin_inff() ? 0.0f : top - kShift;
+    uintx4 p, rest;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float u = __builtin_amdgcn_exp2f(x[2 * j] - from), w = __builtin_amdgcn_exp2f(x[2 * j + 1] - from);
+      total += u + w;
+      const uint32_t hi = pack2<kF16>(u, w);
+      const uint32_t lo = pack2<kF16>(u - unpack_lo<kF16>(hi), w - unpack_hi<kF16>(hi));
+      if constexpr (NP == 1) {
+        p[j] = c < 8 ? hi : lo;
+      } else {
+        p[j] = hi;
+        rest[j] = lo;
+      }
+    }
+
+    // V: pairs of elements of the eight tokens, then pairs of tokens
+    uint32_t w[8][S::kElems / 2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t sc[4] = {scale_for<FMT, 0>(v[i].s), scale_for<FMT, 1>(v[i].s), scale_for<FMT, 2>(v[i].s),
+                              scale_for<FMT, 3>(v[i].s)};
+      auto widen = [&](auto jc) {
+        constexpr int j = decltype(jc)::value;
+#pragma unroll
+        for (int e = 0; e < S::kElems / 2; ++e) {
+          const uint32_t word = v[i].w[j].w[F::kBits == 8 ? e / 2 : e / 4];
+          uint32_t o;
+          if constexpr (F::kBits == 8) {
+            o = e % 2 ? widen2<FMT, 1, j & 1>(word, sc[j]) : widen2<FMT, 0, j & 1>(word, sc[j]);
+          } else {
+            o = e % 4 == 0   ? widen2<FMT, 0, j & 1>(word, sc[j])
+                : e % 4 == 1 ? widen2<FMT, 1, j & 1>(word, sc[j])
+                : e % 4 == 2 ? widen2<FMT, 2, j & 1>(word, sc[j])
+                             : widen2<FMT, 3, j & 1>(word, sc[j]);
+          }
+          w[4 * i + j][e] = o;
+        }
+      };
+      widen(Const<0>());
+      widen(Const<1>());
+      widen(Const<2>());
+      widen(Const<3>());
+    }
+#pragma unroll
+    for (int e = 0; e < S::kElems; ++e) {
+      const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
+      uintx4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2], sel);
+      acc[e] = mfma<kF16>(o, p, acc[e]);
+      if constexpr (NP == 2) acc[e] = mfma<kF16>(o, rest, acc[e]);
+    }
+  }
+
+  // the four waves' sums, lane by lane, in the first
+  total += __shfl_xor(total, 16, 64);
+  total += __shfl_xor(total, 32, 64);
+  if (wave) {
+    float(*to)[64] = meet[wave - 1];
+#pragma unroll
+    for (int e = 0; e < S::kElems; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[4 * e + i][lane] = acc[e][i];
+    to[4 * S::kElems][lane] = top;
+    to[4 * S::kElems + 1][lane] = total;
+  }
+  __syncthreads();
+  if (wave) return;
+  float all = top;
+#pragma unroll
+  for (int w = 0; w < kWaves - 1; ++w) all = fmaxf(all, meet[w][4 * S::kElems][lane]);
+  const float ref = all == -__builtin_inff() ? 0.0f : all;
+  {
+    const float by = __builtin_amdgcn_exp2f(top - ref);
+    total *= by;
+#pragma unroll
+    for (int e = 0; e < S::kElems; ++e) acc[e] *= by;
+  }
+#pragma unroll
+  for (int w = 0; w < kWaves - 1; ++w) {
+    const float by = __builtin_amdgcn_exp2f(meet[w][4 * S::kElems][lane] - ref);
+    total += by * meet[w][4 * S::kElems + 1][lane];
+#pragma unroll
+    for (int e = 0; e < S::kElems; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[e][i] += by * meet[w][4 * e + i][lane];
+  }
+  if constexpr (NP == 1) {
+    // columns 8 .. hold the sums with what rounding p left
+#pragma unroll
+    for (int e = 0; e < S::kElems; ++e)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[e][i] += __uint_as_float(dpp<0x128>(__float_as_uint(acc[e][i])));     // row_ror:8
+    if (c >= 8) return;
+  }
+  if (!mine) return;
+
+  // lane (c, g) has elements (4 g + i) D/16 + e
+  const bool whole = begin == 0 && end >= len;
+  float s_enc, s_dec;
+  tensor_scales<FMT>(a.cache, 1, s_enc, s_dec);
+  if constexpr (FMT == kKvUe4) s_dec *= 32.0f;
+  if (whole) {
+    const float by = total > 0.0f || total != total ? s_dec / total : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t at = row * D + (4 * g + i) * S::kElems;
+#pragma unroll
+      for (int e = 0; e < S::kElems; e += 4) {
+        const float o[4] = {acc[e][i] * by, acc[e + 1][i] * by, acc[e + 2][i] * by, acc[e + 3][i] * by};
+        if (a.out_f32)
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + e) = make_float4(o[0], o[1], o[2], o[3]);
+        else
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + e) =
+              make_uint2(fp8dev::pack_bf16(o[0], o[1]), fp8dev::pack_bf16(o[2], o[3]));
+      }
+    }
+    if (a.lse && g == 0) a.lse[row] = (all + __builtin_log2f(total) - kShift) / kLog2e;
+  } else {
+    // sums with V's tensor scale; the maximum and the sum behind them
+    float* o = a.part + (row * a.splits + split) * (D + 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < S::kElems; e += 2)
+        *reinterpret_cast<float2*>(o + (4 * g + i) * S::kElems + e) =
+            make_float2(acc[e][i] * s_dec, acc[e + 1][i] * s_dec);
+    if (g == 0) *reinterpret_cast<float2*>(o + D) = make_float2(all - kShift, total);
+  }
+}
+
+}  // namespace
+
+namespace fp4lib {
+
+// One translation unit per format of the cache.
+template <>
+hipError_t launch_attention_fmt<FP4_KV_FMT>(const AttnArgs& a, uint32_t grid, hipStream_t s) {
+  return with_dim(a.cache.head_dim, [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (a.q.heads / a.cache.heads <= 8)
+      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, 1>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+    else
+      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, 2>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace fp4lib

@@ -1,4 +1,4 @@
-// Host-only stand-ins for the kernel launchers, linked with fp4_api.cpp and fp8_api.cpp
+// Host-only stand-ins for the kernel launchers, linked with fp4_api.cpp, fp8_api.cpp and kv_api.cpp
 // into the AddressSanitizer / UndefinedBehaviorSanitizer build of the C ABI's
 // validation code (build.py build_sanitized).  That build runs the
 // argument-checking tests, which never reach a device: any call that passes
@@ -6,6 +6,7 @@
 #include <hip/hip_runtime.h>
 
 #include "fp4_internal.hpp"
+#include "kv_internal.hpp"
 
 namespace fp4lib {
 
@@ -60,5 +61,12 @@ hipError_t launch_selftest_sweep(int, const uint32_t*, int, uint64_t*, hipStream
   return hipErrorNoDevice;
 }
 hipError_t launch_selftest_gemm_decode(int, uint16_t*, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_qk_rows(const QkRowsArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_qk_grad(const QkGradArgs&, hipStream_t) { return hipErrorNoDevice; }
+int64_t qk_grad_workspace(int head_dim) { return 4096 * static_cast<int64_t>(head_dim); }
+hipError_t launch_kv_read(const KvReadArgs&, hipStream_t) { return hipErrorNoDevice; }
+hipError_t launch_attention(const AttnArgs&, hipStream_t) { return hipErrorNoDevice; }
+int64_t attention_workspace(const AttnArgs&) { return 0; }
+void set_attention_splits(int) {}
 
 }  // namespace fp4lib

@@ -506,6 +506,171 @@ fp4_status fp4_act_backward(fp4_act act, const uint8_t* h_codes, const uint8_t* 
                             uint8_t* a_t_scales, uint16_t* dh, int64_t ld_dh, uint16_t* a,
                             int64_t ld_a, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Attention on a quantized key-value cache: what lies between the projection
+ * to queries, keys and values and the output projection when a token is
+ * generated, and the norm and rotation of queries and keys in training too.
+ *
+ * Rows of bf16 heads: element d of head h of token t at x[t * token_stride +
+ * h * head_stride + d] (strides in elements, multiples of 8; x 16-byte
+ * aligned).  Heads of one projection's output, beside each other, are such
+ * rows.  head_dim is 64, 128 or 256. */
+typedef struct {
+  uint16_t* x;              /* device; not written where it is an input */
+  int64_t token_stride;
+  int64_t head_stride;
+  int64_t heads;
+} fp4_heads;
+
+/* Norm and rotation of queries and keys (host struct of device pointers):
+ *   r = (mean_d x[d]^2 + eps)^(-1/2);  z = x r w   (w: q_weight or k_weight)
+ *   y = z with its pairs (a, b) turned: (a cos - b sin, b cos + a sin)
+ * Pair i of the first rotary_dim elements is (i, i + rotary_dim / 2), or with
+ * interleaved (2 i, 2 i + 1); the others stay z.  cos and sin are those of row
+ * p of the table, p the token's position: its first rotary_dim / 2 entries and
+ * the ones behind them.  Everything in fp32, rounded once. */
+typedef struct {
+  const void* q_weight;     /* [head_dim] bf16, or fp32 with weight_f32; 16-byte aligned; */
+  const void* k_weight;     /* both NULL: no norm                                          */
+  int weight_f32;
+  float eps;                /* finite, >= 0 */
+  const float* table;       /* [table_rows, rotary_dim], 16-byte aligned; NULL: no rotation */
+  int64_t table_rows;
+  int rotary_dim;           /* a multiple of 16, up to head_dim */
+  int interleaved;
+} fp4_qk_norm;
+
+/*
+ * fp4_qk_norm_rope -- q_out and k_out: q and k normed and rotated.
+ *   norm       weights, table or both
+ *   q, k       inputs; k may be NULL (q too, not both), and its output then is.
+ *              Outputs have the input's number of heads, rows that do not
+ *              overlap, and may be the inputs themselves.
+ *   positions  device int64[tokens]: rows of the table (NULL without a table).
+ *              A position outside the table makes the token's rotated elements NaN.
+ */
+fp4_status fp4_qk_norm_rope(const fp4_qk_norm* norm /* host */, const fp4_heads* q /* host */,
+                            const fp4_heads* k /* host */, const int64_t* positions, int64_t tokens,
+                            int64_t head_dim, const fp4_heads* q_out /* host */,
+                            const fp4_heads* k_out /* host */, void* stream);
+
+/*
+ * fp4_qk_norm_rope_backward -- the gradients of q and k from those of q_out
+ * and k_out (dq, dk), and of the weights:
+ *   dz = dy turned back;  dw = sum over tokens and heads of dz x r;  g = dz w;
+ *   dx = r (g - x r^2 mean_d(g x))
+ *   q, k       the inputs of fp4_qk_norm_rope.
+ *   dq_in, dk_in  outputs, bf16; may be dq and dk, or q and k, themselves.
+ *   dq_weight, dk_weight  device float[head_dim], written, or with accumulate added
+ *              to; NULL where not wanted (and without a norm).  Summed in a fixed order.
+ *   workspace  device, 16-byte aligned, fp4_qk_norm_workspace(head_dim) bytes;
+ *              its contents are of no account, and calls that may run at the same
+ *              time need one each.  NULL where no weight's gradient is wanted.
+ */
+fp4_status fp4_qk_norm_rope_backward(const fp4_qk_norm* norm /* host */, const fp4_heads* q /* host */,
+                                     const fp4_heads* k /* host */, const int64_t* positions,
+                                     int64_t tokens, int64_t head_dim, const fp4_heads* dq /* host */,
+                                     const fp4_heads* dk /* host */, const fp4_heads* dq_in /* host */,
+                                     const fp4_heads* dk_in /* host */, float* dq_weight,
+                                     float* dk_weight, int accumulate, void* workspace,
+                                     int64_t workspace_bytes, void* stream);
+int64_t fp4_qk_norm_workspace(int64_t head_dim);
+
+/* A paged cache of keys and values (host struct of device pointers).  It has
+ * `pages` pages of page_size places; slot s is place s % page_size of page
+ * s / page_size.  A slot holds, for each head, a row of head_dim codes of K and
+ * one of V, encoded as fp4_quantize encodes a ROWWISE 1D matrix of head_dim columns:
+ *   FP8_E4M3      a byte per element, a scale per 128 (a row of 64 is one block)
+ *   MXFP8         a byte per element, a scale per 32
+ *   MXFP4         two codes per byte, a scale per 32
+ *   NVFP4, UE5M3  two codes per byte, a scale per 16 and a tensor scale from
+ *                 `amax` (as with amax_given) and `target`
+ * RNE, scales to nearest.  Codes of place p of head h of page g begin at
+ * codes + g * page_stride + h * head_stride + p * token_stride (bytes); the scale
+ * of its block j lies at scales + g * scale_page_stride + h * scale_head_stride +
+ * j * scale_block_stride + p. */
+typedef struct {
+  fp4_format format;
+  int heads;
+  int head_dim;             /* 64, 128 or 256 */
+  int page_size;            /* a power of two, 16 .. 1024 */
+  int64_t pages;            /* at least 1 */
+  uint8_t* k_codes;         /* all four 16-byte aligned */
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  int64_t page_stride;      /* strides positive, of codes multiples of 16 (one page's */
+  int64_t head_stride;      /* and of its heads' offsets below 2^31) */
+  int64_t token_stride;
+  int64_t scale_page_stride;   /* multiples of 16 */
+  int64_t scale_head_stride;
+  int64_t scale_block_stride;
+  const float* amax;        /* device float[2]: of K, of V (NVFP4, UE5M3) */
+  float target;             /* T of the tensor scales 6 T / amax; finite, > 0 */
+} fp4_kv_cache;
+
+/*
+ * fp4_kv_cache_write -- the rows of `tokens` new tokens, encoded into their
+ * slots.
+ *   k, v    [tokens] rows of the cache's heads.
+ *   slots   device int64[tokens].  A token whose slot is negative or behind the
+ *           last page is not written.  The others' slots are distinct: where two
+ *           tokens name one slot, it may end with bytes of either.
+ *   norm    NULL, or what k goes through first (in fp32, encoded from there with
+ *           one rounding), in the same pass; with it q, which comes out as
+ *           q_out in bf16 (both NULL: k alone), and positions (all as in
+ *           fp4_qk_norm_rope; q is turned whatever the slot).
+ */
+fp4_status fp4_kv_cache_write(const fp4_kv_cache* cache /* host */, const fp4_heads* k /* host */,
+                              const fp4_heads* v /* host */, const int64_t* slots, int64_t tokens,
+                              const fp4_qk_norm* norm /* host */, const int64_t* positions,
+                              const fp4_heads* q /* host */, const fp4_heads* q_out /* host */,
+                              void* stream);
+
+/*
+ * fp4_kv_cache_read -- the values of n slots, as fp4_dequantize forms them.
+ *   slots   device int64[n], any order; one that is no slot of the cache gives zeros.
+ *   k, v    [n, heads, head_dim], 16-byte aligned, fp32 if out_fp32, else bf16;
+ *           one of them may be NULL.
+ */
+fp4_status fp4_kv_cache_read(const fp4_kv_cache* cache /* host */, const int64_t* slots, int64_t n,
+                             void* k, void* v, int out_fp32, void* stream);
+
+/*
+ * fp4_attention_decode -- attention of one new token per request:
+ *   out[r, h] = sum_t p_t v_t,  p = softmax over t of scale * q[r, h] . k_t,
+ * t over the request's first lens[r] tokens, k and v those of key head
+ * h / (q->heads / cache->heads).
+ *   q        rows of `requests` tokens; q->heads a multiple of the cache's.
+ *   page_table  device int32: token t of request r lies in page
+ *            page_table[r * table_stride + t / page_size] (any stride, 0 too: a
+ *            table shared by all), place t % page_size; table_width entries per
+ *            request, of which those behind its length are not read.  Tokens of a
+ *            page that the cache does not have are left out.
+ *   lens     device int32[requests], the new token counted (it is written first).
+ *            0 or less: no tokens.  More than the table has room for: that many.
+ *   out      [requests, q->heads, head_dim], 16-byte aligned; zeros for a request
+ *            without tokens.
+ *   lse      NULL, or float[requests, q->heads]: log sum_t exp(scale q . k_t), with
+ *            which results over parts of a context can be joined; -infinity
+ *            without tokens.
+ *   workspace  device, 16-byte aligned: with fp4_attention_workspace bytes a
+ *            request's tokens are shared among workgroups and joined in order by
+ *            a second kernel; with less, or NULL, they are not.  Contents of no
+ *            account; calls that may run at the same time need one each.
+ * Operands are exact (NVFP4 and UE5M3: q to 2^-38 of its row's largest element),
+ * sums, maxima and p in fp32; p is rounded to 2^-17 of itself or less before it
+ * meets V (NVFP4 and UE5M3: or to 2^-32 of the largest, whichever is more).
+ * fp4_attention_workspace: 0 where none is used and for invalid arguments.
+ */
+fp4_status fp4_attention_decode(const fp4_kv_cache* cache /* host */, const fp4_heads* q /* host */,
+                                const int32_t* page_table, int64_t table_stride, int64_t table_width,
+                                const int32_t* lens, int64_t requests, float scale, void* out,
+                                fp4_out_type out_type, float* lse, void* workspace,
+                                int64_t workspace_bytes, void* stream);
+int64_t fp4_attention_workspace(const fp4_kv_cache* cache /* host */, int64_t q_heads,
+                                int64_t requests, int64_t table_width);
+
 /* Static description of a status code. */
 const char* fp4_status_string(fp4_status status);
 

@@ -112,6 +112,16 @@ fp4_status fp4_selftest_set_geometry(int max_workgroups, int gemm_tile_rows);
  */
 fp4_status fp4_selftest_set_fp8_plan(int tile_rows, int splits);
 
+/*
+ * fp4_selftest_set_attention_splits -- into how many parts fp4_attention_decode
+ * shares a request's tokens (0: chosen by size), so that a test reaches every
+ * number at any size; fewer where a part would have under 128 tokens.  While set,
+ * fp4_attention_workspace returns what it needs.  Process-wide, as
+ * fp4_selftest_set_geometry.  Rejects negative numbers and more than 512
+ * (FP4_ERR_ARG).
+ */
+fp4_status fp4_selftest_set_attention_splits(int splits);
+
 #ifdef __cplusplus
 }
 #endif
