@@ -90,6 +90,23 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t s) {
   }
 }
 
+// Pair i of a lane's words (a constant once the loops around it are unrolled).
+template <int FMT, int N>
+__device__ __forceinline__ uint32_t widen_pair(const uint32_t (&w)[N], int i, uint32_t s, int half) {
+  if constexpr (KvTraits<FMT>::kBits == 8)
+    return i % 2 ? widen2<FMT, 1, 0>(w[i / 2], s) : widen2<FMT, 0, 0>(w[i / 2], s);
+  switch (i % 4 + 4 * half) {
+    case 0: return widen2<FMT, 0, 0>(w[i / 4], s);
+    case 1: return widen2<FMT, 1, 0>(w[i / 4], s);
+    case 2: return widen2<FMT, 2, 0>(w[i / 4], s);
+    case 3: return widen2<FMT, 3, 0>(w[i / 4], s);
+    case 4: return widen2<FMT, 0, 1>(w[i / 4], s);
+    case 5: return widen2<FMT, 1, 1>(w[i / 4], s);
+    case 6: return widen2<FMT, 2, 1>(w[i / 4], s);
+    default: return widen2<FMT, 3, 1>(w[i / 4], s);
+  }
+}
+
 // Scale B of a word of four scale codes as widen2 takes it: a float's bits, or
 // the fp16 pair that holds it in half B % 2.
 template <int FMT, int B>
@@ -146,14 +163,19 @@ struct VHalf {
   uint32_t s;                   // scale codes of the four tokens
 };
 
-// Page and first place of a half, and how many of its tokens there are.
+// Where a half's codes and scales begin, and how many of its tokens there are: the
+// same for the whole wave, so a load is that address plus the lane's own offset.
 struct HalfPos {
-  int64_t page;
-  int place, n;
+  int64_t code, scale;
+  int n;
 };
 
+// Read through the scalar cache (the kernel does not write the page table), whose
+// waits are apart from the vector loads'.
+typedef const __attribute__((address_space(4))) int32_t* ConstInts;
+
 template <int FMT, int D, int NP>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4lib::AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp4lib::AttnArgs a) {
   using F = KvTraits<FMT>;
   using S = Shape<FMT, D>;
   constexpr bool kF16 = F::kTwoLevel;
@@ -173,7 +195,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4
   id /= tiles;
   const int kv = id % a.cache.heads, request = id / a.cache.heads;
 
-  const int len = tokens_of(a, request), per = part_tokens(len, a.splits);
+  const int len = tokens_of(a, request), per = part_tokens(len, a);
   const int begin = split * per, end = min(len, begin + per);
   const int first = kv * group + tile * kHeads, heads = min(kHeads, group - tile * kHeads);
   if (begin >= end && split > 0) return;
@@ -181,16 +203,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4
   const bool mine = col < heads;
   const int64_t row = static_cast<int64_t>(request) * a.q.heads + first + (mine ? col : 0);
 
-  // q, elements g D/4 .. of the lane's head: the operand of each step.
+  // q, elements g D/4 .. of the lane's head: the operand of each step.  The sign of
+  // the scale goes into it, so that the largest score is that of the largest product.
   uintx4 q[S::kSteps];
-  float factor = a.scale * kLog2e;
+  float factor = fabsf(a.scale) * kLog2e;
+  const uint32_t flip = a.scale < 0.0f ? 0x80008000u : 0u, keep = a.scale == 0.0f ? 0u : ~0u;
   {
     const uint16_t* p = a.q.x + request * a.q.token + static_cast<int64_t>(first + (mine ? col : 0)) * a.q.head +
                         g * (D / 4);
 #pragma unroll
     for (int k = 0; k < S::kSteps; ++k) {
       const uint4 w = *reinterpret_cast<const uint4*>(p + 8 * k);
-      q[k] = uintx4{w.x, w.y, w.z, w.w};
+      q[k] = (uintx4{w.x, w.y, w.z, w.w} ^ flip) & keep;
     }
     if constexpr (kF16) {
       float s_enc, s_dec;
@@ -214,82 +238,98 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4
     }
   }
 
+  // masked scores are -infinity, which a factor of 0 would make a NaN (a scale of 0,
+  // or one that a tiny q brings to 0: no score differs from 0 then)
+  if (factor == 0.0f) factor = 0x1p-126f;
+
   floatx4 acc[S::kElems];
 #pragma unroll
   for (int i = 0; i < S::kElems; ++i) acc[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
   float top = -__builtin_inff(), total = 0.0f;
 
-  const int32_t* table = a.table + request * a.table_stride;
+  const ConstInts table = (ConstInts)(a.table + request * a.table_stride);
   const int mask = (1 << a.cache.page_shift) - 1;
-  auto half_at = [&](int t) {
-    HalfPos h{0, t & mask, end - t < 0 ? 0 : end - t > 16 ? 16 : end - t};
-    if (h.n > 0) {
-      const int page = table[t >> a.cache.page_shift];
-      if (page >= 0 && page < a.cache.pages) h.page = page;
-      else h.n = 0;                                           // no such page: its tokens are masked
-    }
+  // (behind the last token: the last one's page)
+  auto page_at = [&](int t) { return table[min(t, end - 1) >> a.cache.page_shift]; };
+  auto half_at = [&](int t, int page) {
+    HalfPos h;
+    const bool there = page >= 0 && page < a.cache.pages;     // else its tokens are masked
+    h.n = end - t > 16 ? 16 : end - t;
+    if (!there || h.n < 0) h.n = 0;
+    if (!there) page = 0;
+    h.code = page * a.cache.page + static_cast<int64_t>(t & mask) * a.cache.token;
+    h.scale = page * a.cache.s_page + (t & mask);
     return h;
   };
-  const uint8_t* kc = a.cache.codes[0] + kv * a.cache.head + g * S::kKBytes;
-  const uint8_t* vc = a.cache.codes[1] + kv * a.cache.head + c * S::kVBytes;
-  const uint8_t* ks = a.cache.scales[0] + kv * a.cache.s_head + (g * (D / 4) / F::kBlock) * a.cache.s_block;
-  const uint8_t* vs = a.cache.scales[1] + kv * a.cache.s_head + (c * S::kElems / F::kBlock) * a.cache.s_block;
+  // the lane's offsets (below 2^31: kv_api.cpp)
+  const uint32_t token = static_cast<uint32_t>(a.cache.token), block = static_cast<uint32_t>(a.cache.s_block);
+  const uint8_t* const codes[2] = {a.cache.codes[0] + kv * a.cache.head, a.cache.codes[1] + kv * a.cache.head};
+  const uint8_t* const scales[2] = {a.cache.scales[0] + kv * a.cache.s_head,
+                                    a.cache.scales[1] + kv * a.cache.s_head};
+  const uint32_t k_code = c * token + g * S::kKBytes, k_scale = c + g * (D / 4) / F::kBlock * block;
+  const uint32_t v_code = 4 * g * token + c * S::kVBytes, v_scale = 4 * g + c * S::kElems / F::kBlock * block;
   auto load_k = [&](KHalf<FMT, D>& k, const HalfPos& h) {
-    k.w.load(kc + h.page * a.cache.page + (h.place + c) * a.cache.token);
+    k.w.load(codes[0] + h.code + k_code);
 #pragma unroll
-    for (int b = 0; b < S::kKBlocks; ++b)
-      k.s[b] = ks[h.page * a.cache.s_page + h.place + c + b * a.cache.s_block];
+    for (int b = 0; b < S::kKBlocks; ++b) k.s[b] = (scales[0] + h.scale)[k_scale + b * block];
   };
   auto load_v = [&](VHalf<FMT, D>& v, const HalfPos& h) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v.w[j].load(vc + h.page * a.cache.page + (h.place + 4 * g + j) * a.cache.token);
-    v.s = *reinterpret_cast<const uint32_t*>(vs + h.page * a.cache.s_page + h.place + 4 * g);
-    // what is not there: zero codes and scales, whatever the memory holds
-    if (h.n < 16) {
-      const int n = h.n - 4 * g;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j >= n)
-#pragma unroll
-          for (auto& w : v.w[j].w) w = 0;
-      v.s &= n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
-    }
+    for (int j = 0; j < 4; ++j) v.w[j].load(codes[1] + h.code + (v_code + j * token));
+    v.s = *reinterpret_cast<const uint32_t*>(scales[1] + h.scale + v_scale);
   };
 
-  for (int t = begin + wave * kTile; t < end; t += kWaves * kTile) {
-    const HalfPos h[2] = {half_at(t), half_at(t + 16)};
-    KHalf<FMT, D> k[2];
-    VHalf<FMT, D> v[2];
-    load_k(k[0], h[0]);
-    load_k(k[1], h[1]);
-    load_v(v[0], h[0]);
-    load_v(v[1], h[1]);
-
-    float x[8];
-    float best = -__builtin_inff();
+  // A tile's loads are issued while the tile before it is worked on: K's when its
+  // scores are done, V's when its products are; its pages are looked up a tile
+  // earlier still.  The last tile's successor is loaded too (from a page that is
+  // there) and not used: a branch around the loads would make the compiler wait for
+  // all of them at once.
+  int t = begin + wave * kTile;
+  if (t < end) {
+  HalfPos h[2];
+  KHalf<FMT, D> k[2];
+  VHalf<FMT, D> v[2];
+  int pages[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    h[i] = half_at(t + 16 * i, page_at(t + 16 * i));
+    load_k(k[i], h[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    load_v(v[i], h[i]);
+    pages[i] = page_at(t + kWaves * kTile + 16 * i);
+  }
+  do {
+    t += kWaves * kTile;
+    const HalfPos next[2] = {half_at(t, pages[0]), half_at(t + 16, pages[1])};
+    floatx4 x[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      floatx4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+      x[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int n = 0; n < S::kSteps; ++n) {
         // elements 8 n .. of the lane's part lie in one block
         const uint32_t sc = scale_for<FMT, 0>(k[i].s[8 * n / F::kBlock < S::kKBlocks ? 8 * n / F::kBlock : 0]);
         uintx4 w;
-        if constexpr (F::kBits == 8)
-          w = uintx4{widen2<FMT, 0, 0>(k[i].w.w[2 * n], sc), widen2<FMT, 1, 0>(k[i].w.w[2 * n], sc),
-                     widen2<FMT, 0, 0>(k[i].w.w[2 * n + 1], sc), widen2<FMT, 1, 0>(k[i].w.w[2 * n + 1], sc)};
-        else
-          w = uintx4{widen2<FMT, 0, 0>(k[i].w.w[n], sc), widen2<FMT, 1, 0>(k[i].w.w[n], sc),
-                     widen2<FMT, 2, 0>(k[i].w.w[n], sc), widen2<FMT, 3, 0>(k[i].w.w[n], sc)};
-        s = mfma<kF16>(w, q[n], s);
-      }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        x[4 * i + j] = 4 * g + j < h[i].n ? s[j] * factor : -__builtin_inff();
-        best = fmaxf(best, x[4 * i + j]);
+        for (int e = 0; e < 4; ++e) w[e] = widen_pair<FMT>(k[i].w.w, 4 * n + e, sc, 0);
+        x[i] = mfma<kF16>(w, q[n], x[i]);
+      }
+      if (h[i].n < 16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (4 * g + j >= h[i].n) x[i][j] = -__builtin_inff();
       }
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      load_k(k[i], next[i]);
+      pages[i] = page_at(t + kWaves * kTile + 16 * i);
+    }
 
+    float best = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                       fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]))) * factor;
     if (__any(best > top + kSlack)) {
       best = fmaxf(best, __shfl_xor(best, 16, 64));
       best = fmaxf(best, __shfl_xor(best, 32, 64));
@@ -304,7 +344,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4
     uintx4 p, rest;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float u = __builtin_amdgcn_exp2f(x[2 * j] - from), w = __builtin_amdgcn_exp2f(x[2 * j + 1] - from);
+      const float u = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2)], factor, -from));
+      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2) + 1], factor, -from));
       total += u + w;
       const uint32_t hi = pack2<kF16>(u, w);
       const uint32_t lo = pack2<kF16>(u - unpack_lo<kF16>(hi), w - unpack_hi<kF16>(hi));
@@ -316,43 +357,53 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4
       }
     }
 
-    // V: pairs of elements of the eight tokens, then pairs of tokens
-    uint32_t w[8][S::kElems / 2];
+    // V: what is not there is zero codes and scales, whatever the memory holds;
+    // pairs of elements of the eight tokens, then pairs of tokens
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t sc[4] = {scale_for<FMT, 0>(v[i].s), scale_for<FMT, 1>(v[i].s), scale_for<FMT, 2>(v[i].s),
-                              scale_for<FMT, 3>(v[i].s)};
-      auto widen = [&](auto jc) {
-        constexpr int j = decltype(jc)::value;
+      if (h[i].n < 16) {
+        const int n = h[i].n - 4 * g;
 #pragma unroll
-        for (int e = 0; e < S::kElems / 2; ++e) {
-          const uint32_t word = v[i].w[j].w[F::kBits == 8 ? e / 2 : e / 4];
-          uint32_t o;
-          if constexpr (F::kBits == 8) {
-            o = e % 2 ? widen2<FMT, 1, j & 1>(word, sc[j]) : widen2<FMT, 0, j & 1>(word, sc[j]);
-          } else {
-            o = e % 4 == 0   ? widen2<FMT, 0, j & 1>(word, sc[j])
-                : e % 4 == 1 ? widen2<FMT, 1, j & 1>(word, sc[j])
-                : e % 4 == 2 ? widen2<FMT, 2, j & 1>(word, sc[j])
-                             : widen2<FMT, 3, j & 1>(word, sc[j]);
-          }
-          w[4 * i + j][e] = o;
-        }
-      };
-      widen(Const<0>());
-      widen(Const<1>());
-      widen(Const<2>());
-      widen(Const<3>());
+        for (int j = 0; j < 4; ++j)
+          if (j >= n)
+#pragma unroll
+            for (auto& w : v[i].w[j].w) w = 0;
+        v[i].s &= n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
+      }
+    }
+    uint32_t sc[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      sc[4 * i] = scale_for<FMT, 0>(v[i].s);
+      sc[4 * i + 1] = scale_for<FMT, 1>(v[i].s);
+      sc[4 * i + 2] = scale_for<FMT, 2>(v[i].s);
+      sc[4 * i + 3] = scale_for<FMT, 3>(v[i].s);
+    }
+    constexpr int kPart = S::kElems < 8 ? S::kElems : 8;      // elements at once
+#pragma unroll
+    for (int e0 = 0; e0 < S::kElems; e0 += kPart) {
+      uint32_t w[8][kPart / 2];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < kPart / 2; ++e)
+          w[j][e] = widen_pair<FMT>(v[j / 4].w[j % 4].w, e0 / 2 + e, sc[j], j & 1);
+#pragma unroll
+      for (int e = 0; e < kPart; ++e) {
+        const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
+        uintx4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2], sel);
+        acc[e0 + e] = mfma<kF16>(o, p, acc[e0 + e]);
+        if constexpr (NP == 2) acc[e0 + e] = mfma<kF16>(o, rest, acc[e0 + e]);
+      }
     }
 #pragma unroll
-    for (int e = 0; e < S::kElems; ++e) {
-      const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
-      uintx4 o;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2], sel);
-      acc[e] = mfma<kF16>(o, p, acc[e]);
-      if constexpr (NP == 2) acc[e] = mfma<kF16>(o, rest, acc[e]);
+    for (int i = 0; i < 2; ++i) {
+      h[i] = next[i];
+      load_v(v[i], h[i]);
     }
+  } while (t < end);
   }
 
   // the four waves' sums, lane by lane, in the first
@@ -421,15 +472,15 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : 4) void k_attention(fp4
     }
     if (a.lse && g == 0) a.lse[row] = (all + __builtin_log2f(total) - kShift) / kLog2e;
   } else {
-    // sums with V's tensor scale; the maximum and the sum behind them
-    float* o = a.part + (row * a.splits + split) * (D + 2);
+    // sums with V's tensor scale; the maximum and the sum of p apart
+    float* o = a.part + (row * a.splits + split) * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < S::kElems; e += 2)
-        *reinterpret_cast<float2*>(o + (4 * g + i) * S::kElems + e) =
-            make_float2(acc[e][i] * s_dec, acc[e + 1][i] * s_dec);
-    if (g == 0) *reinterpret_cast<float2*>(o + D) = make_float2(all - kShift, total);
+      for (int e = 0; e < S::kElems; e += 4)
+        *reinterpret_cast<float4*>(o + (4 * g + i) * S::kElems + e) =
+            make_float4(acc[e][i] * s_dec, acc[e + 1][i] * s_dec, acc[e + 2][i] * s_dec, acc[e + 3][i] * s_dec);
+    if (g == 0) part_sums(a)[row * a.splits + split] = make_float2(all - kShift, total);
   }
 }
 

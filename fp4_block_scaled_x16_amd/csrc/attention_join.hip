@@ -11,78 +11,159 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 
-// The parts of a request, in order: a workgroup per query head, D / 2 threads
-// (two elements each) times 8 shares of the parts.
+// out and lse of a row from its parts' sums o (the thread's four elements), the
+// largest of their maxima and their sum.
 template <int D>
-__global__ __launch_bounds__(4 * D) void k_attention_join(fp4lib::AttnArgs a) {
-  constexpr int kShares = 8, kPair = D / 2;
-  __shared__ float2 sums[kShares - 1][kPair];
-  __shared__ float totals[kShares - 1];
-  const int64_t row = blockIdx.x;
-  const int request = static_cast<int>(row / a.q.heads);
-  const int len = tokens_of(a, request), per = part_tokens(len, a.splits);
-  const int parts = (len + per - 1) / per;
-  if (parts <= 1) return;
-  const int share = threadIdx.x / kPair, d = threadIdx.x % kPair * 2;
-  const float* p = a.part + row * a.splits * (D + 2);
-  float top = -__builtin_inff();
-  for (int s = 0; s < parts; ++s) top = fmaxf(top, p[s * (D + 2) + D]);
-  const float ref = top == -__builtin_inff() ? 0.0f : top;
-  float total = 0.0f;
-  float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-  for (int s = share; s < parts; s += kShares) {
-    const float* e = p + s * (D + 2);
-    const float2 ml = *reinterpret_cast<const float2*>(e + D), v = *reinterpret_cast<const float2*>(e + d);
-    const float by = __builtin_amdgcn_exp2f(ml.x - ref);
-    total += by * ml.y;
-    o.x += by * v.x;
-    o.y += by * v.y;
-  }
-  if (share) {
-    sums[share - 1][d / 2] = o;
-    if (d == 0) totals[share - 1] = total;
-  }
-  __syncthreads();
-  if (share) return;
-  for (int s = 0; s < kShares - 1; ++s) {
-    o.x += sums[s][d / 2].x;
-    o.y += sums[s][d / 2].y;
-    total += totals[s];
-  }
+__device__ __forceinline__ void finish(const fp4lib::AttnArgs& a, int64_t row, int d, float4 o, float top, float total) {
   const float by = total > 0.0f || total != total ? 1.0f / total : 0.0f;
   if (a.out_f32)
-    *reinterpret_cast<float2*>(static_cast<float*>(a.out) + row * D + d) = make_float2(o.x * by, o.y * by);
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * D + 4 * d) =
+        make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
   else
-    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + row * D + d) =
-        fp8dev::pack_bf16(o.x * by, o.y * by);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * D + 4 * d) =
+        make_uint2(fp8dev::pack_bf16(o.x * by, o.y * by), fp8dev::pack_bf16(o.z * by, o.w * by));
   if (a.lse && d == 0) a.lse[row] = (top + __builtin_log2f(total)) / kLog2e;
 }
 
+// Few parts: D / 4 lanes per query head, four elements each.
+constexpr int kFewParts = 16;
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join_few(fp4lib::AttnArgs a) {
+  constexpr int kQuads = D / 4;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / kQuads) + threadIdx.x / kQuads;
+  if (row >= static_cast<int64_t>(a.requests) * a.q.heads) return;
+  const int d = threadIdx.x % kQuads;
+  const int len = tokens_of(a, static_cast<uint32_t>(row) / static_cast<uint32_t>(a.q.heads));
+  const int per = part_tokens(len, a), parts = (len + per - 1) / per;
+  if (parts <= 1) return;
+  const float4* p = reinterpret_cast<const float4*>(a.part + row * a.splits * D) + d;
+  const float2* ml = part_sums(a) + row * a.splits;
+  float top = -__builtin_inff(), total = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, ml[s].x);
+  const float ref = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float4 v = p[s * kQuads];
+    const float by = __builtin_amdgcn_exp2f(ml[s].x - ref);
+    total += by * ml[s].y;
+    o.x += by * v.x;
+    o.y += by * v.y;
+    o.z += by * v.z;
+    o.w += by * v.w;
+  }
+  finish<D>(a, row, d, o, top, total);
+}
+
+// The parts of a request, in order: a workgroup per query head, whose threads take
+// four elements each of every kShares-th part.
+template <int D>
+__global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
+  constexpr int kQuads = D / 4, kShares = 256 / kQuads;
+  __shared__ float4 sums[kShares][kQuads];
+  __shared__ float weights[kMaxParts];
+  __shared__ float2 most[4];
+  const int64_t row = blockIdx.x;
+  const int request = static_cast<int>(row / a.q.heads);
+  const int len = tokens_of(a, request), per = part_tokens(len, a);
+  const int parts = (len + per - 1) / per;
+  if (parts <= 1) return;
+  const float* p = a.part + row * a.splits * D;
+  const float2* ml = part_sums(a) + row * a.splits;
+  // what each part's sums count for: 2^(its maximum - the largest)
+  float2 mine[kMaxParts / 256];
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 256; ++i) {
+    const int s = threadIdx.x + 256 * i;
+    mine[i] = s < parts ? ml[s] : make_float2(-__builtin_inff(), 0.0f);
+    top = fmaxf(top, mine[i].x);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6].x = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, most[i].x);
+  const float ref = top == -__builtin_inff() ? 0.0f : top;
+  float total = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kMaxParts / 256; ++i) {
+    const int s = threadIdx.x + 256 * i;
+    const float by = __builtin_amdgcn_exp2f(mine[i].x - ref);
+    if (s < parts) {
+      weights[s] = by;
+      total += by * mine[i].y;
+    }
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) total += __shfl_xor(total, o, 64);
+  if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6].y = total;
+  __syncthreads();
+  total = ((most[0].y + most[1].y) + most[2].y) + most[3].y;
+
+  const int share = threadIdx.x / kQuads, d = threadIdx.x % kQuads;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = share; s < parts; s += kShares) {
+    const float4 v = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(s) * D + 4 * d);
+    const float by = weights[s];
+    o.x += by * v.x;
+    o.y += by * v.y;
+    o.z += by * v.z;
+    o.w += by * v.w;
+  }
+  sums[share][d] = o;
+  __syncthreads();
+  if (threadIdx.x >= kQuads) return;
+#pragma unroll
+  for (int s = 1; s < kShares; ++s) {
+    o.x += sums[s][d].x;
+    o.y += sums[s][d].y;
+    o.z += sums[s][d].z;
+    o.w += sums[s][d].w;
+  }
+  finish<D>(a, row, d, o, top, total);
+}
 
 std::atomic<int> g_splits{0};
 
-// Parts per request: enough workgroups for kPerCu on every CU where every
-// request has as many tokens as the page table has room for, and none of fewer
-// than kMinPart tokens.  A shorter request is shared among as many workgroups, as
-// far as that leaves each kMinPart tokens: the kernel goes by its length.
-constexpr int kPerCu = 8;
-
-int splits_of(const fp4lib::AttnArgs& a) {
-  const int64_t room = static_cast<int64_t>(a.table_width) << a.cache.page_shift;
-  const int64_t most = (room + kMinPart - 1) / kMinPart;
-  const int group = a.q.heads / a.cache.heads, tiles = (group + (group <= 8 ? 7 : 15)) / (group <= 8 ? 8 : 16);
-  const int64_t each = static_cast<int64_t>(a.requests) * a.cache.heads * tiles;
-  int64_t want = (static_cast<int64_t>(fp4lib::device_cu_count()) * kPerCu + each - 1) / each;
-  if (const int forced = g_splits.load()) want = forced;
-  want = want > most ? most : want;
-  return static_cast<int>(want < 1 ? 1 : want > 512 ? 512 : want);
+int tiles_of(const fp4lib::AttnArgs& a) {
+  const int group = a.q.heads / a.cache.heads, heads = group <= 8 ? 8 : 16;
+  return (group + heads - 1) / heads;
 }
 
-int64_t part_bytes(const fp4lib::AttnArgs& a, int splits) {
-  return splits <= 1 ? 0
-                     : static_cast<int64_t>(a.requests) * a.q.heads * splits * (a.cache.head_dim + 2) *
-                           static_cast<int64_t>(sizeof(float));
+// Parts per request and the least tokens of one, from what the page table has room
+// for (the lengths are on the device; a shorter request is shared among as many).
+// Two workgroups on every CU, if that leaves a part 1024 tokens (each starts with
+// three loads that wait for one another, and ends with a join), else one: 4 requests
+// of 120000 NVFP4 tokens in 8 / 16 / 24 / 64 parts 126 / 109 / 112 / 116 us, 1 of 30000 FP8
+// tokens in 32 / 64 / 128 parts 17.4 / 19.2 / 22.  Where requests alone fill the chip,
+// two parts of over 2048 tokens even out their lengths: 64 of up to 8192 in 1 / 2 / 8
+// parts 124 / 120 / 122 us, 256 of up to 1024 in 1 / 2 parts 15.4 / 21.6.
+void plan(fp4lib::AttnArgs& a) {
+  const int64_t room = static_cast<int64_t>(a.table_width) << a.cache.page_shift, cu = fp4lib::device_cu_count();
+  const int64_t each = static_cast<int64_t>(a.requests) * a.cache.heads * tiles_of(a);
+  const int64_t slots = 2 * cu;
+  const int64_t most = (room + kStep - 1) / kStep, full = slots / each > 1 ? slots / each : 1;
+  int64_t want = full;
+  if (room < 1024 * full) want = (cu + each - 1) / each;
+  const int64_t even = (room + 2047) / 2048;
+  if (want < even) want = even < 2 * full ? even : 2 * full;
+  a.min_part = 2 * each >= slots ? 4 * kStep : kStep;
+  if (const int forced = g_splits.load()) {
+    want = forced;
+    a.min_part = kStep;
+  }
+  want = want > most ? most : want;
+  a.splits = static_cast<int>(want < 1 ? 1 : want > kMaxParts ? kMaxParts : want);
+}
+
+int64_t part_bytes(const fp4lib::AttnArgs& a) {
+  return a.splits <= 1 ? 0
+                       : static_cast<int64_t>(a.requests) * a.q.heads * a.splits * (a.cache.head_dim + 2) *
+                             static_cast<int64_t>(sizeof(float));
 }
 
 }  // namespace
@@ -91,14 +172,17 @@ namespace fp4lib {
 
 void set_attention_splits(int splits) { g_splits.store(splits); }
 
-int64_t attention_workspace(const AttnArgs& a) { return part_bytes(a, splits_of(a)); }
+int64_t attention_workspace(const AttnArgs& args) {
+  AttnArgs a = args;
+  plan(a);
+  return part_bytes(a);
+}
 
 hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
   AttnArgs a = args;
-  a.splits = splits_of(a);
-  if (!a.part || a.part_bytes < part_bytes(a, a.splits)) a.splits = 1;
-  const int group = a.q.heads / a.cache.heads, tiles = (group + (group <= 8 ? 7 : 15)) / (group <= 8 ? 8 : 16);
-  const int64_t grid = static_cast<int64_t>(a.requests) * a.cache.heads * tiles * a.splits;
+  plan(a);
+  if (!a.part || a.part_bytes < part_bytes(a)) a.splits = 1;
+  const int64_t grid = static_cast<int64_t>(a.requests) * a.cache.heads * tiles_of(a) * a.splits;
   if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
   const hipError_t e = with_format(a.cache.fmt, [&](auto f) {
     return launch_attention_fmt<decltype(f)::value>(a, static_cast<uint32_t>(grid), s);
@@ -106,7 +190,12 @@ hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
   if (e != hipSuccess || a.splits == 1) return e;
   return with_dim(a.cache.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    hipLaunchKernelGGL(k_attention_join<D>, dim3(a.requests * a.q.heads), dim3(4 * D), 0, s, a);
+    const int64_t rows = static_cast<int64_t>(a.requests) * a.q.heads;
+    if (a.splits <= kFewParts)
+      hipLaunchKernelGGL(k_attention_join_few<D>, dim3(static_cast<uint32_t>((rows * (D / 4) + 255) / 256)),
+                         dim3(256), 0, s, a);
+    else
+      hipLaunchKernelGGL(k_attention_join<D>, dim3(static_cast<uint32_t>(rows)), dim3(256), 0, s, a);
     return hipGetLastError();
   });
 }

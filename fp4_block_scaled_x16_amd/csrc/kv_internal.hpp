@@ -88,7 +88,7 @@ struct AttnArgs {
   float* lse;                  // null, or [requests, heads]
   float* part;                 // workspace: null with splits == 1
   int64_t part_bytes;
-  int splits;                  // set by the launcher
+  int splits, min_part;        // set by the launcher
 };
 
 hipError_t launch_qk_rows(const QkRowsArgs& a, hipStream_t s);
