@@ -131,7 +131,7 @@ def load_library(path=None):
     lib.fp4_gemm_workspace.argtypes = [ctypes.POINTER(Operand), ctypes.POINTER(Operand), i64, i64,
                                        i64, i32]
     lib.fp4_gemm_workspace.restype = i64
-    heads, norm, cache = (ctypes.POINTER(t) for t in (Heads, QKNormDesc, KVCacheDesc))
+    heads = norm = cache = vp       # structs by address: a byref, or what addressof gives
     lib.fp4_qk_norm_rope.argtypes = [norm, heads, heads, vp, i64, i64, heads, heads, vp]
     lib.fp4_qk_norm_rope_backward.argtypes = [norm, heads, heads, vp, i64, i64, heads, heads, heads,
                                               heads, vp, vp, i32, vp, i64, vp]
@@ -716,23 +716,39 @@ def _gemm_workspace(device, M, N, K, out_type, fmt_a, fmt_b, ld_a, ld_b):
 
 # ------------------------------------------------- attention on a cache --
 HEAD_DIMS = (64, 128, 256)
+_plan_changes = 0          # by selftest_set_attention_splits
 CACHE_FORMATS = (FP8_E4M3, MXFP8, MXFP4, NVFP4, UE5M3)
 PAIRINGS = {"half": 0, "interleaved": 1}
 
 
-def _heads(x, name, tokens=None, heads=None, head_dim=None):
-    """A bf16 [tokens, heads, head_dim] tensor, of any strides but the last, as
-    the library takes it."""
-    if x.dtype is not torch.bfloat16 or x.dim() != 3:
+_BF16 = torch.bfloat16
+
+
+def _heads(x, name):
+    """(tokens, heads, head_dim, a Heads' fields) of a bf16 [tokens, heads, head_dim]
+    tensor of any strides but the last."""
+    if x.dtype is not _BF16 or x.dim() != 3:
         raise ValueError("%s must be a 3-D bfloat16 tensor [tokens, heads, head_dim]" % name)
     t, h, d = x.shape
-    if (tokens is not None and t != tokens or heads is not None and h != heads
-            or head_dim is not None and d != head_dim):
-        raise ValueError("%s must be [%s, %s, %s], not %s" % (name, tokens, heads, head_dim, tuple(x.shape)))
     st, sh, sd = x.stride()
     if sd != 1:
         raise ValueError("%s: the elements of a head must be contiguous" % name)
-    return Heads(x.data_ptr(), st if t > 1 else 0, sh if h > 1 else 0, h)
+    return t, h, d, (x.data_ptr(), st if t > 1 else 0, sh if h > 1 else 0, h)
+
+
+def _heads_like(x, name, like, device):
+    """A Heads' fields of a tensor that must have the shape of `like`, on its device."""
+    t, h, d, fields = _heads(x, name)
+    if (t, h, d) != like:
+        raise ValueError("%s must be %s, not %s" % (name, list(like), [t, h, d]))
+    if x.device != device:
+        raise ValueError("%s is on %s, not on %s" % (name, x.device, device))
+    return fields
+
+
+# several Heads in one buffer, which is cheaper than an object each: the fields of
+# each, 32 bytes
+_HEADS = [None] + [ctypes.c_int64 * (4 * n) for n in range(1, 7)]
 
 
 def _index(x, name, n, device, dtype=torch.int64):
@@ -778,36 +794,26 @@ class QKNorm:
         self._desc = QKNormDesc(_addr(q_weight), _addr(k_weight),
                                 int(q_weight is not None and q_weight.dtype == torch.float32), self.eps,
                                 _addr(table), rows, dim, PAIRINGS[style])
-        self._ref = ctypes.byref(self._desc)
+        self._at = ctypes.addressof(self._desc)
 
-    def _check(self, x, positions, tokens):
-        """The address of the positions that rows x [tokens, heads, head_dim] have."""
-        if x.device != self.device or (self.head_dim is not None and x.shape[2] != self.head_dim):
+    def _positions(self, positions, tokens, head_dim, device):
+        """The address of the positions of rows [tokens, heads, head_dim]."""
+        if device != self.device or (self.head_dim is not None and head_dim != self.head_dim):
             raise ValueError("the norm is for heads of %s on %s" % (self.head_dim, self.device))
         if self.table is None:
             return None
         if positions is None:
             raise ValueError("a rotation needs positions")
-        return _index(positions, "positions", tokens, x.device)
+        return _index(positions, "positions", tokens, device)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, not on %s" % (name, t.device, device))
-
-
-def _out_heads(out, like, name):
-    """(tensor, Heads) of an output for `like`: `out`, or a new dense one."""
-    if out is None:
-        out = torch.empty(like.shape, dtype=torch.bfloat16, device=like.device)
-    elif out.device != like.device:
-        raise ValueError("%s is on %s, not on %s" % (name, out.device, like.device))
-    return out, _heads(out, name, *like.shape)
-
-
-def _ref(h):
-    return None if h is None else ctypes.byref(h)
+def _out_heads(out, like, x, name):
+    """(tensor, a Heads' fields) of an output of x's kind: `out`, or a new dense one."""
+    if out is not None:
+        return out, _heads_like(out, name, like, x.device)
+    t, h, d = like
+    out = x.new_empty(like)
+    return out, (out.data_ptr(), h * d, d, h)
 
 
 def qk_norm_rope(norm: QKNorm, q, k, positions=None, out=(None, None)):
@@ -816,22 +822,28 @@ def qk_norm_rope(norm: QKNorm, q, k, positions=None, out=(None, None)):
     int64 [tokens], rows of the norm's table (one outside it gives NaN).
     out: tensors to write, of any strides but the last, for q and k (the inputs
     themselves, too)."""
-    first = q if q is not None else k
-    if first is None:
+    tokens = d = dev = None
+    results, fields, at = [None, None], [], [None] * 4
+    for i, x in enumerate((q, k)):
+        if x is None:
+            continue
+        t, h, w, row = _heads(x, "qk"[i])
+        if tokens is None:
+            tokens, d, dev = t, w, x.device
+        elif (t, w) != (tokens, d) or x.device != dev:
+            raise ValueError("k must be [%d, heads, %d] on %s" % (tokens, d, dev))
+        results[i], row_out = _out_heads(out[i], (t, h, w), x, "out[%d]" % i)
+        at[i], at[2 + i] = 8 * len(fields), 8 * len(fields) + 32
+        fields += row + row_out
+    if not fields:
         raise ValueError("q and k are None")
-    tokens, _, d = first.shape if first.dim() == 3 else (None, None, None)
-    hq = None if q is None else _heads(q, "q", tokens, None, d)
-    hk = None if k is None else _heads(k, "k", tokens, None, d)
-    _same_device(first.device, k=k)
-    pos = norm._check(first, positions, tokens)
-    yq = yk = oq = ok = None
-    if q is not None:
-        yq, oq = _out_heads(out[0], q, "out[0]")
-    if k is not None:
-        yk, ok = _out_heads(out[1], k, "out[1]")
-    _launch("fp4_qk_norm_rope", load_library().fp4_qk_norm_rope, first.device, norm._ref, _ref(hq), _ref(hk),
-            pos, tokens, d, _ref(oq), _ref(ok))
-    return yq, yk
+    pos = norm._positions(positions, tokens, d, dev)
+    buf = _HEADS[len(fields) // 4](*fields)
+    b = ctypes.addressof(buf)
+    _launch("fp4_qk_norm_rope", load_library().fp4_qk_norm_rope, dev, norm._at,
+            None if q is None else b + at[0], None if k is None else b + at[1], pos, tokens, d,
+            None if q is None else b + at[2], None if k is None else b + at[3])
+    return results[0], results[1]
 
 
 def qk_norm_rope_backward(norm: QKNorm, q, k, positions, dq, dk, out=(None, None), weight_grads=True):
@@ -840,34 +852,41 @@ def qk_norm_rope_backward(norm: QKNorm, q, k, positions, dq, dk, out=(None, None
     gradients are float32 [head_dim], summed in a fixed order (None without a norm).
     weight_grads: False for none, or a dense float32 [2, head_dim] tensor to which q's
     and k's are added (its rows are what is returned)."""
-    first = q if q is not None else k
-    if first is None:
+    tokens = d = dev = None
+    results, fields, at = [None, None], [], [None, None]
+    for i, (x, dy) in enumerate(((q, dq), (k, dk))):
+        if x is None:
+            continue
+        t, h, w, row = _heads(x, "qk"[i])
+        if tokens is None:
+            tokens, d, dev = t, w, x.device
+        elif (t, w) != (tokens, d) or x.device != dev:
+            raise ValueError("k must be [%d, heads, %d] on %s" % (tokens, d, dev))
+        like = (t, h, w)
+        row_dy = _heads_like(dy, "dq" if i == 0 else "dk", like, dev)
+        results[i], row_out = _out_heads(out[i], like, x, "out[%d]" % i)
+        at[i] = 8 * len(fields)
+        fields += row + row_dy + row_out
+    if not fields:
         raise ValueError("q and k are None")
-    tokens, _, d = first.shape if first.dim() == 3 else (None, None, None)
-    hq = hk = hdq = hdk = gq = gk = oq = ok = None
-    if q is not None:
-        hq, hdq = _heads(q, "q", tokens, None, d), _heads(dq, "dq", *q.shape)
-        gq, oq = _out_heads(out[0], q, "out[0]")
-    if k is not None:
-        hk, hdk = _heads(k, "k", tokens, None, d), _heads(dk, "dk", *k.shape)
-        gk, ok = _out_heads(out[1], k, "out[1]")
-    dev = first.device
-    _same_device(dev, k=k, dq=dq if q is not None else None, dk=dk if k is not None else None)
-    pos = norm._check(first, positions, tokens)
+    pos = norm._positions(positions, tokens, d, dev)
     wq = wk = ws = None
     n = 0
     add = isinstance(weight_grads, torch.Tensor)
     if (add or weight_grads) and norm.q_weight is not None:
         w = weight_grads if add else torch.empty((2, d), dtype=torch.float32, device=dev)
-        if w.dtype != torch.float32 or w.shape != (2, d) or not w.is_contiguous() or w.device != dev:
+        if add and (w.dtype != torch.float32 or w.shape != (2, d) or not w.is_contiguous() or w.device != dev):
             raise ValueError("weight_grads must be a dense float32 [2, %d] tensor on %s" % (d, dev))
-        wq, wk = w[0] if q is not None else None, w[1] if k is not None else None
+        wq, wk = w.unbind(0)
+        wq, wk = wq if q is not None else None, wk if k is not None else None
         n = _norm_workspace(dev, d)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
-    _launch("fp4_qk_norm_rope_backward", load_library().fp4_qk_norm_rope_backward, dev, norm._ref, _ref(hq),
-            _ref(hk), pos, tokens, d, _ref(hdq), _ref(hdk), _ref(oq), _ref(ok), _addr(wq), _addr(wk),
-            int(add), _addr(ws), n)
-    return gq, gk, wq, wk
+    buf = _HEADS[len(fields) // 4](*fields)
+    b = ctypes.addressof(buf)
+    (q0, q1, q2), (k0, k1, k2) = ((None,) * 3 if o is None else (b + o, b + o + 32, b + o + 64) for o in at)
+    _launch("fp4_qk_norm_rope_backward", load_library().fp4_qk_norm_rope_backward, dev, norm._at, q0, k0,
+            pos, tokens, d, q1, k1, q2, k2, _addr(wq), _addr(wk), int(add), _addr(ws), n)
+    return results[0], results[1], wq, wk
 
 
 @functools.lru_cache(maxsize=64)
@@ -924,7 +943,20 @@ class KVCache:
         self._desc = KVCacheDesc(f, heads, d, page, pages, k_codes.data_ptr(), k_scales.data_ptr(),
                                  v_codes.data_ptr(), v_scales.data_ptr(), *strides(k_codes, width),
                                  *strides(k_scales, page), _addr(amax), self.target)
-        self._ref = ctypes.byref(self._desc)
+        self._at = ctypes.addressof(self._desc)
+        self._sizes = {}
+
+    def _workspace(self, heads, requests, width):
+        """Bytes of workspace that attention of these sizes can use."""
+        key = heads, requests, width, _plan_changes
+        size = self._sizes.get(key)
+        if size is None:
+            if len(self._sizes) > 4096:
+                self._sizes.clear()
+            with torch.cuda.device(self.device):
+                size = load_library().fp4_attention_workspace(self._at, heads, requests, width)
+            self._sizes[key] = size
+        return size
 
     @classmethod
     def empty(cls, pages, page_size, heads, head_dim, fmt="mxfp8", device="cuda", amax=None, target=448.0):
@@ -953,25 +985,29 @@ def kv_cache_write(cache: KVCache, k, v, slots, q=None, norm: QKNorm = None, pos
     q, q does too and comes back (bf16; into q_out, if given).  positions as in
     `qk_norm_rope`.  Returns q's result, or None.
     """
-    hk = _heads(k, "k", None, cache.heads, cache.head_dim)
-    tokens = k.shape[0]
-    hv = _heads(v, "v", tokens, cache.heads, cache.head_dim)
+    tokens, h, d, fields = _heads(k, "k")
     dev = cache.device
-    _same_device(dev, k=k, v=v, q=q)
+    if (h, d) != (cache.heads, cache.head_dim) or k.device != dev:
+        raise ValueError("k must be [tokens, %d, %d] on %s" % (cache.heads, cache.head_dim, dev))
+    fields += _heads_like(v, "v", (tokens, h, d), dev)
     at = _index(slots, "slots", tokens, dev)
-    if norm is None:
-        if q is not None:
-            raise ValueError("q needs a norm")
-        _launch("fp4_kv_cache_write", load_library().fp4_kv_cache_write, dev, cache._ref, ctypes.byref(hk),
-                ctypes.byref(hv), at, tokens, None, None, None, None)
-        return None
-    pos = norm._check(k, positions, tokens)
-    hq = oq = None
+    pos = where = q_at = out_at = None
+    if norm is not None:
+        where, pos = norm._at, norm._positions(positions, tokens, d, dev)
     if q is not None:
-        hq = _heads(q, "q", tokens, None, cache.head_dim)
-        q_out, oq = _out_heads(q_out, q, "q_out")
-    _launch("fp4_kv_cache_write", load_library().fp4_kv_cache_write, dev, cache._ref, ctypes.byref(hk),
-            ctypes.byref(hv), at, tokens, norm._ref, pos, _ref(hq), _ref(oq))
+        if norm is None:
+            raise ValueError("q needs a norm")
+        t, hq, dq, row = _heads(q, "q")
+        if (t, dq) != (tokens, d) or q.device != dev:
+            raise ValueError("q must be [%d, heads, %d] on %s" % (tokens, d, dev))
+        q_out, row_out = _out_heads(q_out, (t, hq, d), q, "q_out")
+        fields += row + row_out
+    buf = _HEADS[len(fields) // 4](*fields)
+    b = ctypes.addressof(buf)
+    if q is not None:
+        q_at, out_at = b + 64, b + 96
+    _launch("fp4_kv_cache_write", load_library().fp4_kv_cache_write, dev, cache._at, b, b + 32, at, tokens,
+            where, pos, q_at, out_at)
     return q_out if q is not None else None
 
 
@@ -984,9 +1020,10 @@ def kv_cache_read(cache: KVCache, slots, out_dtype=torch.bfloat16):
         raise ValueError("slots must be an int64 [n] tensor")
     n = slots.shape[0]
     at = _index(slots, "slots", n, cache.device)
-    k, v = (torch.empty((n, cache.heads, cache.head_dim), dtype=out_dtype, device=cache.device)
-            for _ in range(2))
-    _launch("fp4_kv_cache_read", load_library().fp4_kv_cache_read, cache.device, cache._ref, at, n,
+    shape = (n, cache.heads, cache.head_dim)
+    k = torch.empty(shape, dtype=out_dtype, device=cache.device)
+    v = k.new_empty(shape)
+    _launch("fp4_kv_cache_read", load_library().fp4_kv_cache_read, cache.device, cache._at, at, n,
             k.data_ptr(), v.data_ptr(), int(out_dtype == torch.float32))
     return k, v
 
@@ -1003,39 +1040,32 @@ def attention_decode(q, cache: KVCache, page_table, lens, scale=None, out=None, 
     [requests, heads] log of each softmax's denominator (-inf without tokens).  Tokens
     on a page that the cache does not have are left out.
     """
-    hq = _heads(q, "q", None, None, cache.head_dim)
-    n, heads, d = q.shape
+    n, heads, d, fields = _heads(q, "q")
     dev = cache.device
-    _same_device(dev, q=q, page_table=page_table)
-    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n
-            or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
-        raise ValueError("page_table must be an int32 [%d, width] tensor, contiguous along its rows" % n)
+    if d != cache.head_dim or q.device != dev:
+        raise ValueError("q must be [requests, heads, %d] on %s" % (cache.head_dim, dev))
+    if (page_table.dtype is not torch.int32 or page_table.dim() != 2 or page_table.device != dev
+            or page_table.shape[0] != n or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
+        raise ValueError("page_table must be an int32 [%d, width] tensor on %s, contiguous along its rows"
+                         % (n, dev))
     at = _index(lens, "lens", n, dev, torch.int32)
     if out is None:
-        out = torch.empty((n, heads, d), dtype=out_dtype, device=dev)
+        out = (q.new_empty((n, heads, d)) if out_dtype is _BF16
+               else torch.empty((n, heads, d), dtype=out_dtype, device=dev))
     elif out.shape != q.shape or not out.is_contiguous() or out.device != dev:
         raise ValueError("out must be a contiguous tensor of q's shape on its device")
     if out.dtype not in OUT_TYPES:
         raise ValueError("the output is float32 or bfloat16")
     lse = torch.empty((n, heads), dtype=torch.float32, device=dev) if return_lse else None
     width = page_table.shape[1]
-    size = _attention_workspace(dev, cache.fmt, cache.heads, d, cache.page_size, heads, n, width)
+    size = cache._workspace(heads, n, width)
     ws = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    _launch("fp4_attention_decode", load_library().fp4_attention_decode, dev, cache._ref, ctypes.byref(hq),
+    buf = _HEADS[1](*fields)
+    _launch("fp4_attention_decode", load_library().fp4_attention_decode, dev, cache._at, ctypes.addressof(buf),
             page_table.data_ptr(), page_table.stride(0) if n > 1 else 0, width, at, n,
             d ** -0.5 if scale is None else float(scale), out.data_ptr(), OUT_TYPES[out.dtype], _addr(lse),
             _addr(ws), size)
     return (out, lse) if return_lse else out
-
-
-@functools.lru_cache(maxsize=4096)
-def _attention_workspace(device, fmt, heads, head_dim, page_size, q_heads, requests, width):
-    """Bytes of workspace that a call of these sizes can use."""
-    some = 4096                        # any aligned address: none is read
-    c = KVCacheDesc(fmt, heads, head_dim, page_size, 1, some, some, some, some, 4096, 4096, 4096, 1024, 1024,
-                    1024, some, 448.0)
-    with torch.cuda.device(device):
-        return load_library().fp4_attention_workspace(ctypes.byref(c), q_heads, requests, width)
 
 
 # ------------------------------------------------------------- self-test --
@@ -1083,6 +1113,7 @@ def selftest_set_fp8_plan(tile_rows=0, splits=1):
 
 def selftest_set_attention_splits(splits=0):
     """Parts that attention shares a request's tokens among (0: chosen by size)."""
+    global _plan_changes
     _check(load_library().fp4_selftest_set_attention_splits(int(splits)),
            "fp4_selftest_set_attention_splits")
-    _attention_workspace.cache_clear()
+    _plan_changes += 1

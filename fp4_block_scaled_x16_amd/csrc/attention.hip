@@ -12,8 +12,8 @@
 // Codes go from global memory into registers and, widened, straight into MFMA
 // operands: no byte of the cache is used twice, so nothing is staged in LDS.
 //   scores^T [token, head] = K q^T.  Lane (c, g) (c = lane % 16, g = lane / 16)
-//     has token c of each half tile, elements g D/4 .. of its row; q's operand
-//     is laid out to match.  It gets back tokens 4 g .. 4 g + 3 of head c.
+//     has a token of each half tile, elements g D/4 .. of its row; q's operand
+//     is laid out to match.  It gets back tokens g, 4 + g, 8 + g and 12 + g of head c.
 //   out^T [element, head] += V^T p^T.  The four scores of each half are the
 //     lane's own part of p's operand: p never leaves its lane.  V^T's operand
 //     holds elements of 8 tokens (4 g .. of each half), so a lane loads elements
@@ -117,22 +117,28 @@ __device__ __forceinline__ uint32_t scale_for(uint32_t word) {
     return ((word >> (8 * B)) & 0xFFu) << 23;
 }
 
-// N bytes (2, 4, 8 or a multiple of 16) into words.
-template <int N>
+// N bytes (2, 4, 8 or a multiple of 16) into words.  STREAM: past the caches, where
+// one instruction of the wave takes the whole of every line that it touches.
+template <bool STREAM, typename T>
+__device__ __forceinline__ T load_as(const uint8_t* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  return *reinterpret_cast<const T*>(p);
+}
+template <int N, bool STREAM>
 struct Raw {
   uint32_t w[N < 4 ? 1 : N / 4];
   __device__ __forceinline__ void load(const uint8_t* p) {
     if constexpr (N == 2) {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
+      w[0] = load_as<STREAM, uint16_t>(p);
     } else if constexpr (N == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
+      w[0] = load_as<STREAM, uint32_t>(p);
     } else if constexpr (N == 8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      const words2 v = load_as<STREAM, words2>(p);
       w[0] = v.x, w[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < N / 16; ++i) {
-        const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+        const words4 v = load_as<STREAM, words4>(p + 16 * i);
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
     }
@@ -147,20 +153,47 @@ struct Shape {
   static constexpr int kKBlocks = D / 4 <= F::kBlock ? 1 : D / 4 / F::kBlock;
   static constexpr int kElems = D / 16;                       // of a lane's part of a row of V
   static constexpr int kVBytes = kElems * F::kBits / 8;
+  // A quad whose elements lie in one block shares the loading of its tokens' scales.
+  // (Pairs could too, but NVFP4's step is short of instructions, not of loads: 4 requests
+  // of 120000 in 107 instead of 104 us.)
+  static constexpr int kShare = F::kBlock / kElems >= 4 ? 4 : 1;
 };
 
-// One half (16 tokens) of a tile of K as a lane loads it.
-template <int FMT, int D>
+// One half (16 tokens) of a tile as a lane loads it: of K its part of token
+// 4 (c % 4) + c / 4, so that V's tokens are g, 4 + g, 8 + g and 12 + g, four
+// neighbouring rows to an instruction.
+template <int FMT, int D, bool STREAM>
 struct KHalf {
   using S = Shape<FMT, D>;
-  Raw<S::kKBytes> w;
+  Raw<S::kKBytes, STREAM && S::kKBytes <= 16> w;
   uint32_t s[S::kKBlocks];
 };
-template <int FMT, int D>
+template <int FMT, int D, bool STREAM>
 struct VHalf {
   using S = Shape<FMT, D>;
-  Raw<S::kVBytes> w[4];
-  uint32_t s;                   // scale codes of the four tokens
+  Raw<S::kVBytes, STREAM> w[4];
+  Raw<16 / S::kShare, false> s;      // this lane's share of the scale codes of the half's 16 tokens
+};
+
+// The scale codes of the lane's tokens g, 4 + g, 8 + g and 12 + g, in a word: byte g
+// of each of four words, of which the lane holds one (SHARE lanes together the four) or all.
+struct ScalePick {
+  uint32_t own, pair, quad;
+  __device__ __forceinline__ explicit ScalePick(int c, int g) {
+    own = 0x0C0C0400u + 0x0101u * g;                       // byte g of two words
+    pair = c & 1 ? 0x0C0C0004u + 0x0101u * g : own;        // the even lane's first
+    quad = c & 2 ? 0x01000504u : 0x05040100u;              // two halves, the lower lanes' first
+  }
+  template <int SHARE>
+  __device__ __forceinline__ uint32_t take(const uint32_t* w) const {
+    if constexpr (SHARE == 4) {
+      const uint32_t t = __builtin_amdgcn_perm(dpp<kXor1>(w[0]), w[0], pair);
+      return __builtin_amdgcn_perm(dpp<kXor2>(t), t, quad);
+    } else {
+      return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w[3], w[2], own), __builtin_amdgcn_perm(w[1], w[0], own),
+                                   0x05040100u);
+    }
+  }
 };
 
 // Where a half's codes and scales begin, and how many of its tokens there are: the
@@ -174,7 +207,7 @@ struct HalfPos {
 // waits are apart from the vector loads'.
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;
 
-template <int FMT, int D, int NP>
+template <int FMT, int D, int NP, bool STREAM>
 __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp4lib::AttnArgs a) {
   using F = KvTraits<FMT>;
   using S = Shape<FMT, D>;
@@ -266,17 +299,19 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
   const uint8_t* const codes[2] = {a.cache.codes[0] + kv * a.cache.head, a.cache.codes[1] + kv * a.cache.head};
   const uint8_t* const scales[2] = {a.cache.scales[0] + kv * a.cache.s_head,
                                     a.cache.scales[1] + kv * a.cache.s_head};
-  const uint32_t k_code = c * token + g * S::kKBytes, k_scale = c + g * (D / 4) / F::kBlock * block;
-  const uint32_t v_code = 4 * g * token + c * S::kVBytes, v_scale = 4 * g + c * S::kElems / F::kBlock * block;
-  auto load_k = [&](KHalf<FMT, D>& k, const HalfPos& h) {
+  const uint32_t k_row = 4 * (c & 3) + (c >> 2);
+  const uint32_t k_code = k_row * token + g * S::kKBytes, k_scale = k_row + g * (D / 4) / F::kBlock * block;
+  const uint32_t v_code = g * token + c * S::kVBytes;
+  const uint32_t v_scale = c * S::kElems / F::kBlock * block + c % S::kShare * (16 / S::kShare);
+  auto load_k = [&](KHalf<FMT, D, STREAM>& k, const HalfPos& h) {
     k.w.load(codes[0] + h.code + k_code);
 #pragma unroll
     for (int b = 0; b < S::kKBlocks; ++b) k.s[b] = (scales[0] + h.scale)[k_scale + b * block];
   };
-  auto load_v = [&](VHalf<FMT, D>& v, const HalfPos& h) {
+  auto load_v = [&](VHalf<FMT, D, STREAM>& v, const HalfPos& h) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v.w[j].load(codes[1] + h.code + (v_code + j * token));
-    v.s = *reinterpret_cast<const uint32_t*>(scales[1] + h.scale + v_scale);
+    for (int j = 0; j < 4; ++j) v.w[j].load(codes[1] + h.code + (v_code + 4 * j * token));
+    v.s.load(scales[1] + h.scale + v_scale);
   };
 
   // A tile's loads are issued while the tile before it is worked on: K's when its
@@ -286,9 +321,10 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
   // all of them at once.
   int t = begin + wave * kTile;
   if (t < end) {
+  const ScalePick pick(c, g);
   HalfPos h[2];
-  KHalf<FMT, D> k[2];
-  VHalf<FMT, D> v[2];
+  KHalf<FMT, D, STREAM> k[2];
+  VHalf<FMT, D, STREAM> v[2];
   int pages[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -319,7 +355,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
       if (h[i].n < 16) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (4 * g + j >= h[i].n) x[i][j] = -__builtin_inff();
+          if (4 * j + g >= h[i].n) x[i][j] = -__builtin_inff();
       }
     }
 #pragma unroll
@@ -359,25 +395,28 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
 
     // V: what is not there is zero codes and scales, whatever the memory holds;
     // pairs of elements of the eight tokens, then pairs of tokens
+    uint32_t own[2];              // scale codes of the lane's four tokens
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      own[i] = pick.take<S::kShare>(v[i].s.w);
       if (h[i].n < 16) {
-        const int n = h[i].n - 4 * g;
+        const int n = h[i].n - g;                 // token 4 j + g is there if 4 j < n
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          if (j >= n)
+          if (4 * j >= n) {
 #pragma unroll
             for (auto& w : v[i].w[j].w) w = 0;
-        v[i].s &= n <= 0 ? 0u : n >= 4 ? ~0u : (1u << (8 * n)) - 1u;
+            own[i] &= ~(0xFFu << (8 * j));
+          }
       }
     }
     uint32_t sc[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      sc[4 * i] = scale_for<FMT, 0>(v[i].s);
-      sc[4 * i + 1] = scale_for<FMT, 1>(v[i].s);
-      sc[4 * i + 2] = scale_for<FMT, 2>(v[i].s);
-      sc[4 * i + 3] = scale_for<FMT, 3>(v[i].s);
+      sc[4 * i] = scale_for<FMT, 0>(own[i]);
+      sc[4 * i + 1] = scale_for<FMT, 1>(own[i]);
+      sc[4 * i + 2] = scale_for<FMT, 2>(own[i]);
+      sc[4 * i + 3] = scale_for<FMT, 3>(own[i]);
     }
     constexpr int kPart = S::kElems < 8 ? S::kElems : 8;      // elements at once
 #pragma unroll
@@ -493,10 +532,15 @@ template <>
 hipError_t launch_attention_fmt<FP4_KV_FMT>(const AttnArgs& a, uint32_t grid, hipStream_t s) {
   return with_dim(a.cache.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (a.q.heads / a.cache.heads <= 8)
-      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, 1>), dim3(grid), dim3(64 * kWaves), 0, s, a);
-    else
-      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, 2>), dim3(grid), dim3(64 * kWaves), 0, s, a);
+    auto launch = [&](auto np, auto stream) {
+      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, decltype(np)::value, decltype(stream)::value>), dim3(grid),
+                         dim3(64 * kWaves), 0, s, a);
+    };
+    const bool few = a.q.heads / a.cache.heads <= 8;
+    if (few && a.stream) launch(Const<1>(), Const<1>());
+    else if (few) launch(Const<1>(), Const<0>());
+    else if (a.stream) launch(Const<2>(), Const<1>());
+    else launch(Const<2>(), Const<0>());
     return hipGetLastError();
   });
 }

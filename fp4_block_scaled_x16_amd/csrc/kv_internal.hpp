@@ -52,7 +52,7 @@ struct QkRowsArgs {
   const int64_t* slots;
   int64_t tokens;
   int head_dim, cached;
-  int part[4], per_wave;       // set by the launcher
+  int part[4];                 // set by the launcher
 };
 
 struct QkGradArgs {
@@ -89,6 +89,7 @@ struct AttnArgs {
   float* part;                 // workspace: null with splits == 1
   int64_t part_bytes;
   int splits, min_part;        // set by the launcher
+  int stream;                  // set by the launcher: codes are read past the caches
 };
 
 hipError_t launch_qk_rows(const QkRowsArgs& a, hipStream_t s);

@@ -18,30 +18,34 @@ using namespace kvdev;
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kManyRows = 4;
+constexpr int kRowWaves = 8;      // of a workgroup of the forward pass, at most
 
-// The lane's 8 elements of a rotation: y = x c + xp s, xp being their partners
+// "half" style: element from which the partners of the lane's elements d0 .. lie;
+// -1 where they are neighbours, or not turned.
+__device__ __forceinline__ int partner_of(const fp4lib::NormArgs& n, int d0) {
+  if (!n.table || n.interleaved || d0 >= 2 * n.pairs) return -1;
+  return d0 < n.pairs ? d0 + n.pairs : d0 - n.pairs;
+}
+
+// The rotation of the lane's 8 elements: y = x c + xp s, xp being their partners
 // (the sign of sin is in s).
 struct Turn {
   float c[8], s[8];
-  int partner;          // "half": element from which the partners lie; else -1
-  bool turned;
 };
 
-template <int D>
-__device__ __forceinline__ Turn turn_of(const fp4lib::NormArgs& n, int64_t token, int d0) {
+__device__ __forceinline__ Turn turn_of(const fp4lib::NormArgs& n, int64_t token, int d0, int partner) {
   Turn t;
-  t.turned = n.table && d0 < 2 * n.pairs;
-  t.partner = -1;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     t.c[i] = 1.0f;
     t.s[i] = 0.0f;
   }
-  if (!t.turned) return t;
+  if (!n.table || d0 >= 2 * n.pairs) return t;
   const int64_t pos = n.positions[token];
   const bool in = pos >= 0 && pos < n.table_rows;       // outside the table: NaN, and no access
   const float* row = n.table + (in ? pos : 0) * (2 * n.pairs);
-  if (n.interleaved) {
+  if (partner < 0) {
     const float4 c = *reinterpret_cast<const float4*>(row + d0 / 2);
     const float4 s = *reinterpret_cast<const float4*>(row + n.pairs + d0 / 2);
     const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
@@ -52,8 +56,7 @@ __device__ __forceinline__ Turn turn_of(const fp4lib::NormArgs& n, int64_t token
     }
   } else {
     const bool first = d0 < n.pairs;
-    t.partner = first ? d0 + n.pairs : d0 - n.pairs;
-    const float* p = row + (first ? d0 : d0 - n.pairs);
+    const float* p = row + (first ? d0 : partner);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const float4 c = *reinterpret_cast<const float4*>(p + 4 * h);
@@ -73,15 +76,23 @@ __device__ __forceinline__ Turn turn_of(const fp4lib::NormArgs& n, int64_t token
   return t;
 }
 
-// The partners of the lane's elements v of the row at p.
-__device__ __forceinline__ void partners(float (&vp)[8], const float (&v)[8], const uint16_t* p, const Turn& t) {
-  if (t.partner >= 0) {
-    load8(vp, p + t.partner);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) vp[i] = v[i ^ 1];
+// A lane's elements of a row and, in "half" style, their partners, as they lie in memory.
+struct RawRow {
+  uint4 v, p;
+  __device__ __forceinline__ void load(const uint16_t* row, int d0, int partner) {
+    v = *reinterpret_cast<const uint4*>(row + d0);
+    if (partner >= 0) p = *reinterpret_cast<const uint4*>(row + partner);
   }
-}
+  __device__ __forceinline__ void values(float (&x)[8], float (&xp)[8], int partner) const {
+    fp4quant::unpack8(v, x);
+    if (partner >= 0) {
+      fp4quant::unpack8(p, xp);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) xp[i] = x[i ^ 1];
+    }
+  }
+};
 
 __device__ __forceinline__ void weights(float (&w)[8], const fp4lib::NormArgs& n, int which, int d) {
   if (!n.w[which]) {
@@ -101,85 +112,82 @@ __device__ __forceinline__ float inv_rms(const float (&v)[8], float eps) {
   float q = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) q = __builtin_fmaf(v[i], v[i], q);
-  return 1.0f / __builtin_sqrtf(lane_sum<D / 8>(q) * (1.0f / D) + eps);
+  return __builtin_amdgcn_rsqf(lane_sum<D / 8>(q) * (1.0f / D) + eps);      // within an ulp
 }
 
-// Iterations of a token: ceil(heads / rows of a wave) for q, then k, then v.
-template <int D, int FMT>
-__global__ __launch_bounds__(kThreads) void k_qk_rows(fp4lib::QkRowsArgs a) {
+// A wave has R times 64 / (D / 8) rows of one token, all of q, of k or of v
+// (a.part[kind] is the first wave of the kind), whose loads it issues before
+// anything else; a workgroup has neighbouring rows of a token.
+template <int D, int FMT, int R>
+__global__ __launch_bounds__(64 * kRowWaves) void k_qk_rows(fp4lib::QkRowsArgs a) {
   constexpr int kLanes = D / 8, kRows = 64 / kLanes;
   const int lane = threadIdx.x & 63;
-  const int64_t token =
-      static_cast<int64_t>(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (token >= a.tokens) return;
-  const int row = lane / kLanes, d0 = lane % kLanes * 8;
-  const Turn t = turn_of<D>(a.norm, token, d0);
-  const bool norm = a.norm.w[0] != nullptr;
+  const int64_t token = blockIdx.x;
+  const int part = blockIdx.y * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (part >= a.part[3]) return;
+  const int kind = part < a.part[1] ? 0 : part < a.part[2] ? 1 : 2;
+  const fp4lib::HeadsArgs& in = a.in[kind];
+  const int d0 = lane % kLanes * 8, head0 = (part - a.part[kind]) * (R * kRows) + lane / kLanes;
+  const int partner = kind < 2 ? partner_of(a.norm, d0) : -1;
+  RawRow raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int head = head0 + i * kRows < in.heads ? head0 + i * kRows : 0;
+    raw[i].load(in.x + token * in.token + static_cast<int64_t>(head) * in.head, d0, partner);
+  }
+
+  // where k and v go
   int64_t page = 0;
   int place = 0;
-  bool kept = false;
-  float s_enc[2], s_dec[2];
-  if constexpr (FMT >= 0) {
+  float s_enc = 1.0f, s_dec = 1.0f;
+  if (FMT >= 0 && kind > 0) {
     const int64_t slot = a.slots[token];
     page = slot >> a.cache.page_shift;
     place = static_cast<int>(slot & ((1 << a.cache.page_shift) - 1));
-    kept = slot >= 0 && page < a.cache.pages;
-    tensor_scales<FMT>(a.cache, 0, s_enc[0], s_dec[0]);
-    tensor_scales<FMT>(a.cache, 1, s_enc[1], s_dec[1]);
+    if (slot < 0 || page >= a.cache.pages) return;
+    tensor_scales<FMT>(a.cache, kind - 1, s_enc, s_dec);
   }
-  const int first = blockIdx.y * a.per_wave, last = min(first + a.per_wave, a.part[3]);
-  for (int kind = 0; kind < 3; ++kind) {
-    const int lo = max(first, a.part[kind]), hi = min(last, a.part[kind + 1]);
-    if (lo >= hi) continue;
-    if (FMT >= 0 && kind > 0 && !kept) continue;
-    const fp4lib::HeadsArgs& in = a.in[kind];
-    // w c and (partner's w) s: y = r (x wc + xp ws)
-    float wc[8], ws[8];
+  // y = r (x wc + xp ws): w c, and the partner's w s
+  float wc[8], ws[8];
+  if (kind < 2) {
+    const Turn t = turn_of(a.norm, token, d0, partner);
+    weights(wc, a.norm, kind, d0);
+    if (partner >= 0) {
+      weights(ws, a.norm, kind, partner);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ws[i] = wc[i ^ 1];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      wc[i] *= t.c[i];
+      ws[i] *= t.s[i];
+    }
+  }
+  const bool norm = a.norm.w[0] != nullptr, turned = a.norm.table && d0 < 2 * a.norm.pairs;
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int head = head0 + i * kRows;
+    float v[8], vp[8];
+    raw[i].values(v, vp, partner);
     if (kind < 2) {
-      weights(wc, a.norm, kind, d0);
-      if (t.partner >= 0) {
-        weights(ws, a.norm, kind, t.partner);
-      } else {
+      const float r = norm ? inv_rms<D>(v, a.norm.eps) : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ws[i] = wc[i ^ 1];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        wc[i] *= t.c[i];
-        ws[i] *= t.s[i];
+      for (int e = 0; e < 8; ++e) {
+        float y = v[e] * wc[e];
+        if (turned) y = __builtin_fmaf(vp[e], ws[e], y);
+        v[e] = y * r;
       }
     }
-    for (int it = lo; it < hi; ++it) {
-      const int head = (it - a.part[kind]) * kRows + row;
-      const bool valid = head < in.heads;
-      const uint16_t* p = in.x + token * in.token + static_cast<int64_t>(valid ? head : 0) * in.head;
-      float v[8];
-      load8(v, p + d0);
-      if (kind < 2) {
-        float vp[8];
-        if (t.turned) partners(vp, v, p, t);
-        const float r = norm ? inv_rms<D>(v, a.norm.eps) : 1.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float y = v[i] * wc[i];
-          if (t.turned) y = __builtin_fmaf(vp[i], ws[i], y);
-          v[i] = y * r;
-        }
-      }
-      if constexpr (FMT >= 0) {
-        if (kind > 0) {
-          // a row's lanes are valid together, and so are those of a block
-          if (valid)
-            encode_row<FMT, D>(v, lane % kLanes, a.cache, kind - 1, page, place, head, s_enc[kind - 1],
-                               s_dec[kind - 1]);
-          continue;
-        }
-      }
-      if (valid && kind < 2) {
-        const fp4lib::HeadsArgs& out = a.out[kind];
-        store8(out.x + token * out.token + head * out.head + d0, v);
+    if (head >= in.heads) continue;          // a row's lanes together
+    if constexpr (FMT >= 0) {
+      if (kind > 0) {
+        encode_row<FMT < 0 ? 0 : FMT, D>(v, lane % kLanes, a.cache, kind - 1, page, place, head, s_enc, s_dec);
+        continue;
       }
     }
+    const fp4lib::HeadsArgs& out = a.out[kind];
+    store8(out.x + token * out.token + head * out.head + d0, v);
   }
 }
 
@@ -207,25 +215,39 @@ __global__ __launch_bounds__(kThreads) void k_qk_grad(fp4lib::QkGradArgs a) {
   for (int i = 0; i < 8; ++i) dw[i] = 0.0f;
   int64_t token = begin / iters;
   int it = static_cast<int>(begin - token * iters);
+  const int partner = partner_of(a.norm, d0);
+  const bool turned = a.norm.table && d0 < 2 * a.norm.pairs;
   Turn t;
-  bool fresh = true;
+  RawRow rx, ry;
+  auto load = [&](RawRow& x, RawRow& y, int64_t token, int it) {
+    const int64_t h = it * kRows + row < hx.heads ? it * kRows + row : 0;
+    // read once, past the caches (57 instead of 65 us for 8192 tokens; dy's line is read
+    // again for the partners)
+    x.v = __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const words4*>(
+                                        hx.x + token * hx.token + h * hx.head + d0)));
+    y.load(hdy.x + token * hdy.token + h * hdy.head, d0, partner);
+  };
+  if (begin < end) {
+    load(rx, ry, token, it);
+    t = turn_of(a.norm, token, d0, partner);
+  }
   for (int64_t task = begin; task < end; ++task) {
-    if (fresh) t = turn_of<D>(a.norm, token, d0);
-    fresh = false;
-    const int head = it * kRows + row;
-    const bool valid = head < hx.heads;
-    const int64_t h = valid ? head : 0;
-    const uint16_t* px = hx.x + token * hx.token + h * hx.head;
-    const uint16_t* py = hdy.x + token * hdy.token + h * hdy.head;
-    float x[8], dz[8];
-    load8(x, px + d0);
-    load8(dz, py + d0);
-    if (t.turned) {
-      float dp[8];
-      partners(dp, dz, py, t);
+    const int64_t h = it * kRows + row;
+    const bool valid = h < hx.heads;
+    uint16_t* out = hdx.x + token * hdx.token + h * hdx.head + d0;
+    float x[8], dz[8], dp[8];
+    fp4quant::unpack8(rx.v, x);
+    ry.values(dz, dp, partner);
+    if (turned) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) dz[i] = dz[i] * t.c[i] - dp[i] * t.s[i];
     }
+    // the next rows' loads, before these are worked on (behind the last: these again)
+    const bool turn_page = it + 1 == iters && task + 1 < end;
+    if (task + 1 < end) it = turn_page ? 0 : it + 1;
+    if (turn_page) ++token;
+    load(rx, ry, token, it);
+    if (turn_page) t = turn_of(a.norm, token, d0, partner);
     if (norm) {
       const float r = inv_rms<D>(x, a.norm.eps);
       float gx = 0.0f;
@@ -241,12 +263,7 @@ __global__ __launch_bounds__(kThreads) void k_qk_grad(fp4lib::QkGradArgs a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) dz[i] = r * (dz[i] - x[i] * m);
     }
-    if (valid) store8(hdx.x + token * hdx.token + h * hdx.head + d0, dz);
-    if (++it == iters) {
-      it = 0;
-      ++token;
-      fresh = true;
-    }
+    if (valid) store8(out, dz);
   }
   if (!norm || !a.part) return;
 #pragma unroll
@@ -260,48 +277,56 @@ __global__ __launch_bounds__(kThreads) void k_qk_grad(fp4lib::QkGradArgs a) {
   }
 }
 
-// The workgroups' sums in their order: 32 columns per workgroup, 8 threads each.
-__global__ __launch_bounds__(256) void k_qk_grad_join(fp4lib::QkGradArgs a) {
-  __shared__ float sum[8][32];
+// The workgroups' sums in their order: 32 columns per workgroup, 32 threads each.
+__global__ __launch_bounds__(1024) void k_qk_grad_join(fp4lib::QkGradArgs a) {
+  __shared__ float sum[32][33];
   const int which = blockIdx.y, col = threadIdx.x & 31, r = threadIdx.x >> 5;
   if (!a.dw[which]) return;
   const float* p = a.part + (which ? static_cast<int64_t>(a.groups[0]) * a.head_dim : 0) + blockIdx.x * 32 + col;
   float v = 0.0f;
-#pragma unroll 8
-  for (int g = r; g < a.groups[which]; g += 8) v += p[static_cast<int64_t>(g) * a.head_dim];
+#pragma unroll 16
+  for (int g = r; g < a.groups[which]; g += 32) v += p[static_cast<int64_t>(g) * a.head_dim];
   sum[r][col] = v;
   __syncthreads();
-  if (r) return;
-  for (int k = 1; k < 8; ++k) v += sum[k][col];
-  float* dw = a.dw[which] + blockIdx.x * 32 + col;
+  // thread (row r, column col): sums of column r of this workgroup's 32
+  v = sum[col][r];
+  v = lane_sum<32>(v);
+  if (col) return;
+  float* dw = a.dw[which] + blockIdx.x * 32 + r;
   *dw = a.accumulate ? *dw + v : v;
 }
 
-constexpr int kGradGroupsPerCu = 4;
+// What the registers leave room for at once (8192 tokens of 32 + 8 heads of 128: 3 / 4 / 5 / 8
+// per CU 62.6 / 56.7 / 53.4 / 58.2 us).
+constexpr int kGradGroupsPerCu = 5;
 
 }  // namespace
 
 namespace fp4lib {
 
+// kManyRows for long sequences (8192 tokens of 32 + 8 heads of 128, before the stores went past
+// the caches: R = 1 / 2 / 3 / 4 / 5 50 / 41.5 / 40.2 / 39.2 / 41.4 us; of one token's waves in one
+// workgroup, with 4 tokens' waves of one kind instead 41.3); 1 where that leaves CUs with
+// fewer than 8 waves.
 hipError_t launch_qk_rows(const QkRowsArgs& args, hipStream_t s) {
   QkRowsArgs a = args;
-  const int rows = 512 / a.head_dim;       // of a wave
-  for (int i = 0; i < 3; ++i) a.part[i + 1] = a.part[i] + (a.in[i].x ? (a.in[i].heads + rows - 1) / rows : 0);
-  // enough waves for 16 on a CU before a wave takes several rows
-  const int64_t want = a.tokens * a.part[3] / (16 * static_cast<int64_t>(device_cu_count()));
-  a.per_wave = static_cast<int>(want < 1 ? 1 : want < a.part[3] ? want : a.part[3]);
-  const dim3 grid(static_cast<uint32_t>((a.tokens + kWaves - 1) / kWaves),
-                  (a.part[3] + a.per_wave - 1) / a.per_wave);
+  auto parts = [&](int r) {
+    const int rows = r * 512 / a.head_dim;       // of a wave
+    for (int i = 0; i < 3; ++i) a.part[i + 1] = a.part[i] + (a.in[i].x ? (a.in[i].heads + rows - 1) / rows : 0);
+    return a.part[3];
+  };
+  const bool many = a.tokens * parts(kManyRows) >= 8 * static_cast<int64_t>(device_cu_count());
+  const int all = many ? a.part[3] : parts(1), waves = all < kRowWaves ? all : kRowWaves;
+  const dim3 grid(static_cast<uint32_t>(a.tokens), (all + waves - 1) / waves), block(64 * waves);
   return with_dim(a.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (!a.cached) {
-      hipLaunchKernelGGL((k_qk_rows<D, -1>), grid, dim3(kThreads), 0, s, a);
+    auto launch = [&](auto f) {
+      constexpr int F = decltype(f)::value;
+      if (many) hipLaunchKernelGGL((k_qk_rows<D, F, kManyRows>), grid, block, 0, s, a);
+      else hipLaunchKernelGGL((k_qk_rows<D, F, 1>), grid, block, 0, s, a);
       return hipGetLastError();
-    }
-    return with_format(a.cache.fmt, [&](auto f) {
-      hipLaunchKernelGGL((k_qk_rows<D, decltype(f)::value>), grid, dim3(kThreads), 0, s, a);
-      return hipGetLastError();
-    });
+    };
+    return a.cached ? with_format(a.cache.fmt, launch) : launch(Const<-1>());
   });
 }
 
@@ -328,7 +353,7 @@ hipError_t launch_qk_grad(const QkGradArgs& args, hipStream_t s) {
   return with_dim(a.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
     if (all) hipLaunchKernelGGL(k_qk_grad<D>, dim3(a.groups[0] + a.groups[1]), dim3(kThreads), 0, s, a);
-    if (a.dw[0] || a.dw[1]) hipLaunchKernelGGL(k_qk_grad_join, dim3(D / 32, 2), dim3(256), 0, s, a);
+    if (a.dw[0] || a.dw[1]) hipLaunchKernelGGL(k_qk_grad_join, dim3(D / 32, 2), dim3(1024), 0, s, a);
     return hipGetLastError();
   });
 }
