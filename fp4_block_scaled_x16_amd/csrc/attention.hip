@@ -159,6 +159,13 @@ struct Shape {
   static constexpr int kShare = F::kBlock / kElems >= 4 ? 4 : 1;
 };
 
+// Where a half's codes and scales begin, and how many of its tokens there are: the
+// same for the whole wave, so a load is that address plus the lane's own offset.
+struct HalfPos {
+  int64_t code, scale;
+  int n;
+};
+
 // One half (16 tokens) of a tile as a lane loads it: of K its part of token
 // 4 (c % 4) + c / 4, so that V's tokens are g, 4 + g, 8 + g and 12 + g, four
 // neighbouring rows to an instruction.
@@ -196,26 +203,19 @@ struct ScalePick {
   }
 };
 
-// Where a half's codes and scales begin, and how many of its tokens there are: the
-// same for the whole wave, so a load is that address plus the lane's own offset.
-struct HalfPos {
-  int64_t code, scale;
-  int n;
-};
-
 // Read through the scalar cache (the kernel does not write the page table), whose
 // waits are apart from the vector loads'.
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;
 
-template <int FMT, int D, int NP, bool STREAM>
-__global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp4lib::AttnArgs a) {
+template <int FMT, int D, int NP, bool STREAM, int W>
+__global__ __launch_bounds__(64 * W, W == kWaves ? waves_per_simd(D) : 2) void k_attention(fp4lib::AttnArgs a) {
   using F = KvTraits<FMT>;
   using S = Shape<FMT, D>;
   constexpr bool kF16 = F::kTwoLevel;
   constexpr int kHeads = NP == 1 ? 8 : 16;                   // query heads of a workgroup
   // fp16 holds p down to 2^-24: its largest, 2^kSlack, is moved up by 2^7
   constexpr float kShift = kF16 ? 7.0f : 0.0f;
-  __shared__ float meet[kWaves - 1][S::kElems * 4 + 2][64];
+  __shared__ float meet[W - 1][S::kElems * 4 + 2][64];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -282,16 +282,17 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
 
   const ConstInts table = (ConstInts)(a.table + request * a.table_stride);
   const int mask = (1 << a.cache.page_shift) - 1;
-  // (behind the last token: the last one's page)
+  // (behind the last token: the 16 tokens with the last one, whose lines are near)
   auto page_at = [&](int t) { return table[min(t, end - 1) >> a.cache.page_shift]; };
   auto half_at = [&](int t, int page) {
     HalfPos h;
     const bool there = page >= 0 && page < a.cache.pages;     // else its tokens are masked
+    const int place = min(t, end - 1) & mask & ~15;
     h.n = end - t > 16 ? 16 : end - t;
     if (!there || h.n < 0) h.n = 0;
     if (!there) page = 0;
-    h.code = page * a.cache.page + static_cast<int64_t>(t & mask) * a.cache.token;
-    h.scale = page * a.cache.s_page + (t & mask);
+    h.code = page * a.cache.page + static_cast<int64_t>(place) * a.cache.token;
+    h.scale = page * a.cache.s_page + place;
     return h;
   };
   // the lane's offsets (below 2^31: kv_api.cpp)
@@ -315,137 +316,137 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
   };
 
   // A tile's loads are issued while the tile before it is worked on: K's when its
-  // scores are done, V's when its products are; its pages are looked up a tile
-  // earlier still.  The last tile's successor is loaded too (from a page that is
-  // there) and not used: a branch around the loads would make the compiler wait for
-  // all of them at once.
-  int t = begin + wave * kTile;
-  if (t < end) {
+  // scores are done, V's when its products are; its pages are looked up a tile earlier
+  // still.  They are not branched around at the end (the compiler would wait for all of
+  // them at once): the last 16 tokens are loaded again then, and not used.  (Two tiles
+  // under way at lower occupancy were no faster at any size.)
   const ScalePick pick(c, g);
   HalfPos h[2];
   KHalf<FMT, D, STREAM> k[2];
   VHalf<FMT, D, STREAM> v[2];
-  int pages[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    h[i] = half_at(t + 16 * i, page_at(t + 16 * i));
-    load_k(k[i], h[i]);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    load_v(v[i], h[i]);
-    pages[i] = page_at(t + kWaves * kTile + 16 * i);
-  }
-  do {
-    t += kWaves * kTile;
-    const HalfPos next[2] = {half_at(t, pages[0]), half_at(t + 16, pages[1])};
-    floatx4 x[2];
+  int t = begin + wave * kTile;
+  if (t < end) {
+    int pages[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      x[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int n = 0; n < S::kSteps; ++n) {
-        // elements 8 n .. of the lane's part lie in one block
-        const uint32_t sc = scale_for<FMT, 0>(k[i].s[8 * n / F::kBlock < S::kKBlocks ? 8 * n / F::kBlock : 0]);
-        uintx4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = widen_pair<FMT>(k[i].w.w, 4 * n + e, sc, 0);
-        x[i] = mfma<kF16>(w, q[n], x[i]);
-      }
-      if (h[i].n < 16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * j + g >= h[i].n) x[i][j] = -__builtin_inff();
-      }
+      h[i] = half_at(t + 16 * i, page_at(t + 16 * i));
+      load_k(k[i], h[i]);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      load_k(k[i], next[i]);
-      pages[i] = page_at(t + kWaves * kTile + 16 * i);
-    }
-
-    float best = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
-                       fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]))) * factor;
-    if (__any(best > top + kSlack)) {
-      best = fmaxf(best, __shfl_xor(best, 16, 64));
-      best = fmaxf(best, __shfl_xor(best, 32, 64));
-      const float to = fmaxf(top, best);
-      const float by = to == top ? 1.0f : __builtin_amdgcn_exp2f(top - to);
-      top = to;
-      total *= by;
-#pragma unroll
-      for (int i = 0; i < S::kElems; ++i) acc[i] *= by;
-    }
-    const float from = top == -__builtin_inff() ? 0.0f : top - kShift;
-    uintx4 p, rest;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float u = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2)], factor, -from));
-      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2) + 1], factor, -from));
-      total += u + w;
-      const uint32_t hi = pack2<kF16>(u, w);
-      const uint32_t lo = pack2<kF16>(u - unpack_lo<kF16>(hi), w - unpack_hi<kF16>(hi));
-      if constexpr (NP == 1) {
-        p[j] = c < 8 ? hi : lo;
-      } else {
-        p[j] = hi;
-        rest[j] = lo;
-      }
-    }
-
-    // V: what is not there is zero codes and scales, whatever the memory holds;
-    // pairs of elements of the eight tokens, then pairs of tokens
-    uint32_t own[2];              // scale codes of the lane's four tokens
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      own[i] = pick.take<S::kShare>(v[i].s.w);
-      if (h[i].n < 16) {
-        const int n = h[i].n - g;                 // token 4 j + g is there if 4 j < n
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (4 * j >= n) {
-#pragma unroll
-            for (auto& w : v[i].w[j].w) w = 0;
-            own[i] &= ~(0xFFu << (8 * j));
-          }
-      }
-    }
-    uint32_t sc[8];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      sc[4 * i] = scale_for<FMT, 0>(own[i]);
-      sc[4 * i + 1] = scale_for<FMT, 1>(own[i]);
-      sc[4 * i + 2] = scale_for<FMT, 2>(own[i]);
-      sc[4 * i + 3] = scale_for<FMT, 3>(own[i]);
-    }
-    constexpr int kPart = S::kElems < 8 ? S::kElems : 8;      // elements at once
-#pragma unroll
-    for (int e0 = 0; e0 < S::kElems; e0 += kPart) {
-      uint32_t w[8][kPart / 2];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < kPart / 2; ++e)
-          w[j][e] = widen_pair<FMT>(v[j / 4].w[j % 4].w, e0 / 2 + e, sc[j], j & 1);
-#pragma unroll
-      for (int e = 0; e < kPart; ++e) {
-        const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
-        uintx4 o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2], sel);
-        acc[e0 + e] = mfma<kF16>(o, p, acc[e0 + e]);
-        if constexpr (NP == 2) acc[e0 + e] = mfma<kF16>(o, rest, acc[e0 + e]);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      h[i] = next[i];
       load_v(v[i], h[i]);
+      pages[i] = page_at(t + W * kTile + 16 * i);
     }
-  } while (t < end);
+    do {
+      t += W * kTile;
+      const HalfPos next[2] = {half_at(t, pages[0]), half_at(t + 16, pages[1])};
+      floatx4 x[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int n = 0; n < S::kSteps; ++n) {
+          // elements 8 n .. of the lane's part lie in one block
+          const uint32_t sc = scale_for<FMT, 0>(k[i].s[8 * n / F::kBlock < S::kKBlocks ? 8 * n / F::kBlock : 0]);
+          uintx4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = widen_pair<FMT>(k[i].w.w, 4 * n + e, sc, 0);
+          x[i] = mfma<kF16>(w, q[n], x[i]);
+        }
+        if (h[i].n < 16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (4 * j + g >= h[i].n) x[i][j] = -__builtin_inff();
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        load_k(k[i], next[i]);
+        pages[i] = page_at(t + W * kTile + 16 * i);
+      }
+
+      float best = fmaxf(fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3])),
+                         fmaxf(fmaxf(x[1][0], x[1][1]), fmaxf(x[1][2], x[1][3]))) * factor;
+      if (__any(best > top + kSlack)) {
+        best = fmaxf(best, __shfl_xor(best, 16, 64));
+        best = fmaxf(best, __shfl_xor(best, 32, 64));
+        const float to = fmaxf(top, best);
+        const float by = to == top ? 1.0f : __builtin_amdgcn_exp2f(top - to);
+        top = to;
+        total *= by;
+#pragma unroll
+        for (int i = 0; i < S::kElems; ++i) acc[i] *= by;
+      }
+      const float from = top == -__builtin_inff() ? 0.0f : top - kShift;
+      uintx4 p, rest;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float u = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2)], factor, -from));
+        const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2) + 1], factor, -from));
+        total += u + w;
+        const uint32_t hi = pack2<kF16>(u, w);
+        const uint32_t lo = pack2<kF16>(u - unpack_lo<kF16>(hi), w - unpack_hi<kF16>(hi));
+        if constexpr (NP == 1) {
+          p[j] = c < 8 ? hi : lo;
+        } else {
+          p[j] = hi;
+          rest[j] = lo;
+        }
+      }
+
+      // V: what is not there is zero codes and scales, whatever the memory holds;
+      // pairs of elements of the eight tokens, then pairs of tokens
+      uint32_t own[2];              // scale codes of the lane's four tokens
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        own[i] = pick.take<S::kShare>(v[i].s.w);
+        if (h[i].n < 16) {
+          const int n = h[i].n - g;                 // token 4 j + g is there if 4 j < n
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (4 * j >= n) {
+#pragma unroll
+              for (auto& w : v[i].w[j].w) w = 0;
+              own[i] &= ~(0xFFu << (8 * j));
+            }
+        }
+      }
+      uint32_t sc[8];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sc[4 * i] = scale_for<FMT, 0>(own[i]);
+        sc[4 * i + 1] = scale_for<FMT, 1>(own[i]);
+        sc[4 * i + 2] = scale_for<FMT, 2>(own[i]);
+        sc[4 * i + 3] = scale_for<FMT, 3>(own[i]);
+      }
+      constexpr int kPart = S::kElems < 8 ? S::kElems : 8;      // elements at once
+#pragma unroll
+      for (int e0 = 0; e0 < S::kElems; e0 += kPart) {
+        uint32_t w[8][kPart / 2];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < kPart / 2; ++e)
+            w[j][e] = widen_pair<FMT>(v[j / 4].w[j % 4].w, e0 / 2 + e, sc[j], j & 1);
+#pragma unroll
+        for (int e = 0; e < kPart; ++e) {
+          const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
+          uintx4 o;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2], sel);
+          acc[e0 + e] = mfma<kF16>(o, p, acc[e0 + e]);
+          if constexpr (NP == 2) acc[e0 + e] = mfma<kF16>(o, rest, acc[e0 + e]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        h[i] = next[i];
+        load_v(v[i], h[i]);
+      }
+    } while (t < end);
   }
 
-  // the four waves' sums, lane by lane, in the first
+  // the waves' sums, lane by lane, in the first
   total += __shfl_xor(total, 16, 64);
   total += __shfl_xor(total, 32, 64);
   if (wave) {
@@ -461,7 +462,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
   if (wave) return;
   float all = top;
 #pragma unroll
-  for (int w = 0; w < kWaves - 1; ++w) all = fmaxf(all, meet[w][4 * S::kElems][lane]);
+  for (int w = 0; w < W - 1; ++w) all = fmaxf(all, meet[w][4 * S::kElems][lane]);
   const float ref = all == -__builtin_inff() ? 0.0f : all;
   {
     const float by = __builtin_amdgcn_exp2f(top - ref);
@@ -470,7 +471,7 @@ __global__ __launch_bounds__(64 * kWaves, waves_per_simd(D)) void k_attention(fp
     for (int e = 0; e < S::kElems; ++e) acc[e] *= by;
   }
 #pragma unroll
-  for (int w = 0; w < kWaves - 1; ++w) {
+  for (int w = 0; w < W - 1; ++w) {
     const float by = __builtin_amdgcn_exp2f(meet[w][4 * S::kElems][lane] - ref);
     total += by * meet[w][4 * S::kElems + 1][lane];
 #pragma unroll
@@ -532,15 +533,23 @@ template <>
 hipError_t launch_attention_fmt<FP4_KV_FMT>(const AttnArgs& a, uint32_t grid, hipStream_t s) {
   return with_dim(a.cache.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
-    auto launch = [&](auto np, auto stream) {
-      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, decltype(np)::value, decltype(stream)::value>), dim3(grid),
-                         dim3(64 * kWaves), 0, s, a);
+    auto launch = [&](auto np, auto stream, auto waves) {
+      constexpr int W = decltype(waves)::value;
+      hipLaunchKernelGGL((k_attention<FP4_KV_FMT, D, decltype(np)::value, decltype(stream)::value, W>), dim3(grid),
+                         dim3(64 * W), 0, s, a);
     };
     const bool few = a.q.heads / a.cache.heads <= 8;
-    if (few && a.stream) launch(Const<1>(), Const<1>());
-    else if (few) launch(Const<1>(), Const<0>());
-    else if (a.stream) launch(Const<2>(), Const<1>());
-    else launch(Const<2>(), Const<0>());
+    if constexpr (D <= kWideDim) {
+      if (a.wide) {
+        if (few) launch(Const<1>(), Const<0>(), Const<kWideWaves>());
+        else launch(Const<2>(), Const<0>(), Const<kWideWaves>());
+        return hipGetLastError();
+      }
+    }
+    if (few && a.stream) launch(Const<1>(), Const<1>(), Const<kWaves>());
+    else if (few) launch(Const<1>(), Const<0>(), Const<kWaves>());
+    else if (a.stream) launch(Const<2>(), Const<1>(), Const<kWaves>());
+    else launch(Const<2>(), Const<0>(), Const<kWaves>());
     return hipGetLastError();
   });
 }
