@@ -117,28 +117,40 @@ __device__ __forceinline__ uint32_t scale_for(uint32_t word) {
     return ((word >> (8 * B)) & 0xFFu) << 23;
 }
 
+// An address in scalar registers, of global memory: without this the compiler adds the
+// lane's offset to the loop's invariant part and keeps 64-bit sums for every load in
+// vector registers.
+typedef const __attribute__((address_space(1))) uint8_t* GlobalBytes;
+__device__ __forceinline__ GlobalBytes uniform(const uint8_t* p) {
+  GlobalBytes q = (GlobalBytes)p;
+  asm("" : "+s"(q));
+  return q;
+}
+
 // N bytes (2, 4, 8 or a multiple of 16) into words.  STREAM: past the caches, where
 // one instruction of the wave takes the whole of every line that it touches.
 template <bool STREAM, typename T>
-__device__ __forceinline__ T load_as(const uint8_t* p) {
-  if constexpr (STREAM) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
-  return *reinterpret_cast<const T*>(p);
+__device__ __forceinline__ T load_as(GlobalBytes p, uint32_t at) {
+  typedef const __attribute__((address_space(1))) T* Ptr;
+  asm("" : "+v"(at));          // 32 bits here, too: widened where it is made, it is no operand of the load
+  if constexpr (STREAM) return __builtin_nontemporal_load((Ptr)(p + at));
+  return *(Ptr)(p + at);
 }
 template <int N, bool STREAM>
 struct Raw {
   uint32_t w[N < 4 ? 1 : N / 4];
-  __device__ __forceinline__ void load(const uint8_t* p) {
+  __device__ __forceinline__ void load(GlobalBytes p, uint32_t at) {
     if constexpr (N == 2) {
-      w[0] = load_as<STREAM, uint16_t>(p);
+      w[0] = load_as<STREAM, uint16_t>(p, at);
     } else if constexpr (N == 4) {
-      w[0] = load_as<STREAM, uint32_t>(p);
+      w[0] = load_as<STREAM, uint32_t>(p, at);
     } else if constexpr (N == 8) {
-      const words2 v = load_as<STREAM, words2>(p);
+      const words2 v = load_as<STREAM, words2>(p, at);
       w[0] = v.x, w[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < N / 16; ++i) {
-        const words4 v = load_as<STREAM, words4>(p + 16 * i);
+        const words4 v = load_as<STREAM, words4>(p + 16 * i, at);
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
     }
@@ -162,13 +174,10 @@ struct Shape {
 // Where a half's codes and scales begin, and how many of its tokens there are: the
 // same for the whole wave, so a load is that address plus the lane's own offset.
 struct HalfPos {
-  int64_t code, scale;
-  int n;
+  uint64_t code, scale;
+  int n;                        // 16 or more: all; 0 or less: none
 };
 
-// One half (16 tokens) of a tile as a lane loads it: of K its part of token
-// 4 (c % 4) + c / 4, so that V's tokens are g, 4 + g, 8 + g and 12 + g, four
-// neighbouring rows to an instruction.
 template <int FMT, int D, bool STREAM>
 struct KHalf {
   using S = Shape<FMT, D>;
@@ -281,22 +290,22 @@ __global__ __launch_bounds__(64 * W, W == kWaves ? waves_per_simd(D) : 2) void k
   float top = -__builtin_inff(), total = 0.0f;
 
   const ConstInts table = (ConstInts)(a.table + request * a.table_stride);
-  const int mask = (1 << a.cache.page_shift) - 1;
+  const int mask = ((1 << a.cache.page_shift) - 1) & ~15;
   // (behind the last token: the 16 tokens with the last one, whose lines are near)
   auto page_at = [&](int t) { return table[min(t, end - 1) >> a.cache.page_shift]; };
-  auto half_at = [&](int t, int page) {
+  const uint32_t count = static_cast<uint32_t>(a.cache.pages), stride = static_cast<uint32_t>(a.cache.page);
+  const uint32_t s_stride = static_cast<uint32_t>(a.cache.s_page), token = static_cast<uint32_t>(a.cache.token);
+  const uint32_t block = static_cast<uint32_t>(a.cache.s_block);
+  auto half_at = [&](int t, int number) {
     HalfPos h;
-    const bool there = page >= 0 && page < a.cache.pages;     // else its tokens are masked
-    const int place = min(t, end - 1) & mask & ~15;
-    h.n = end - t > 16 ? 16 : end - t;
-    if (!there || h.n < 0) h.n = 0;
-    if (!there) page = 0;
-    h.code = page * a.cache.page + static_cast<int64_t>(place) * a.cache.token;
-    h.scale = page * a.cache.s_page + place;
+    const bool there = static_cast<uint32_t>(number) < count;       // else its tokens are masked
+    const uint32_t place = min(t, end - 1) & mask, page = there ? number : 0;
+    h.n = there ? end - t : 0;
+    h.code = static_cast<uint64_t>(page) * stride + place * token;
+    h.scale = static_cast<uint64_t>(page) * s_stride + place;
     return h;
   };
   // the lane's offsets (below 2^31: kv_api.cpp)
-  const uint32_t token = static_cast<uint32_t>(a.cache.token), block = static_cast<uint32_t>(a.cache.s_block);
   const uint8_t* const codes[2] = {a.cache.codes[0] + kv * a.cache.head, a.cache.codes[1] + kv * a.cache.head};
   const uint8_t* const scales[2] = {a.cache.scales[0] + kv * a.cache.s_head,
                                     a.cache.scales[1] + kv * a.cache.s_head};
@@ -305,14 +314,15 @@ __global__ __launch_bounds__(64 * W, W == kWaves ? waves_per_simd(D) : 2) void k
   const uint32_t v_code = g * token + c * S::kVBytes;
   const uint32_t v_scale = c * S::kElems / F::kBlock * block + c % S::kShare * (16 / S::kShare);
   auto load_k = [&](KHalf<FMT, D, STREAM>& k, const HalfPos& h) {
-    k.w.load(codes[0] + h.code + k_code);
+    k.w.load(uniform(codes[0] + h.code), k_code);
+    const GlobalBytes p = uniform(scales[0] + h.scale);
 #pragma unroll
-    for (int b = 0; b < S::kKBlocks; ++b) k.s[b] = (scales[0] + h.scale)[k_scale + b * block];
+    for (int b = 0; b < S::kKBlocks; ++b) k.s[b] = load_as<false, uint8_t>(p, k_scale + b * block);
   };
   auto load_v = [&](VHalf<FMT, D, STREAM>& v, const HalfPos& h) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v.w[j].load(codes[1] + h.code + (v_code + 4 * j * token));
-    v.s.load(scales[1] + h.scale + v_scale);
+    for (int j = 0; j < 4; ++j) v.w[j].load(uniform(codes[1] + h.code), v_code + 4 * j * token);
+    v.s.load(uniform(scales[1] + h.scale), v_scale);
   };
 
   // A tile's loads are issued while the tile before it is worked on: K's when its

@@ -131,6 +131,8 @@ fp4_status check_cache(const fp4_kv_cache* c) {
   for (int i = 0; i < 3; ++i)
     if (codes[i] <= 0 || codes[i] % 16 || scales[i] <= 0 || scales[i] % 16)
       return fail(FP4_ERR_ARG, "cache: strides must be positive multiples of 16");
+  if (codes[0] >= 2 * kMost || scales[0] >= 2 * kMost)
+    return fail(FP4_ERR_SHAPE, "cache: page strides must be below 2^32");
   // within a page the kernels' offsets are 32 bits wide
   if (codes[1] >= kMost || codes[2] >= kMost || scales[1] >= kMost || scales[2] >= kMost ||
       (c->heads - 1) * codes[1] + c->page_size * codes[2] >= kMost ||

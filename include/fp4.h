@@ -599,8 +599,8 @@ typedef struct {
   uint8_t* k_scales;
   uint8_t* v_codes;
   uint8_t* v_scales;
-  int64_t page_stride;      /* strides positive, of codes multiples of 16 (one page's */
-  int64_t head_stride;      /* and of its heads' offsets below 2^31) */
+  int64_t page_stride;      /* strides positive, of codes multiples of 16, below 2^32; */
+  int64_t head_stride;      /* offsets within a page below 2^31 */
   int64_t token_stride;
   int64_t scale_page_stride;   /* multiples of 16 */
   int64_t scale_head_stride;
