@@ -20,6 +20,7 @@ passes pointers (through `api`).
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import api
 from .linear import grad_alias, reach_hooks
@@ -39,6 +40,8 @@ def slots_of(page_table, positions, page_size):
     """int64 [n]: the slot of position positions[i] of request i (int64; its entry of
     the int32 [n, width] page table), -1 for a position that is negative or has no
     page."""
+    if page_table.shape[1] == 0:
+        return torch.full_like(positions, -1)
     page = positions // page_size
     there = (positions >= 0) & (page < page_table.shape[1])
     entry = page_table.gather(1, torch.where(there, page, 0).unsqueeze(1)).squeeze(1).long()
@@ -55,11 +58,13 @@ def _grad_heads(dy):
 
 
 class QKNormRope:
-    """q, k -> both normed and rotated (`api.QKNorm`), under autograd.
+    """q, k -> both normed and rotated (`api.QKNorm`), under autograd; either may be
+    None, and its result then is.
 
     As with the linears, the gradients of the weights are added to main_grad
     (float32 [2, head_dim]: q's, then k's; zero it between optimizer steps) and the weights
-    get no .grad; hooks on them run in the backward pass.  A step may be captured into
+    get no .grad; hooks on them run in the backward pass.  Weights changed in place
+    between the two passes are refused there, as is a gradient of the gradient.  A step may be captured into
     a graph; the captured q and k should be no leaves of an eager graph that is still
     alive (a leaf keeps its first stream).
     """
@@ -72,22 +77,29 @@ class QKNormRope:
                           torch.zeros((2, q_weight.shape[0]), dtype=torch.float32, device=q_weight.device))
 
     def __call__(self, q, k, positions=None):
+        n = self.norm
+        if self.weights and [w.data_ptr() for w in self.weights] != [n.q_weight.data_ptr(), n.k_weight.data_ptr()]:
+            # the weights' .data has been replaced
+            self.norm = api.QKNorm(*(w.detach() for w in self.weights), n.table, n.eps, n.style)
         return _QKNormRopeFunction.apply(q, k, positions, self, *(grad_alias(w) for w in self.weights))
 
 
 class _QKNormRopeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, layer, *aliases):
-        ctx.save_for_backward(q, k, positions)
-        ctx.layer, ctx.aliases = layer, aliases
+        ctx.save_for_backward(q, k, positions, *aliases)       # the weights for the check of their versions
+        ctx.layer, ctx.norm, ctx.aliases = layer, layer.norm, aliases
         return api.qk_norm_rope(layer.norm, q, k, positions)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         layer = ctx.layer
-        q, k, positions = ctx.saved_tensors
-        dq, dk, _, _ = api.qk_norm_rope_backward(layer.norm, q, k, positions, _grad_heads(dq), _grad_heads(dk),
-                                                 weight_grads=layer.main_grad)
+        q, k, positions, *_ = ctx.saved_tensors
+        dq, dk, _, _ = api.qk_norm_rope_backward(
+            ctx.norm, q, k, positions, None if q is None else _grad_heads(dq),
+            None if k is None else _grad_heads(dk),
+            weight_grads=False if layer.main_grad is None else layer.main_grad)
         for weight, alias in zip(layer.weights, ctx.aliases):
             reach_hooks(weight, alias)
         return dq, dk, None, None, *(None for _ in ctx.aliases)
@@ -143,4 +155,4 @@ class QuantizedAttention:
             # in place: the projection's rows are nobody else's
             q = api.kv_cache_write(cache, k, v, slots, q=q, norm=self.norm, positions=positions, q_out=q)
         o = api.attention_decode(q, cache, page_table, lens, self.scale)
-        return self._product(o.view(tokens, -1), self._out, self.out.shape[0])
+        return self._product(o.view(tokens, h * self.head_dim), self._out, self.out.shape[0])

@@ -230,12 +230,16 @@ __global__ __launch_bounds__(64 * W, W == kWaves ? waves_per_simd(D) : 2) void k
   const int c = lane & 15, g = lane >> 4;
   const int group = a.q.heads / a.cache.heads;               // query heads of a key head
   const int tiles = (group + kHeads - 1) / kHeads;
+  // Workgroups go round the 8 XCDs: those of one part (more than 16 query heads to a key
+  // head) are 8 apart, so that they find its codes in one L2 (64 requests of 4096 MXFP8
+  // tokens, 64 heads on one, 47.8 -> 35.9 us; 64 of 8000 in FP8, 32 heads of 256 on one, 86 -> 69).
   int id = blockIdx.x;
+  if (tiles > 1) id = id / (8 * tiles) * 8 + id % 8;
+  const int tile = tiles > 1 ? static_cast<int>(blockIdx.x) / 8 % tiles : 0;
   const int split = id % a.splits;
   id /= a.splits;
-  const int tile = id % tiles;
-  id /= tiles;
   const int kv = id % a.cache.heads, request = id / a.cache.heads;
+  if (request >= a.requests) return;
 
   const int len = tokens_of(a, request), per = part_tokens(len, a);
   const int begin = split * per, end = min(len, begin + per);

@@ -159,8 +159,9 @@ void plan(fp4lib::AttnArgs& a) {
   // More codes than half of the 256 MB last-level cache do not come from there again:
   // they are read past it (64 requests of up to 8192 MXFP8 tokens 122 -> 115 us, 32 of 6000
   // FP8 tokens, 197 MB, 45 -> 40; but 1 of 30000, 61 MB, 17.9 -> 19.1 when they are).
+  // More than 16 query heads to a key head: several workgroups read the same codes.
   const int row = a.cache.head_dim >> (a.cache.fmt != kKvFp8 && a.cache.fmt != kKvMx8);
-  a.stream = 2 * room * a.requests * a.cache.heads * row > (int64_t(128) << 20);
+  a.stream = tiles_of(a) == 1 && 2.0 * room * a.requests * a.cache.heads * row > 0x1p27;
   want = want > most ? most : want;
   // Short requests whole, eight waves each: one launch instead of two (1 of 200 / 500 / 1000
   // FP8 tokens 7.6 / 9.5 / 12.4 us instead of 8.9 / 8.8 / 9.4, and 8.3 / 10.0 / 12.8 instead of
@@ -192,12 +193,13 @@ int64_t attention_workspace(const AttnArgs& args) {
   return part_bytes(a);
 }
 
-hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
-  AttnArgs a = args;
-  plan(a);
-  if (!a.part || a.part_bytes < part_bytes(a)) a.splits = 1;
-  const int64_t grid = static_cast<int64_t>(a.requests) * a.cache.heads * tiles_of(a) * a.splits;
-  if (grid >= (int64_t(1) << 31)) return hipErrorInvalidConfiguration;
+namespace {
+
+// One launch's requests.
+hipError_t launch_some(const AttnArgs& a, hipStream_t s) {
+  const int tiles = tiles_of(a);
+  int64_t grid = static_cast<int64_t>(a.requests) * a.cache.heads * a.splits;
+  if (tiles > 1) grid = (grid + 7) / 8 * 8 * tiles;
   const hipError_t e = with_format(a.cache.fmt, [&](auto f) {
     return launch_attention_fmt<decltype(f)::value>(a, static_cast<uint32_t>(grid), s);
   });
@@ -212,6 +214,30 @@ hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
       hipLaunchKernelGGL(k_attention_join<D>, dim3(static_cast<uint32_t>(rows)), dim3(256), 0, s, a);
     return hipGetLastError();
   });
+}
+
+constexpr int64_t kMostGroups = int64_t(1) << 22;     // of a launch: a grid has fewer than 2^32 threads
+
+}  // namespace
+
+hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
+  AttnArgs a = args;
+  plan(a);
+  if (!a.part || a.part_bytes < part_bytes(a)) a.splits = 1;
+  const int64_t groups = static_cast<int64_t>(a.cache.heads) * tiles_of(a) * a.splits;
+  const int most = static_cast<int>(groups < kMostGroups ? kMostGroups / groups : 1);
+  const int64_t row = static_cast<int64_t>(a.q.heads) * a.cache.head_dim * (a.out_f32 ? 4 : 2);
+  for (int first = 0; first < args.requests; first += most) {
+    a.requests = args.requests - first < most ? args.requests - first : most;
+    a.q.x = args.q.x + first * args.q.token;
+    a.table = args.table + first * args.table_stride;
+    a.lens = args.lens + first;
+    a.out = static_cast<uint8_t*>(args.out) + first * row;
+    a.lse = args.lse ? args.lse + static_cast<int64_t>(first) * a.q.heads : nullptr;
+    const hipError_t e = launch_some(a, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp4lib

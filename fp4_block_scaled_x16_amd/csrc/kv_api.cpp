@@ -15,6 +15,8 @@ namespace {
 constexpr int64_t kMaxTokens = int64_t(1) << 31;
 constexpr int64_t kMaxHeads = 1024;
 
+bool aligned(const void* p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 bool head_dim_ok(int64_t d) { return d == 64 || d == 128 || d == 256; }
 
 fp4_status check_tokens(const char* what, int64_t n) {
@@ -71,6 +73,7 @@ fp4_status check_norm(const fp4_qk_norm* n, const int64_t* positions, int64_t to
       return fail(FP4_ERR_SHAPE, "rotary_dim=%d must be a multiple of 16 up to head_dim", n->rotary_dim);
     if (n->table_rows < 1) return fail(FP4_ERR_SHAPE, "table_rows=%lld must be positive", (long long)n->table_rows);
     if (tokens > 0 && !positions) return fail(FP4_ERR_ARG, "positions is null");
+    if (!aligned(positions, 8)) return fail(FP4_ERR_ARG, "positions must be aligned to their elements");
   }
   return FP4_OK;
 }
@@ -141,7 +144,8 @@ fp4_status check_cache(const fp4_kv_cache* c) {
   const int row = c->head_dim / (c->format == FP4_FP8_E4M3 || c->format == FP4_MXFP8 ? 1 : 2);
   if (codes[2] < row) return fail(FP4_ERR_ARG, "cache: token_stride=%lld below a row's %d bytes", (long long)codes[2], row);
   if (c->format == FP4_NVFP4 || c->format == FP4_UE5M3) {
-    if (!c->amax) return fail(FP4_ERR_ARG, "cache: amax is null");
+    if (!c->amax || !aligned(c->amax, 4))
+      return fail(FP4_ERR_ARG, "cache: amax must be non-null and aligned to its elements");
     if (!std::isfinite(c->target) || c->target <= 0) return fail(FP4_ERR_ARG, "cache: target must be finite and positive");
   }
   return FP4_OK;
@@ -234,7 +238,7 @@ FP4_EXPORT fp4_status fp4_qk_norm_rope_backward(const fp4_qk_norm* norm, const f
   }
   const bool sums = dq_weight || dk_weight;
   if (sums && !norm->q_weight) return fail(FP4_ERR_ARG, "a weight's gradient is asked for without a norm");
-  if (reinterpret_cast<uintptr_t>(dq_weight) % 4 || reinterpret_cast<uintptr_t>(dk_weight) % 4)
+  if (!aligned(dq_weight, 4) || !aligned(dk_weight, 4))
     return fail(FP4_ERR_ARG, "weight gradients must be aligned to their elements");
   if (sums && (!workspace || !aligned16(workspace)))
     return fail(FP4_ERR_ARG, "the workspace must be non-null and 16-byte aligned");
@@ -275,6 +279,7 @@ FP4_EXPORT fp4_status fp4_kv_cache_write(const fp4_kv_cache* cache, const fp4_he
     return fail(FP4_ERR_SHAPE, "k has %lld heads and v %lld, the cache %d", (long long)k->heads,
                 (long long)v->heads, cache->heads);
   if (tokens > 0 && !slots) return fail(FP4_ERR_ARG, "slots is null");
+  if (!aligned(slots, 8)) return fail(FP4_ERR_ARG, "slots must be aligned to their elements");
   if (norm) {
     st = check_norm(norm, positions, tokens, d);
     if (!st) st = check_pair("q", q, "q_out", q_out, tokens, d);
@@ -304,6 +309,7 @@ FP4_EXPORT fp4_status fp4_kv_cache_read(const fp4_kv_cache* cache, const int64_t
   if (st) return st;
   if (n == 0) return ok();
   if (!slots) return fail(FP4_ERR_ARG, "slots is null");
+  if (!aligned(slots, 8)) return fail(FP4_ERR_ARG, "slots must be aligned to their elements");
   if (!k && !v) return fail(FP4_ERR_ARG, "k and v are null");
   if (!aligned16(k) || !aligned16(v)) return fail(FP4_ERR_ARG, "outputs must be 16-byte aligned");
   fp4lib::KvReadArgs a{};
@@ -325,8 +331,8 @@ fp4_status check_attention(const fp4_kv_cache* cache, int64_t q_heads, int64_t r
   if (q_heads < 1 || q_heads > kMaxHeads || q_heads % cache->heads)
     return fail(FP4_ERR_SHAPE, "%lld query heads: a multiple of the cache's %d, up to %lld, is needed",
                 (long long)q_heads, cache->heads, (long long)kMaxHeads);
-  if (width < 0 || width * cache->page_size >= kMaxTokens - 1024)
-    return fail(FP4_ERR_SHAPE, "table_width=%lld: contexts are shorter than 2^31 - 1024", (long long)width);
+  if (width < 0 || width > kMaxTokens || width * cache->page_size >= kMaxTokens / 2)
+    return fail(FP4_ERR_SHAPE, "table_width=%lld: contexts are shorter than 2^30", (long long)width);
   // rows of the output, which the kernel that joins parts has a workgroup each for
   if (requests * q_heads >= kMaxTokens)
     return fail(FP4_ERR_SHAPE, "requests * heads must be below 2^31");
@@ -364,8 +370,7 @@ FP4_EXPORT fp4_status fp4_attention_decode(const fp4_kv_cache* cache, const fp4_
   if (requests == 0) return ok();
   if (table_width > 0 && !page_table) return fail(FP4_ERR_ARG, "page_table is null");
   if (!lens) return fail(FP4_ERR_ARG, "lens is null");
-  if (reinterpret_cast<uintptr_t>(page_table) % 4 || reinterpret_cast<uintptr_t>(lens) % 4 ||
-      reinterpret_cast<uintptr_t>(lse) % 4)
+  if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
     return fail(FP4_ERR_ARG, "page_table, lens and lse must be aligned to their elements");
   if (!out || !aligned16(out)) return fail(FP4_ERR_ARG, "out must be non-null and 16-byte aligned");
   if (workspace_bytes < 0 || (workspace && !aligned16(workspace)))

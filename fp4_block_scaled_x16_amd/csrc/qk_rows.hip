@@ -323,6 +323,23 @@ hipError_t launch_qk_rows(const QkRowsArgs& args, hipStream_t s) {
   };
   const bool many = a.tokens * parts(kManyRows) >= 8 * static_cast<int64_t>(device_cu_count());
   const int all = many ? a.part[3] : parts(1), waves = all < kRowWaves ? all : kRowWaves;
+  // a grid has fewer than 2^32 threads along x
+  constexpr int64_t kMostTokens = int64_t(1) << 22;
+  if (a.tokens > kMostTokens) {
+    for (int64_t first = 0; first < args.tokens; first += kMostTokens) {
+      a = args;
+      a.tokens = args.tokens - first < kMostTokens ? args.tokens - first : kMostTokens;
+      for (auto& h : a.in)
+        if (h.x) h.x += first * h.token;
+      for (auto& h : a.out)
+        if (h.x) h.x += first * h.token;
+      if (a.norm.positions) a.norm.positions += first;
+      if (a.slots) a.slots += first;
+      const hipError_t e = launch_qk_rows(a, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  }
   const dim3 grid(static_cast<uint32_t>(a.tokens), (all + waves - 1) / waves), block(64 * waves);
   return with_dim(a.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;

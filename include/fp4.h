@@ -645,7 +645,7 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache* cache /* host */, const int64_t
  *   page_table  device int32: token t of request r lies in page
  *            page_table[r * table_stride + t / page_size] (any stride, 0 too: a
  *            table shared by all), place t % page_size; table_width entries per
- *            request, of which those behind its length are not read.  Tokens of a
+ *            request (fewer than 2^30 tokens), of which those behind its length are not read.  Tokens of a
  *            page that the cache does not have are left out.
  *   lens     device int32[requests], the new token counted (it is written first).
  *            0 or less: no tokens.  More than the table has room for: that many.

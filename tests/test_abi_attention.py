@@ -266,3 +266,22 @@ def test_slots():
     t = torch.tensor([[4, 7, -1], [2, 0, 1]], dtype=torch.int32)
     s = lambda *p: attention.slots_of(t, torch.tensor(p), 16).tolist()        # noqa: E731
     assert s(0, 47) == [64, 31] and s(17, -1) == [113, -1] and s(32, 48) == [-1, -1]
+
+
+def test_index_arrays_are_aligned_to_their_elements(lib):
+    off = FAKE + 4
+    assert rope(lib, pos=off) == ARG and back(lib, pos=off) == ARG
+    assert write(lib, slots=off) == ARG and write(lib, n=norm(), pos=off) == ARG and read(lib, slots=off) == ARG
+    bad = cache(format=api.NVFP4, amax=FAKE + 2)
+    assert write(lib, c=bad) == ARG and read(lib, c=bad) == ARG and decode(lib, c=bad) == ARG
+
+
+def test_contexts_end_at_2_30(lib):
+    """Token numbers and what lies a few tiles behind them are 32 bits wide in the kernels."""
+    assert decode(lib, width=1 << 26) == SHAPE and decode(lib, width=1 << 62) == SHAPE
+    assert decode(lib, width=(1 << 26) - 1, n=0) == 0
+
+
+def test_slots_without_pages():
+    t = torch.empty((2, 0), dtype=torch.int32)
+    assert attention.slots_of(t, torch.tensor([0, 5]), 16).tolist() == [-1, -1]
