@@ -217,14 +217,14 @@ struct ScalePick {
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;
 
 template <int FMT, int D, int NP, bool STREAM, int W>
-__global__ __launch_bounds__(64 * W, W == kWaves ? waves_per_simd(D) : 2) void k_attention(fp4lib::AttnArgs a) {
+__global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) void k_attention(fp4lib::AttnArgs a) {
   using F = KvTraits<FMT>;
   using S = Shape<FMT, D>;
   constexpr bool kF16 = F::kTwoLevel;
   constexpr int kHeads = NP == 1 ? 8 : 16;                   // query heads of a workgroup
   // fp16 holds p down to 2^-24: its largest, 2^kSlack, is moved up by 2^7
   constexpr float kShift = kF16 ? 7.0f : 0.0f;
-  __shared__ float meet[W - 1][S::kElems * 4 + 2][64];
+  __shared__ float meet[W > 1 ? W - 1 : 1][S::kElems * 4 + 2][64];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -472,7 +472,7 @@ __global__ __launch_bounds__(64 * W, W == kWaves ? waves_per_simd(D) : 2) void k
     to[4 * S::kElems][lane] = top;
     to[4 * S::kElems + 1][lane] = total;
   }
-  __syncthreads();
+  if constexpr (W > 1) __syncthreads();
   if (wave) return;
   float all = top;
 #pragma unroll
@@ -553,17 +553,14 @@ hipError_t launch_attention_fmt<FP4_KV_FMT>(const AttnArgs& a, uint32_t grid, hi
                          dim3(64 * W), 0, s, a);
     };
     const bool few = a.q.heads / a.cache.heads <= 8;
-    if constexpr (D <= kWideDim) {
-      if (a.wide) {
-        if (few) launch(Const<1>(), Const<0>(), Const<kWideWaves>());
-        else launch(Const<2>(), Const<0>(), Const<kWideWaves>());
-        return hipGetLastError();
-      }
-    }
-    if (few && a.stream) launch(Const<1>(), Const<1>(), Const<kWaves>());
-    else if (few) launch(Const<1>(), Const<0>(), Const<kWaves>());
-    else if (a.stream) launch(Const<2>(), Const<1>(), Const<kWaves>());
-    else launch(Const<2>(), Const<0>(), Const<kWaves>());
+    auto by_heads = [&](auto stream, auto waves) {
+      if (few) launch(Const<1>(), stream, waves);
+      else launch(Const<2>(), stream, waves);
+    };
+    if (a.waves == 1) by_heads(Const<0>(), Const<1>());
+    else if (D <= kWideDim && a.waves == kWideWaves) by_heads(Const<0>(), Const<(D <= kWideDim ? kWideWaves : kWaves)>());
+    else if (a.stream) by_heads(Const<1>(), Const<kWaves>());
+    else by_heads(Const<0>(), Const<kWaves>());
     return hipGetLastError();
   });
 }

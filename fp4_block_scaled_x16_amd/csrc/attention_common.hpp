@@ -8,6 +8,7 @@ namespace fp4attn {
 
 constexpr int kWaves = 4, kTile = 32;
 constexpr int kWideWaves = 8, kWideDim = 128; // of a workgroup that has a short request alone, heads up to 128
+constexpr int kLoneTokens = 384;              // many requests of up to as many: one wave each
 constexpr int kMaxParts = 512;
 constexpr int kStep = kWaves * kTile;         // tokens that a workgroup takes at once
 

@@ -167,10 +167,20 @@ void plan(fp4lib::AttnArgs& a) {
   // FP8 tokens 7.6 / 9.5 / 12.4 us instead of 8.9 / 8.8 / 9.4, and 8.3 / 10.0 / 12.8 instead of
   // 11.6 / 11.7 / 11.8 a call where the host's part counts; heads of 64, MXFP4: 5.5 / 6.5 / 8.4
   // instead of 7.3 / 7.3 / 7.9, and 8.2 / 8.1 / 9.1 instead of 12).
+  // Many of them, a wave each: no meeting at the end (8 heads of 128: 2000 of up to 64 FP8 tokens with
+  // 4 / 2 / 1 waves 98 / 59 / 50 us, 2000 of up to 256 MXFP4 tokens 117 / 83 / 75, 128 of up to 200 MXFP8
+  // tokens 14.4 / - / 11.7; but 256 of up to 512 MXFP4 tokens of 4 heads of 64 11.8 / - / 15.1, and
+  // 512 of up to 1024 MXFP4 tokens 66 / 69 / 78).
   const int steps = a.cache.head_dim == 64 ? 4 : 2;
-  if (a.cache.head_dim <= kWideDim && want > 1 && room <= steps * kWideWaves * kTile && !g_splits.load()) {
-    a.wide = 1;
-    want = 1;
+  a.waves = kWaves;
+  if (!g_splits.load()) {
+    if (4 * room <= each && room <= kLoneTokens) {
+      a.waves = 1;
+      want = 1;
+    } else if (a.cache.head_dim <= kWideDim && want > 1 && room <= steps * kWideWaves * kTile) {
+      a.waves = kWideWaves;
+      want = 1;
+    }
   }
   a.splits = static_cast<int>(want < 1 ? 1 : want > kMaxParts ? kMaxParts : want);
 }

@@ -89,7 +89,7 @@ struct AttnArgs {
   float* part;                 // workspace: null with splits == 1
   int64_t part_bytes;
   int splits, min_part;        // set by the launcher
-  int wide;                    // set by the launcher: kWideWaves waves in a workgroup
+  int waves;                   // set by the launcher: of a workgroup
   int stream;                  // set by the launcher: codes are read past the caches
 };
 

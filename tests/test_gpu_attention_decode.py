@@ -294,3 +294,20 @@ def test_parts_of_a_context_join_by_their_lse():
     # that of both logs, times |a - b|
     rel = 2 * (2 * (d + 2) + 8) * U * size + 2.0 ** -16 + 2 * (120 + 64) * U
     assert torch.allclose(w * a + (1 - w) * b, whole, rtol=0, atol=5 * rel * np.abs(vv).max())
+
+
+@pytest.mark.parametrize("group,requests,heads,page,width", [(5, 70, 4, 16, 4), (12, 130, 2, 32, 2), (1, 1600, 1, 128, 3)])
+@pytest.mark.parametrize("d", DIMS)
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_short_requests(fmt, d, group, requests, heads, page, width):
+    """One wave to a request: lengths from none to all that the table has room for."""
+    pages = 768 // page
+    cache = filled(fmt, pages, page, heads, d)
+    pool = C.contents(cache)
+    lens = [(37 * i) % (page * width + 1) for i in range(requests)]
+    table = tables(lens, page, pages, width, 3)
+    q = query(requests, heads * group, d, 4)
+    out, lse = api.attention_decode(q.to(DEV), cache, torch.from_numpy(table).to(DEV),
+                                    torch.tensor(lens, dtype=torch.int32, device=DEV), return_lse=True)
+    sel = list(range(0, requests, max(1, requests // 24)))
+    check(out[sel], lse[sel], q[sel], cache, pool, table[sel], [lens[i] for i in sel], d ** -0.5)
