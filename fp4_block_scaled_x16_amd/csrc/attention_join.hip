@@ -1,5 +1,6 @@
 // Launch of the attention of one new token per request (attention.hip): how many
 // parts a request's tokens are shared among, and the kernel that joins them.
+#include <algorithm>
 #include <atomic>
 
 #include "attention_common.hpp"
@@ -137,20 +138,24 @@ int tiles_of(const fp4lib::AttnArgs& a) {
 // Parts per request and the least tokens of one, from what the page table has room
 // for (the lengths are on the device; a shorter request is shared among as many).
 // Two workgroups on every CU, if that leaves a part 1024 tokens (each starts with
-// three loads that wait for one another, and ends with a join), else one: 4 requests
-// of 120000 NVFP4 tokens in 8 / 16 / 24 / 64 parts 126 / 109 / 112 / 116 us, 1 of 30000 FP8
-// tokens in 32 / 64 / 128 parts 17.4 / 19.2 / 22.  Where requests alone fill the chip,
-// two parts of over 2048 tokens even out their lengths: 64 of up to 8192 in 1 / 2 / 8
-// parts 124 / 120 / 122 us, 256 of up to 1024 in 1 / 2 parts 15.4 / 21.6.
+// three loads that wait for one another, and ends with a join), else as many as there
+// are CUs, but not more: 4 requests of 120000 NVFP4 tokens in 8 / 16 / 24 / 64 parts
+// 126 / 109 / 112 / 116 us, 1 of 30000 FP8 tokens in 32 / 64 / 128 parts 17.4 / 19.2 / 22, 6 of
+// 3084 MXFP8 tokens of 8 heads in 4 / 5 / 6 / 8 parts 16.0 / 15.2 / 18.9 / 18.2, 72 of 551 of 2
+// heads in 1 / 2 parts 11.1 / 15.6.  Where requests alone fill the chip, two parts of
+// over 2048 tokens even out their lengths (64 of up to 8192 in 1 / 2 / 8 parts 124 / 120 /
+// 122 us, 256 of up to 1024 in 1 / 2 parts 15.4 / 21.6), and more of over 4096, up to eight
+// times what fills it (20 of up to 21080 NVFP4 tokens of 16 heads of 64 in 2 / 4 / 6 parts
+// 111 / 76 / 75.5).
 void plan(fp4lib::AttnArgs& a) {
   const int64_t room = static_cast<int64_t>(a.table_width) << a.cache.page_shift, cu = fp4lib::device_cu_count();
   const int64_t each = static_cast<int64_t>(a.requests) * a.cache.heads * tiles_of(a);
   const int64_t slots = 2 * cu;
   const int64_t most = (room + kStep - 1) / kStep, full = slots / each > 1 ? slots / each : 1;
   int64_t want = full;
-  if (room < 1024 * full) want = (cu + each - 1) / each;
-  const int64_t even = (room + 2047) / 2048;
-  if (want < even) want = even < 2 * full ? even : 2 * full;
+  if (room < 1024 * full) want = cu / each;
+  auto parts_of = [&](int64_t tokens, int64_t cap) { return std::min((room + tokens - 1) / tokens, cap); };
+  want = std::max({want, parts_of(2048, 2 * full), parts_of(4096, 8 * full)});
   a.min_part = 2 * each >= slots ? 4 * kStep : kStep;
   if (const int forced = g_splits.load()) {
     want = forced;
