@@ -2,8 +2,9 @@
 // qk_rows.hip.)
 //
 // Bound by memory, mostly by what it writes: 1 (0.5) bytes in and 2 out per
-// element.  A thread takes 8 elements of K and the same 8 of V: 16-byte stores,
-// a wave 1 KiB of the output.
+// element (32768 NVFP4 slots of 8 heads of 128 in 31 us, 172 MB at 5.5 TB/s; 1000 MXFP4
+// slots of 4 heads of 256 in 3.1, a launch's time).  A thread takes 8 elements of K and the same
+// 8 of V: 16-byte stores, a wave 1 KiB of the output.
 #include "kv_common.hpp"
 
 using namespace kvdev;

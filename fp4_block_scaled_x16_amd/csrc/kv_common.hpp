@@ -12,6 +12,12 @@
 
 namespace kvdev {
 
+// A constant as an argument.
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+
 using fp4lib::kKvFp8;
 using fp4lib::kKvMx4;
 using fp4lib::kKvMx8;
@@ -50,6 +56,21 @@ __device__ __forceinline__ float lane_sum(float v) {
   if constexpr (N > 2) v = add(v, dpp<kXor2>(__float_as_uint(v)));
   if constexpr (N > 4) v = add(v, dpp<kHalfMirror>(__float_as_uint(v)));
   if constexpr (N > 8) v = add(v, dpp<kMirror>(__float_as_uint(v)));
+  if constexpr (N > 16) v += __shfl_xor(v, 16, 64);
+  return v;
+}
+template <int N>
+__device__ __forceinline__ double lane_sum(double v) {
+  auto moved = [&](auto ctrl) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    constexpr int kCtrl = decltype(ctrl)::value;
+    return __builtin_bit_cast(double, static_cast<uint64_t>(dpp<kCtrl>(static_cast<uint32_t>(b >> 32))) << 32 |
+                                          dpp<kCtrl>(static_cast<uint32_t>(b)));
+  };
+  if constexpr (N > 1) v += moved(Const<kXor1>());
+  if constexpr (N > 2) v += moved(Const<kXor2>());
+  if constexpr (N > 4) v += moved(Const<kHalfMirror>());
+  if constexpr (N > 8) v += moved(Const<kMirror>());
   if constexpr (N > 16) v += __shfl_xor(v, 16, 64);
   return v;
 }
@@ -161,10 +182,6 @@ struct Coded {
 };
 
 // Calls f with the format and head dimension as constants.
-template <int V>
-struct Const {
-  static constexpr int value = V;
-};
 template <typename F>
 hipError_t with_dim(int head_dim, F&& f) {
   return head_dim == 64 ? f(Const<64>()) : head_dim == 128 ? f(Const<128>()) : f(Const<256>());

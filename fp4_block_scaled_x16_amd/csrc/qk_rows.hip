@@ -6,11 +6,16 @@
 //   R turns the pair (a, b) of angle t into (a cos t - b sin t, b cos t + a sin t)
 //   dz = R^T dy;  dw = sum dz x r;  g = dz w;  dx = r (g - x r^2 mean(g x))
 //
-// Bound by memory: 2 bytes in and 2 out per element (backward 4 in).  A row
-// lies in D / 8 lanes, 16 bytes each.  A rotated pair's other half ("half"
-// style: D / 2 lanes' distance or less) is not exchanged between lanes but
-// loaded a second time, from the line that is in flight already.  A wave stays
-// with one token, whose angles it holds in registers for all of its heads.
+// Bound by memory: 2 bytes in and 2 out per element (backward 4 in, 2 out).  8192 tokens
+// of 32 + 8 heads of 128 take 34.4 us, 4.9 TB/s, where a large copy reaches 5.0 to 5.2;
+// backward 53 us, 4.8 TB/s; 8192 tokens normed, turned and written to an MXFP8 cache 41.5 us,
+// 4.6 TB/s; 64 of them to an FP8 cache 3.9 us, of which a launch is 3.
+//
+// A row lies in D / 8 lanes, 16 bytes each.  A rotated pair's other half ("half"
+// style: D / 2 lanes' distance or less) is not exchanged between lanes but loaded a
+// second time, from the line that is in flight already.  Forward, a workgroup has
+// one token (up to 512 / 64 waves of its rows), whose angles a wave holds for all of
+// its heads; backward, a wave has a run of consecutive rows.
 #include "kv_common.hpp"
 
 using namespace kvdev;
@@ -20,6 +25,8 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kManyRows = 4;
 constexpr int kRowWaves = 8;      // of a workgroup of the forward pass, at most
+// Rows of k or v that go into a cache, where q has r: 64-bit sums take registers.
+constexpr int coded_rows_of(int r) { return r > 1 ? 2 : 1; }
 
 // "half" style: element from which the partners of the lane's elements d0 .. lie;
 // -1 where they are neighbours, or not turned.
@@ -115,9 +122,92 @@ __device__ __forceinline__ float inv_rms(const float (&v)[8], float eps) {
   return __builtin_amdgcn_rsqf(lane_sum<D / 8>(q) * (1.0f / D) + eps);      // within an ulp
 }
 
-// A wave has R times 64 / (D / 8) rows of one token, all of q, of k or of v
-// (a.part[kind] is the first wave of the kind), whose loads it issues before
-// anything else; a workgroup has neighbouring rows of a token.
+// The same in 64 bits, in which the squares of bf16 elements are exact.
+template <int D>
+__device__ __forceinline__ double inv_rms64(const float (&v)[8], float eps) {
+  double q = 0.0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q = __builtin_fma(static_cast<double>(v[i]), static_cast<double>(v[i]), q);
+  const double a = lane_sum<D / 8>(q) * (1.0 / D) + eps, r = __builtin_amdgcn_rsq(a);
+  const double off = __builtin_fma(-a * r, r, 1.0);
+  return __builtin_fabs(off) < 0.5 ? __builtin_fma(0.5 * r, off, r) : r;       // (0 and infinity as they are)
+}
+
+// To fp32 such that a second rounding, to fewer bits, gives what one from z gives: what
+// is cut off leaves a mark in the last bit.
+__device__ __forceinline__ float to_odd(double z) {
+  const float f = static_cast<float>(z);
+  const double back = f;
+  uint32_t b = __float_as_uint(f);
+  if (__builtin_fabs(back) > __builtin_fabs(z)) b -= 1;       // (of the magnitude)
+  return __uint_as_float(back == z || z != z ? b : b | 1u);
+}
+
+// Rows of k or v into their slot: from head0 on, every kRows-th.
+//
+// What a norm or a rotation gives is formed in 64 bits and encoded with one rounding:
+// in fp32 a value next to a border between two codes would now and then fall on its
+// other side, 6 or 12 % away (12 of 8 million elements, as many as in elementary fp32 operations;
+// 8192 tokens to an MXFP8 cache took 40.7 us, and 64 to an FP8 one 3.4).
+template <int D, int FMT, int R>
+__device__ __forceinline__ void coded_rows(const fp4lib::QkRowsArgs& a, int kind, int64_t token, int head0, int lane) {
+  constexpr int kLanes = D / 8, kRows = 64 / kLanes;
+  const fp4lib::HeadsArgs& in = a.in[kind];
+  const int d0 = lane % kLanes * 8;
+  const int partner = kind == 1 ? partner_of(a.norm, d0) : -1;
+  RawRow raw[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int head = head0 + i * kRows < in.heads ? head0 + i * kRows : 0;
+    raw[i].load(in.x + token * in.token + static_cast<int64_t>(head) * in.head, d0, partner);
+  }
+  const int64_t slot = a.slots[token], page = slot >> a.cache.page_shift;
+  const int place = static_cast<int>(slot & ((1 << a.cache.page_shift) - 1));
+  if (slot < 0 || page >= a.cache.pages) return;
+  float s_enc = 1.0f, s_dec = 1.0f;
+  tensor_scales<FMT>(a.cache, kind - 1, s_enc, s_dec);
+  const bool norm = a.norm.w[1] != nullptr, turned = a.norm.table && d0 < 2 * a.norm.pairs;
+  if (kind == 1 && (norm || a.norm.table)) {
+    // y = r (x wc + xp ws): w c, and the partner's w s (products of two fp32 numbers: exact)
+    double wc[8], ws[8];
+    {
+      const Turn t = turn_of(a.norm, token, d0, partner);
+      float w[8];
+      weights(w, a.norm, 1, d0);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wc[e] = static_cast<double>(w[e]) * t.c[e];
+      if (partner >= 0) weights(w, a.norm, 1, partner);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ws[e] = static_cast<double>(w[partner >= 0 ? e : e ^ 1]) * t.s[e];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float v[8], vp[8];
+      raw[i].values(v, vp, partner);
+      const double r = norm ? inv_rms64<D>(v, a.norm.eps) : 1.0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        double z = v[e] * wc[e];
+        if (turned) z = __builtin_fma(static_cast<double>(vp[e]), ws[e], z);
+        v[e] = to_odd(z * r);
+      }
+      if (head0 + i * kRows < in.heads)          // a row's lanes together
+        encode_row<FMT, D>(v, lane % kLanes, a.cache, 0, page, place, head0 + i * kRows, s_enc, s_dec);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    float v[8];
+    fp4quant::unpack8(raw[i].v, v);
+    if (head0 + i * kRows < in.heads)
+      encode_row<FMT, D>(v, lane % kLanes, a.cache, kind - 1, page, place, head0 + i * kRows, s_enc, s_dec);
+  }
+}
+
+// A wave has R times (k and v for a cache: coded_rows_of(R) times) 64 / (D / 8) rows of one
+// token, all of q, of k or of v (a.part[kind] is the first wave of the kind), whose
+// loads it issues before anything else; a workgroup has neighbouring rows of a token.
 template <int D, int FMT, int R>
 __global__ __launch_bounds__(64 * kRowWaves) void k_qk_rows(fp4lib::QkRowsArgs a) {
   constexpr int kLanes = D / 8, kRows = 64 / kLanes;
@@ -126,68 +216,52 @@ __global__ __launch_bounds__(64 * kRowWaves) void k_qk_rows(fp4lib::QkRowsArgs a
   const int part = blockIdx.y * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (part >= a.part[3]) return;
   const int kind = part < a.part[1] ? 0 : part < a.part[2] ? 1 : 2;
+  if constexpr (FMT >= 0) {
+    if (kind > 0) {
+      coded_rows<D, FMT, coded_rows_of(R)>(a, kind, token,
+                                           (part - a.part[kind]) * (coded_rows_of(R) * kRows) + lane / kLanes, lane);
+      return;
+    }
+  }
   const fp4lib::HeadsArgs& in = a.in[kind];
   const int d0 = lane % kLanes * 8, head0 = (part - a.part[kind]) * (R * kRows) + lane / kLanes;
-  const int partner = kind < 2 ? partner_of(a.norm, d0) : -1;
+  const int partner = partner_of(a.norm, d0);
   RawRow raw[R];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int head = head0 + i * kRows < in.heads ? head0 + i * kRows : 0;
     raw[i].load(in.x + token * in.token + static_cast<int64_t>(head) * in.head, d0, partner);
   }
-
-  // where k and v go
-  int64_t page = 0;
-  int place = 0;
-  float s_enc = 1.0f, s_dec = 1.0f;
-  if (FMT >= 0 && kind > 0) {
-    const int64_t slot = a.slots[token];
-    page = slot >> a.cache.page_shift;
-    place = static_cast<int>(slot & ((1 << a.cache.page_shift) - 1));
-    if (slot < 0 || page >= a.cache.pages) return;
-    tensor_scales<FMT>(a.cache, kind - 1, s_enc, s_dec);
-  }
   // y = r (x wc + xp ws): w c, and the partner's w s
   float wc[8], ws[8];
-  if (kind < 2) {
-    const Turn t = turn_of(a.norm, token, d0, partner);
-    weights(wc, a.norm, kind, d0);
-    if (partner >= 0) {
-      weights(ws, a.norm, kind, partner);
-    } else {
+  const Turn t = turn_of(a.norm, token, d0, partner);
+  weights(wc, a.norm, kind, d0);
+  if (partner >= 0) {
+    weights(ws, a.norm, kind, partner);
+  } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ws[i] = wc[i ^ 1];
-    }
+    for (int i = 0; i < 8; ++i) ws[i] = wc[i ^ 1];
+  }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      wc[i] *= t.c[i];
-      ws[i] *= t.s[i];
-    }
+  for (int i = 0; i < 8; ++i) {
+    wc[i] *= t.c[i];
+    ws[i] *= t.s[i];
   }
   const bool norm = a.norm.w[0] != nullptr, turned = a.norm.table && d0 < 2 * a.norm.pairs;
+  const fp4lib::HeadsArgs& out = a.out[kind];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int head = head0 + i * kRows;
     float v[8], vp[8];
     raw[i].values(v, vp, partner);
-    if (kind < 2) {
-      const float r = norm ? inv_rms<D>(v, a.norm.eps) : 1.0f;
+    const float r = norm ? inv_rms<D>(v, a.norm.eps) : 1.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float y = v[e] * wc[e];
-        if (turned) y = __builtin_fmaf(vp[e], ws[e], y);
-        v[e] = y * r;
-      }
+    for (int e = 0; e < 8; ++e) {
+      float y = v[e] * wc[e];
+      if (turned) y = __builtin_fmaf(vp[e], ws[e], y);
+      v[e] = y * r;
     }
-    if (head >= in.heads) continue;          // a row's lanes together
-    if constexpr (FMT >= 0) {
-      if (kind > 0) {
-        encode_row<FMT < 0 ? 0 : FMT, D>(v, lane % kLanes, a.cache, kind - 1, page, place, head, s_enc, s_dec);
-        continue;
-      }
-    }
-    const fp4lib::HeadsArgs& out = a.out[kind];
-    store8(out.x + token * out.token + head * out.head + d0, v);
+    if (head < in.heads) store8(out.x + token * out.token + head * out.head + d0, v);      // a row's lanes together
   }
 }
 
@@ -317,8 +391,10 @@ namespace fp4lib {
 hipError_t launch_qk_rows(const QkRowsArgs& args, hipStream_t s) {
   QkRowsArgs a = args;
   auto parts = [&](int r) {
-    const int rows = r * 512 / a.head_dim;       // of a wave
-    for (int i = 0; i < 3; ++i) a.part[i + 1] = a.part[i] + (a.in[i].x ? (a.in[i].heads + rows - 1) / rows : 0);
+    for (int i = 0; i < 3; ++i) {
+      const int rows = (a.cached && i > 0 ? coded_rows_of(r) : r) * 512 / a.head_dim;       // of a wave
+      a.part[i + 1] = a.part[i] + (a.in[i].x ? (a.in[i].heads + rows - 1) / rows : 0);
+    }
     return a.part[3];
   };
   const bool many = a.tokens * parts(kManyRows) >= 8 * static_cast<int64_t>(device_cu_count());

@@ -616,7 +616,7 @@ typedef struct {
  *   slots   device int64[tokens].  A token whose slot is negative or behind the
  *           last page is not written.  The others' slots are distinct: where two
  *           tokens name one slot, it may end with bytes of either.
- *   norm    NULL, or what k goes through first (in fp32, encoded from there with
+ *   norm    NULL, or what k goes through first (in 64 bits, encoded from there with
  *           one rounding), in the same pass; with it q, which comes out as
  *           q_out in bf16 (both NULL: k alone), and positions (all as in
  *           fp4_qk_norm_rope; q is turned whatever the slot).

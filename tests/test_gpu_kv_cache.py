@@ -236,3 +236,31 @@ def test_graph_and_stream():
         wk, wv = api.kv_cache_read(eager, slots)
         torch.cuda.synchronize()
         assert torch.equal(q, want) and torch.equal(k, wk) and torch.equal(v, wv)
+
+
+@pytest.mark.parametrize("style,rot", [("half", 128), ("interleaved", 64)])
+@pytest.mark.parametrize("fmt", ["fp8", "mxfp8", "mxfp4"])
+def test_codes_are_those_of_the_exact_values(fmt, style, rot):
+    """Of 250000 elements as many as lie next to a border between two codes: within what 64 bits
+    leave (2^-50 of a value, of which a border is nearer with a chance of 1e-9 in all)."""
+    d, heads, tokens, page, eps = 128, 4, 500, 16, np.float32(1e-6)
+    cache = C.make_cache(fmt, 32, page, heads, d)
+    k = C.rows((tokens, heads, d), 5).to(DEV)
+    w = [1 + 0.3 * torch.randn(d, generator=torch.Generator().manual_seed(i)).to(DEV) for i in range(2)]
+    tab = torch.from_numpy(C.table(tokens, rot)).to(DEV)
+    pos = slots = torch.arange(tokens, device=DEV)
+    api.kv_cache_write(cache, k, k, slots, norm=api.QKNorm(*w, tab, eps=float(eps), style=style), positions=pos)
+    t = C.as64(tab)[:, None]
+    y = A.norm_rope(C.as64(k), C.as64(w[1]), t[..., :rot // 2], t[..., rot // 2:], float(eps), style == "interleaved")
+    s = np.arange(tokens)
+    codes, scales, *_ = C.contents(cache)
+    n = tokens * heads
+    got = A.row_values(codes[s // page, :, s % page].reshape(n, -1), scales[s // page, :, :, s % page].reshape(n, -1), fmt, d)
+    top, low, m = (448.0, -6, 3) if fmt != "mxfp4" else (6.0, 0, 1)
+    b = y.reshape(n, -1, A.BLOCK[fmt])
+    big = np.maximum(np.abs(b).max(2), 2.0 ** -110)
+    by = np.exp2(np.ceil(np.log2(big / top)))
+    by = np.where(big > top * by, 2 * by, np.where(big <= top * by / 2, by / 2, by))[..., None]
+    z = b / by
+    step = np.exp2(np.maximum(np.floor(np.log2(np.maximum(np.abs(z), 2.0 ** -200))), low) - m)
+    assert np.array_equal(got, (np.rint(z / step) * step * by).reshape(n, d))
