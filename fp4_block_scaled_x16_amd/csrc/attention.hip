@@ -223,6 +223,57 @@ struct ScalePick {
   }
 };
 
+// The nth request from the longest on (of up to kOrdered, in 16 classes of lengths; in each
+// by number): where more workgroups wait than the chip holds, those that come last
+// should have least to do.
+struct Nth {
+  int request, len;
+};
+__device__ __forceinline__ Nth nth_longest(const fp4lib::AttnArgs& a, int nth, int lane) {
+  constexpr int kChunks = kOrdered / 64, kClasses = 16;
+  int len[kChunks], cls[kChunks];
+  uint32_t most = 0;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) len[k] = tokens_of(a, min(64 * k + lane, a.requests - 1));
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) most = fp8dev::umax(most, len[k]);
+  most = lane_max<16>(most);
+  uint32_t top = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) top = fp8dev::umax(top, __builtin_amdgcn_readlane(most, 16 * k));
+  const float by = kClasses * __builtin_amdgcn_rcpf(static_cast<float>(top) + 1.0f);
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k)
+    cls[k] = 64 * k + lane < a.requests ? min(static_cast<int>(static_cast<float>(len[k]) * by), kClasses - 1) : -1;
+  // the class: the highest with more than nth requests in it and above; `above` it
+  int c = 0, above = 0;
+#pragma unroll
+  for (int bit = kClasses / 2; bit; bit /= 2) {
+    int count = 0;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+      if (64 * k < a.requests) count += __popcll(__ballot(cls[k] >= c + bit));
+    if (count > nth) c += bit;
+    else above = count;
+  }
+  nth -= above;
+  Nth found{0, 0};
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    if (64 * k >= a.requests) break;
+    const uint64_t in = __ballot(cls[k] == c);
+    const int count = __popcll(in);
+    if (nth >= 0 && nth < count) {
+      const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(in >> 32),
+                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(in), 0));
+      const int at = __ffsll(static_cast<unsigned long long>(__ballot(cls[k] == c && before == nth))) - 1;
+      found = {64 * k + at, __builtin_amdgcn_readlane(len[k], at)};
+    }
+    nth -= count;
+  }
+  return {__builtin_amdgcn_readfirstlane(found.request), __builtin_amdgcn_readfirstlane(found.len)};
+}
+
 // Read through the scalar cache (the kernel does not write the page table), whose
 // waits are apart from the vector loads'.
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;
@@ -239,20 +290,26 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int group = a.q.heads / a.cache.heads;               // query heads of a key head
-  const int tiles = (group + kHeads - 1) / kHeads;
+  const int group = a.group, tiles = a.tiles;
   // Workgroups go round the 8 XCDs: those of one part (more than 16 query heads to a key
   // head) are 8 apart, so that they find its codes in one L2 (64 requests of 4096 MXFP8
   // tokens, 64 heads on one, 47.8 -> 35.9 us; 64 of 8000 in FP8, 32 heads of 256 on one, 86 -> 69).
-  int id = blockIdx.x;
-  if (tiles > 1) id = id / (8 * tiles) * 8 + id % 8;
-  const int tile = tiles > 1 ? static_cast<int>(blockIdx.x) / 8 % tiles : 0;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int kv = id % a.cache.heads, request = id / a.cache.heads;
-  if (request >= a.requests) return;
-
-  const int len = tokens_of(a, request), per = part_tokens(len, a);
+  uint32_t id = blockIdx.x;
+  int tile = 0;
+  if (tiles > 1) {
+    const uint32_t eight = id / 8, part = eight / tiles;
+    tile = eight - part * tiles;
+    id = 8 * part + id % 8;
+  }
+  // (the quotients are exact: id < 2^32 / 1024)
+  const uint32_t part = a.splits > 1 ? __umulhi(id, a.by_splits) : id;
+  const int split = id - part * a.splits;
+  id = a.cache.heads > 1 ? __umulhi(part, a.by_heads) : part;
+  const int kv = part - id * a.cache.heads;
+  if (id >= static_cast<uint32_t>(a.requests)) return;
+  const Nth nth = W == kWaves && a.longest_first ? nth_longest(a, id, lane)
+                                                      : Nth{static_cast<int>(id), tokens_of(a, id)};
+  const int request = nth.request, len = nth.len, per = part_tokens(len, a);
   const int begin = split * per, end = min(len, begin + per);
   const int first = kv * group + tile * kHeads, heads = min(kHeads, group - tile * kHeads);
   if (begin >= end && split > 0) return;

@@ -31,6 +31,9 @@ __device__ __forceinline__ int tokens_of(const fp4lib::AttnArgs& a, int request)
   return len < 0 ? 0 : len > room ? static_cast<int>(room) : len;
 }
 
+// Requests of which the longest may come first (a wave looks at 64 lengths at once).
+constexpr int kOrdered = 256;
+
 // The workspace: the parts' sums [row][part][head_dim], and behind them each one's
 // maximum (in powers of two) and sum of p, [row][part].
 __device__ __forceinline__ float2* part_sums(const fp4lib::AttnArgs& a) {

@@ -134,11 +134,6 @@ __global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
 
 std::atomic<int> g_splits{0};
 
-int tiles_of(const fp4lib::AttnArgs& a) {
-  const int group = a.q.heads / a.cache.heads, heads = group <= 8 ? 8 : 16;
-  return (group + heads - 1) / heads;
-}
-
 // Parts per request and the least tokens of one, from what the page table has room
 // for (the lengths are on the device; a shorter request is shared among as many).
 // Two workgroups on every CU, if that leaves a part 1024 tokens (each starts with
@@ -153,7 +148,9 @@ int tiles_of(const fp4lib::AttnArgs& a) {
 // 111 / 76 / 75.5).
 void plan(fp4lib::AttnArgs& a) {
   const int64_t room = static_cast<int64_t>(a.table_width) << a.cache.page_shift, cu = fp4lib::device_cu_count();
-  const int64_t each = static_cast<int64_t>(a.requests) * a.cache.heads * tiles_of(a);
+  a.group = a.q.heads / a.cache.heads;
+  a.tiles = a.group <= 8 ? 1 : (a.group + 15) / 16;
+  const int64_t each = static_cast<int64_t>(a.requests) * a.cache.heads * a.tiles;
   const int64_t slots = 2 * cu;
   const int64_t most = (room + kStep - 1) / kStep, full = slots / each > 1 ? slots / each : 1;
   int64_t want = full;
@@ -170,7 +167,7 @@ void plan(fp4lib::AttnArgs& a) {
   // FP8 tokens, 197 MB, 45 -> 40; but 1 of 30000, 61 MB, 17.9 -> 19.1 when they are).
   // More than 16 query heads to a key head: several workgroups read the same codes.
   const int row = a.cache.head_dim >> (a.cache.fmt != kKvFp8 && a.cache.fmt != kKvMx8);
-  a.stream = tiles_of(a) == 1 && 2.0 * room * a.requests * a.cache.heads * row > 0x1p27;
+  a.stream = a.tiles == 1 && 2.0 * room * a.requests * a.cache.heads * row > 0x1p27;
   want = want > most ? most : want;
   // Short requests whole, eight waves each: one launch instead of two (1 of 200 / 500 / 1000
   // FP8 tokens 7.6 / 9.5 / 12.4 us instead of 8.9 / 8.8 / 9.4, and 8.3 / 10.0 / 12.8 instead of
@@ -192,6 +189,9 @@ void plan(fp4lib::AttnArgs& a) {
     }
   }
   a.splits = static_cast<int>(want < 1 ? 1 : want > kMaxParts ? kMaxParts : want);
+  // Longest requests first, where workgroups wait for others (64 of up to 8192 MXFP8 tokens 113 ->
+  // 101.5 us, 32 of up to 16000 MXFP4 tokens 74.6 -> 59; the order costs half a microsecond).
+  a.longest_first = a.requests > 1 && a.requests <= kOrdered && a.waves == kWaves && each * a.splits > cu;
 }
 
 int64_t part_bytes(const fp4lib::AttnArgs& a) {
@@ -216,9 +216,8 @@ namespace {
 
 // One launch's requests.
 hipError_t launch_some(const AttnArgs& a, hipStream_t s) {
-  const int tiles = tiles_of(a);
   int64_t grid = static_cast<int64_t>(a.requests) * a.cache.heads * a.splits;
-  if (tiles > 1) grid = (grid + 7) / 8 * 8 * tiles;
+  if (a.tiles > 1) grid = (grid + 7) / 8 * 8 * a.tiles;
   const hipError_t e = with_format(a.cache.fmt, [&](auto f) {
     return launch_attention_fmt<decltype(f)::value>(a, static_cast<uint32_t>(grid), s);
   });
@@ -235,7 +234,9 @@ hipError_t launch_some(const AttnArgs& a, hipStream_t s) {
   });
 }
 
-constexpr int64_t kMostGroups = int64_t(1) << 22;     // of a launch: a grid has fewer than 2^32 threads
+// Workgroups of a launch: a grid has fewer than 2^32 threads, and the kernel divides a part's
+// number, which is smaller, by up to 1024 with a product.
+constexpr int64_t kMostGroups = int64_t(1) << 22;
 
 }  // namespace
 
@@ -243,7 +244,10 @@ hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
   AttnArgs a = args;
   plan(a);
   if (!a.part || a.part_bytes < part_bytes(a)) a.splits = 1;
-  const int64_t groups = static_cast<int64_t>(a.cache.heads) * tiles_of(a) * a.splits;
+  auto inverse = [](int n) { return static_cast<uint32_t>(((int64_t(1) << 32) + n - 1) / n); };
+  a.by_splits = inverse(a.splits);
+  a.by_heads = inverse(a.cache.heads);
+  const int64_t groups = static_cast<int64_t>(a.cache.heads) * a.tiles * a.splits;
   const int most = static_cast<int>(groups < kMostGroups ? kMostGroups / groups : 1);
   const int64_t row = static_cast<int64_t>(a.q.heads) * a.cache.head_dim * (a.out_f32 ? 4 : 2);
   for (int first = 0; first < args.requests; first += most) {

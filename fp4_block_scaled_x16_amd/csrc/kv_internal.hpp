@@ -91,6 +91,9 @@ struct AttnArgs {
   int splits, min_part;        // set by the launcher
   int waves;                   // set by the launcher: of a workgroup
   int stream;                  // set by the launcher: codes are read past the caches
+  int longest_first;           // set by the launcher: the order of the requests' workgroups
+  int group, tiles;            // set by the launcher: query heads of a key head, workgroups that share them
+  uint32_t by_splits, by_heads;   // set by the launcher: 2^32 / splits and / cache.heads, rounded up
 };
 
 hipError_t launch_qk_rows(const QkRowsArgs& a, hipStream_t s);
