@@ -2,13 +2,14 @@
 // key-value cache:  out = softmax(scale q K^T) V  over the request's tokens.
 //
 // Bound by reading the codes once, where there are many: 64 requests of up to 8192
-// MXFP8 tokens (8 heads of 128 for 32 query heads) take 113 us, 4.9 TB/s of codes and
-// scales; 4 of 120000 NVFP4 tokens 102 us, 5.5 TB/s; 1000 of up to 4000 MXFP8 tokens of
-// heads of 64 365 us, 5.8 TB/s.  Few or short requests by their steps, one after the
-// other: about 1 us for 128 tokens of heads of 128 (a tile's 220 vector and 90 scalar
-// instructions, and the wait for its codes), and about 5 for the launch, the loads that
-// wait for one another at the start, and the meeting of the waves (1 request of 1000
-// FP8 tokens: 6 us and 3 for the join).
+// MXFP8 tokens (8 heads of 128 for 32 query heads) take 101 us, 5.5 TB/s of codes and
+// scales, 64 of 8192 178 us, 6.2 TB/s; 1000 of up to 4000 of heads of 64 365 us, 5.8 TB/s.
+// With 4-bit codes and block scales that are no powers of two by the vector instructions
+// as well (4 of 120000 NVFP4 tokens: 75 % of cycles; 103 to 109 us, 5.1 to 5.4 TB/s).  Few
+// or short requests by their steps, one after the other: about 1 us for 128 tokens of
+// heads of 128 (a tile's 220 vector and 90 scalar instructions, and the wait for its
+// codes), and about 5 for the launch, the loads that wait for one another at the start,
+// and the meeting of the waves (1 request of 1000 FP8 tokens: 6 us and 3 for the join).
 //
 // A workgroup of four waves has one request, one key head, up to 16 of the query heads
 // that share it, and a part of the request's tokens; its waves take turns at tiles of

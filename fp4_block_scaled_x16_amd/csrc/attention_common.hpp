@@ -31,7 +31,8 @@ __device__ __forceinline__ int tokens_of(const fp4lib::AttnArgs& a, int request)
   return len < 0 ? 0 : len > room ? static_cast<int>(room) : len;
 }
 
-// Requests of which the longest may come first (a wave looks at 64 lengths at once).
+// Requests of which the longest may come first (a wave looks at 64 lengths at once; with 512
+// what it costs is more than it gives: 500 of up to 3000 MXFP4 tokens 177 -> 188 us).
 constexpr int kOrdered = 256;
 
 // The workspace: the parts' sums [row][part][head_dim], and behind them each one's

@@ -311,3 +311,29 @@ def test_many_short_requests(fmt, d, group, requests, heads, page, width):
                                     torch.tensor(lens, dtype=torch.int32, device=DEV), return_lse=True)
     sel = list(range(0, requests, max(1, requests // 24)))
     check(out[sel], lse[sel], q[sel], cache, pool, table[sel], [lens[i] for i in sel], d ** -0.5)
+
+
+@pytest.mark.parametrize("requests", [2, 63, 65, 128, 200, 256, 257])
+def test_order_of_the_requests(requests):
+    """Whichever request a workgroup takes: every one is served, with equal lengths and with
+    different ones, none and all that there is room for among them."""
+    page, width, heads = 16, 40, 4
+    cache = filled("mxfp8", 40, page, heads, 64)
+    table = torch.stack([torch.randperm(40, generator=torch.Generator().manual_seed(i)) for i in range(requests)]).int().to(DEV)
+    q = query(requests, 8, 64, 3).to(DEV)
+    r = torch.arange(requests, device=DEV)
+    for lens in (torch.full_like(r, 640), torch.full_like(r, 1), torch.zeros_like(r), r * 977 % 641, torch.where(r == 1, 640, 0),
+                 r * 977 % 700 - 30, torch.where(r % 2 == 0, 2 ** 31 - 1, 0)):
+        lens = lens.int()
+        api.selftest_set_attention_splits(0)
+        out, lse = api.attention_decode(q, cache, table, lens, return_lse=True)
+        # one by one, in one part
+        api.selftest_set_attention_splits(1)
+        for i in range(requests):
+            a, b = api.attention_decode(q[i:i + 1], cache, table[i:i + 1], lens[i:i + 1], return_lse=True, out_dtype=torch.float32)
+            n = int(lens[i].clamp(0, 640))
+            # bf16's half step of the output (the parts' sums and p are exact to 2^-15 of |v|, here up to 2^9)
+            assert (out[i].float() - a[0]).abs().max() <= 2.0 ** -8 * a.abs().max() + 2.0 ** -6, (i, n)
+            assert torch.equal(torch.isinf(lse[i]), torch.isinf(b[0])) and (n == 0) == bool(torch.isinf(b).all())
+            if n:
+                assert (lse[i] - b[0]).abs().max() <= 2.0 ** -10
