@@ -224,55 +224,175 @@ struct ScalePick {
   }
 };
 
-// The nth request from the longest on (of up to kOrdered, in 16 classes of lengths; in each
-// by number): where more workgroups wait than the chip holds, those that come last
-// should have least to do.
-struct Nth {
-  int request, len;
+// A workgroup's part of a request: tokens part * per .., as one of `parts`, the first of
+// which is part number `base` of its key head's.
+struct Item {
+  int request, len, part, parts, per, base;
 };
-__device__ __forceinline__ Nth nth_longest(const fp4lib::AttnArgs& a, int nth, int lane) {
-  constexpr int kChunks = kOrdered / 64, kClasses = 16;
-  int len[kChunks], cls[kChunks];
-  uint32_t most = 0;
+
+// x / d rounded down, for x below 2^24 and d of 1 or more.
+__device__ __forceinline__ int quotient(int x, int d) {
+  const int q = static_cast<int>(static_cast<float>(x) * __builtin_amdgcn_rcpf(static_cast<float>(d)));
+  const int rest = x - q * d;
+  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
+}
+
+__device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  return __builtin_amdgcn_readlane(v, 0) + __builtin_amdgcn_readlane(v, 16) + __builtin_amdgcn_readlane(v, 32) +
+         __builtin_amdgcn_readlane(v, 48);
+}
+
+// Sum over the lanes up to this one.
+__device__ __forceinline__ int wave_scan(int v) {
+  auto moved = [&](auto ctrl, auto rows) {
+    return __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+  };
+  v += moved(Const<0x111>(), Const<0xF>());      // row_shr:1, 2, 4, 8
+  v += moved(Const<0x112>(), Const<0xF>());
+  v += moved(Const<0x114>(), Const<0xF>());
+  v += moved(Const<0x118>(), Const<0xF>());
+  v += moved(Const<0x142>(), Const<0xA>());      // row_bcast:15 into the odd rows, row_bcast:31 into the upper two
+  v += moved(Const<0x143>(), Const<0xC>());
+  return v;
+}
+
+// n / d rounded up (n in steps, kStep tokens), exact below 2^23, and else too much by a step.
+__device__ __forceinline__ int share(uint32_t n, int d) {
+  return n < (1u << 23) ? quotient(n + d - 1, d) : min(1 << 23, static_cast<int>(n / static_cast<uint32_t>(d)) + 1);
+}
+
+// Parts by the lengths; the one that has place nth when the longest come first (in 16
+// classes; in each by request): where more workgroups wait than the chip holds, those
+// that come last should have least to do.  parts = 0: there is no nth.
+// kWhole: every request is one part.
+template <int D, bool kWhole>
+__device__ __forceinline__ Item planned_item(const fp4lib::AttnArgs& a, int nth, int lane) {
+  constexpr int kChunks = kPlanned / 64, kClasses = 16;
+  // parts of as many steps that there are target[0] of all requests', fewer (target[1]: one to a
+  // CU) if they were short
+  int want = 1, step = 1 << 23;
+  auto set_step = [&](uint32_t all) {
+    want = a.target[0];
+    step = share(all, want);
+    if (D == 64 && step < 16) {
+      want = max(want / 2, 1);
+      step = share(all, want);
+    }
+    if (step < (D == 64 ? 5 : 8)) {
+      want = a.target[1];
+      step = share(all, want);
+    }
+    step = max(step, a.min_part / kStep);
+  };
+  if (!kWhole && a.requests == 1) {
+    const int len = tokens_of(a, 0), size = (len + kStep - 1) / kStep;
+    set_step(size);
+    const int parts = max(1, quotient(size + step - 1, step));
+    return {0, len, nth, parts, quotient(size + parts - 1, parts) * kStep, 0};
+  }
+  int len[kChunks], parts[kChunks], size[kChunks];       // size: steps, then steps of a part
+  uint32_t all = 0;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) len[k] = tokens_of(a, min(64 * k + lane, a.requests - 1));
 #pragma unroll
-  for (int k = 0; k < kChunks; ++k) most = fp8dev::umax(most, len[k]);
-  most = lane_max<16>(most);
-  uint32_t top = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) top = fp8dev::umax(top, __builtin_amdgcn_readlane(most, 16 * k));
-  const float by = kClasses * __builtin_amdgcn_rcpf(static_cast<float>(top) + 1.0f);
-#pragma unroll
-  for (int k = 0; k < kChunks; ++k)
-    cls[k] = 64 * k + lane < a.requests ? min(static_cast<int>(static_cast<float>(len[k]) * by), kClasses - 1) : -1;
-  // the class: the highest with more than nth requests in it and above; `above` it
-  int c = 0, above = 0;
-#pragma unroll
-  for (int bit = kClasses / 2; bit; bit /= 2) {
-    int count = 0;
-#pragma unroll
-    for (int k = 0; k < kChunks; ++k)
-      if (64 * k < a.requests) count += __popcll(__ballot(cls[k] >= c + bit));
-    if (count > nth) c += bit;
-    else above = count;
+  for (int k = 0; k < kChunks; ++k) {
+    size[k] = 64 * k + lane < a.requests ? (len[k] + kStep - 1) / kStep : 0;
+    all += size[k];
   }
-  nth -= above;
-  Nth found{0, 0};
+  if constexpr (!kWhole) set_step(wave_sum(all));
+  auto split = [&] {
+    uint32_t count = 0;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) {
+      if (64 * k >= a.requests) break;
+      parts[k] = 64 * k + lane < a.requests ? max(1, quotient(size[k] + step - 1, step)) : 0;
+      count += parts[k];
+    }
+    return static_cast<int>(wave_sum(count));
+  };
+  int count = a.requests;
+  if constexpr (kWhole) {
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k) parts[k] = 64 * k + lane < a.requests;
+  } else {
+    count = split();
+  }
+  // what rounding up each request's number has added comes off again: a round of workgroups that
+  // is not full costs as much as one that is
+  if (!kWhole && count > want && a.requests < want) {
+    step = share(static_cast<uint32_t>(min(step, 1 << 12)) * count, want);
+    count = split();
+  }
+  const bool order = kWhole || count > a.target[1];      // (else each has a CU to itself)
+  uint32_t longest = 0;
 #pragma unroll
   for (int k = 0; k < kChunks; ++k) {
     if (64 * k >= a.requests) break;
-    const uint64_t in = __ballot(cls[k] == c);
-    const int count = __popcll(in);
-    if (nth >= 0 && nth < count) {
-      const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(in >> 32),
-                                                   __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(in), 0));
-      const int at = __ffsll(static_cast<unsigned long long>(__ballot(cls[k] == c && before == nth))) - 1;
-      found = {64 * k + at, __builtin_amdgcn_readlane(len[k], at)};
-    }
-    nth -= count;
+    const int n = max(parts[k], 1);
+    if constexpr (!kWhole) size[k] = quotient(size[k] + n - 1, n);
+    longest = fp8dev::umax(longest, size[k]);
   }
-  return {__builtin_amdgcn_readfirstlane(found.request), __builtin_amdgcn_readfirstlane(found.len)};
+  int c = 0;
+  float by = 0.0f;               // all in class 0
+  if (order) {
+    longest = lane_max<16>(longest);
+    longest = fp8dev::umax(fp8dev::umax(__builtin_amdgcn_readlane(longest, 0), __builtin_amdgcn_readlane(longest, 16)),
+                           fp8dev::umax(__builtin_amdgcn_readlane(longest, 32), __builtin_amdgcn_readlane(longest, 48)));
+    by = kClasses * __builtin_amdgcn_rcpf(static_cast<float>(longest) + 1.0f);
+    auto class_of = [&](int k) { return min(static_cast<int>(static_cast<float>(size[k]) * by), kClasses - 1); };
+    // the class: the highest with more than nth parts in it and above; `above` it
+    int above = 0;
+#pragma unroll
+    for (int bit = kClasses / 2; bit; bit /= 2) {
+      uint32_t over = 0;
+#pragma unroll
+      for (int k = 0; k < kChunks; ++k) {
+        if (64 * k >= a.requests) break;
+        if constexpr (kWhole) over += __popcll(__ballot(parts[k] && class_of(k) >= c + bit));
+        else over += class_of(k) >= c + bit ? parts[k] : 0;
+      }
+      if constexpr (!kWhole) over = wave_sum(over);
+      if (static_cast<int>(over) > nth) c += bit;
+      else above = over;
+    }
+    nth = __builtin_amdgcn_readfirstlane(nth - above);
+  }
+  Item found{0, 0, 0, 0, 0, 0};
+  int base = 0;
+#pragma unroll
+  for (int k = 0; k < kChunks; ++k) {
+    if (64 * k >= a.requests) break;
+    const bool mine = min(static_cast<int>(static_cast<float>(size[k]) * by), kClasses - 1) == c;
+    if constexpr (kWhole) {
+      const uint64_t in = __ballot(mine && parts[k]);
+      const int many = __popcll(in);
+      if (nth >= 0 && nth < many) {
+        const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(in >> 32),
+                                                     __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(in), 0));
+        const int at = __builtin_amdgcn_readfirstlane(
+            __ffsll(static_cast<unsigned long long>(__ballot(mine && parts[k] && before == nth))) - 1);
+        found = {64 * k + at, __builtin_amdgcn_readlane(len[k], at), 0, 1,
+                 __builtin_amdgcn_readlane(size[k], at) * kStep, 64 * k + at};
+      }
+      nth -= many;
+      continue;
+    }
+    const int up_to = wave_scan(parts[k]), in = wave_scan(mine ? parts[k] : 0);
+    const uint64_t here = __ballot(mine && nth < in && nth >= in - parts[k]);
+    if (here) {
+      const int at = __builtin_amdgcn_readfirstlane(__ffsll(static_cast<unsigned long long>(here)) - 1);
+      const int n = __builtin_amdgcn_readlane(parts[k], at);
+      found = {64 * k + at, __builtin_amdgcn_readlane(len[k], at), nth - (__builtin_amdgcn_readlane(in, at) - n), n,
+               __builtin_amdgcn_readlane(size[k], at) * kStep, base + __builtin_amdgcn_readlane(up_to, at) - n};
+    }
+    nth -= __builtin_amdgcn_readlane(in, 63);
+    base += __builtin_amdgcn_readlane(up_to, 63);
+  }
+  return found;
 }
 
 // Read through the scalar cache (the kernel does not write the page table), whose
@@ -303,17 +423,31 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
     id = 8 * part + id % 8;
   }
   // (the quotients are exact: id < 2^32 / 1024)
-  const uint32_t part = a.splits > 1 ? __umulhi(id, a.by_splits) : id;
+  const bool planned = W == kWaves && a.planned;
+  const uint32_t part = !planned && a.splits > 1 ? __umulhi(id, a.by_splits) : id;
   const int split = id - part * a.splits;
   id = a.cache.heads > 1 ? __umulhi(part, a.by_heads) : part;
   const int kv = part - id * a.cache.heads;
-  if (id >= static_cast<uint32_t>(a.requests)) return;
-  const Nth nth = W == kWaves && a.longest_first ? nth_longest(a, id, lane)
-                                                      : Nth{static_cast<int>(id), tokens_of(a, id)};
-  const int request = nth.request, len = nth.len, per = part_tokens(len, a);
-  const int begin = split * per, end = min(len, begin + per);
+  Item item;
+  if (planned) {
+    item = a.splits > 1 ? planned_item<D, false>(a, id, lane) : planned_item<D, true>(a, id, lane);
+  } else {
+    if (id >= static_cast<uint32_t>(a.requests)) return;
+    item.request = id;
+    item.len = tokens_of(a, id);
+    item.part = split;
+    item.per = part_tokens(item.len, a);
+    item.parts = max(1, (item.len + item.per - 1) / item.per);
+    item.base = item.request * a.splits;
+  }
+  if (item.part >= item.parts) return;
+  const int request = __builtin_amdgcn_readfirstlane(item.request);
+  const int begin = __builtin_amdgcn_readfirstlane(item.part * item.per);
+  const int end = __builtin_amdgcn_readfirstlane(min(item.len, begin + item.per));
   const int first = kv * group + tile * kHeads, heads = min(kHeads, group - tile * kHeads);
-  if (begin >= end && split > 0) return;
+  // (every thread: the compiler fails where one of them is chosen)
+  if (a.splits > 1 && kv == 0 && tile == 0 && item.part == 0)
+    request_parts(a)[request] = make_int2(item.base, item.parts);
   const int col = NP == 1 ? c & 7 : c;
   const bool mine = col < heads;
   const int64_t row = static_cast<int64_t>(request) * a.q.heads + first + (mine ? col : 0);
@@ -574,7 +708,7 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
   if (!mine) return;
 
   // lane (c, g) has elements (4 g + i) D/16 + e
-  const bool whole = begin == 0 && end >= len;
+  const bool whole = item.parts == 1;
   float s_enc, s_dec;
   tensor_scales<FMT>(a.cache, 1, s_enc, s_dec);
   if constexpr (FMT == kKvUe4) s_dec *= 32.0f;
@@ -596,14 +730,15 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
     if (a.lse && g == 0) a.lse[row] = (all + __builtin_log2f(total) - kShift) / kLog2e;
   } else {
     // sums with V's tensor scale; the maximum and the sum of p apart
-    float* o = a.part + (row * a.splits + split) * D;
+    const int64_t at = (kv * a.items + item.base + item.part) * group + (tile * kHeads + col);
+    float* o = a.part + at * D;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int e = 0; e < S::kElems; e += 4)
         *reinterpret_cast<float4*>(o + (4 * g + i) * S::kElems + e) =
             make_float4(acc[e][i] * s_dec, acc[e + 1][i] * s_dec, acc[e + 2][i] * s_dec, acc[e + 3][i] * s_dec);
-    if (g == 0) part_sums(a)[row * a.splits + split] = make_float2(all - kShift, total);
+    if (g == 0) part_sums(a)[at] = make_float2(all - kShift, total);
   }
 }
 

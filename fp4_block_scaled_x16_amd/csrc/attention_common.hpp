@@ -18,8 +18,12 @@ constexpr int kStep = kWaves * kTile;         // tokens that a workgroup takes a
 // instead of 66 us for 16 of 8000).
 __host__ __device__ constexpr int waves_per_simd(int head_dim) { return head_dim == 64 ? 4 : head_dim == 128 ? 3 : 2; }
 
-// Tokens of a part (the last may have fewer) of a request of len tokens: at most
-// a.splits parts of at least a.min_part, whole steps each.
+// Requests whose parts may go by their lengths (a wave looks at 64 of these at once; with
+// 512 what it costs is more than it gives: 500 of up to 3000 MXFP4 tokens 177 -> 188 us).
+constexpr int kPlanned = 256;
+
+// Tokens of a part (the last may have fewer) of a request of len tokens where the parts
+// do not go by the lengths: at most a.splits parts of at least a.min_part, whole steps each.
 __host__ __device__ __forceinline__ int part_tokens(int len, const fp4lib::AttnArgs& a) {
   const int even = (len + a.splits - 1) / a.splits;
   return even <= a.min_part ? a.min_part : (even + kStep - 1) / kStep * kStep;
@@ -31,14 +35,14 @@ __device__ __forceinline__ int tokens_of(const fp4lib::AttnArgs& a, int request)
   return len < 0 ? 0 : len > room ? static_cast<int>(room) : len;
 }
 
-// Requests of which the longest may come first (a wave looks at 64 lengths at once; with 512
-// what it costs is more than it gives: 500 of up to 3000 MXFP4 tokens 177 -> 188 us).
-constexpr int kOrdered = 256;
-
-// The workspace: the parts' sums [row][part][head_dim], and behind them each one's
-// maximum (in powers of two) and sum of p, [row][part].
+// The workspace: the parts' sums [key head][part][query head of it][head_dim], behind
+// them each one's maximum (in powers of two) and sum of p, and behind these each request's
+// first part and number of parts.
 __device__ __forceinline__ float2* part_sums(const fp4lib::AttnArgs& a) {
-  return reinterpret_cast<float2*>(a.part + static_cast<int64_t>(a.requests) * a.q.heads * a.splits * a.cache.head_dim);
+  return reinterpret_cast<float2*>(a.part + a.items * a.q.heads * a.cache.head_dim);
+}
+__device__ __forceinline__ int2* request_parts(const fp4lib::AttnArgs& a) {
+  return reinterpret_cast<int2*>(part_sums(a) + a.items * a.q.heads);
 }
 
 }  // namespace fp4attn

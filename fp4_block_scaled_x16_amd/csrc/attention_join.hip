@@ -30,6 +30,19 @@ __device__ __forceinline__ void finish(const fp4lib::AttnArgs& a, int64_t row, i
   if (a.lse && d == 0) a.lse[row] = (top + __builtin_log2f(total)) / kLog2e;
 }
 
+// A row's parts: every a.group-th row of sums from `first` on.
+struct Parts {
+  int64_t first;
+  int count;
+  __device__ __forceinline__ Parts(const fp4lib::AttnArgs& a, uint32_t row) {
+    const uint32_t heads = a.q.heads, request = row / heads, head = row - request * heads;
+    const uint32_t kv = head / static_cast<uint32_t>(a.group);
+    const int2 p = request_parts(a)[request];
+    first = (kv * a.items + p.x) * a.group + (head - kv * a.group);
+    count = p.y;
+  }
+};
+
 // Few parts: D / 4 lanes per query head, four elements each.
 constexpr int kFewParts = 16;
 template <int D>
@@ -38,21 +51,23 @@ __global__ __launch_bounds__(256) void k_attention_join_few(fp4lib::AttnArgs a) 
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / kQuads) + threadIdx.x / kQuads;
   if (row >= static_cast<int64_t>(a.requests) * a.q.heads) return;
   const int d = threadIdx.x % kQuads;
-  const int len = tokens_of(a, static_cast<uint32_t>(row) / static_cast<uint32_t>(a.q.heads));
-  const int per = part_tokens(len, a), parts = (len + per - 1) / per;
+  const Parts in(a, static_cast<uint32_t>(row));
+  const int parts = in.count;
   if (parts <= 1) return;
-  const float4* p = reinterpret_cast<const float4*>(a.part + row * a.splits * D) + d;
-  const float2* ml = part_sums(a) + row * a.splits;
+  const int step = a.group;
+  const float4* p = reinterpret_cast<const float4*>(a.part + in.first * D) + d;
+  const float2* ml = part_sums(a) + in.first;
   float top = -__builtin_inff(), total = 0.0f;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int s = 0; s < parts; ++s) top = fmaxf(top, ml[s].x);
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, ml[s * step].x);
   const float ref = top == -__builtin_inff() ? 0.0f : top;
 #pragma unroll 4
   for (int s = 0; s < parts; ++s) {
-    const float4 v = p[s * kQuads];
-    const float by = __builtin_amdgcn_exp2f(ml[s].x - ref);
-    total += by * ml[s].y;
+    const float4 v = p[s * step * kQuads];
+    const float2 m = ml[s * step];
+    const float by = __builtin_amdgcn_exp2f(m.x - ref);
+    total += by * m.y;
     o.x += by * v.x;
     o.y += by * v.y;
     o.z += by * v.z;
@@ -70,19 +85,18 @@ __global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
   __shared__ float weights[kMaxParts];
   __shared__ float2 most[4];
   const int64_t row = blockIdx.x;
-  const int request = static_cast<int>(row / a.q.heads);
-  const int len = tokens_of(a, request), per = part_tokens(len, a);
-  const int parts = (len + per - 1) / per;
+  const Parts in(a, static_cast<uint32_t>(row));
+  const int parts = in.count;
   if (parts <= 1) return;
-  const float* p = a.part + row * a.splits * D;
-  const float2* ml = part_sums(a) + row * a.splits;
+  const float* p = a.part + in.first * D;
+  const float2* ml = part_sums(a) + in.first;
   // what each part's sums count for: 2^(its maximum - the largest)
   float2 mine[kMaxParts / 256];
   float top = -__builtin_inff();
 #pragma unroll
   for (int i = 0; i < kMaxParts / 256; ++i) {
     const int s = threadIdx.x + 256 * i;
-    mine[i] = s < parts ? ml[s] : make_float2(-__builtin_inff(), 0.0f);
+    mine[i] = s < parts ? ml[s * a.group] : make_float2(-__builtin_inff(), 0.0f);
     top = fmaxf(top, mine[i].x);
   }
 #pragma unroll
@@ -112,7 +126,7 @@ __global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
   for (int s = share; s < parts; s += kShares) {
-    const float4 v = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(s) * D + 4 * d);
+    const float4 v = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(s) * a.group * D + 4 * d);
     const float by = weights[s];
     o.x += by * v.x;
     o.y += by * v.y;
@@ -134,18 +148,26 @@ __global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
 
 std::atomic<int> g_splits{0};
 
-// Parts per request and the least tokens of one, from what the page table has room
-// for (the lengths are on the device; a shorter request is shared among as many).
-// Two workgroups on every CU, if that leaves a part 1024 tokens (each starts with
-// three loads that wait for one another, and ends with a join), else as many as there
-// are CUs, but not more: 4 requests of 120000 NVFP4 tokens in 8 / 16 / 24 / 64 parts
-// 126 / 109 / 112 / 116 us, 1 of 30000 FP8 tokens in 32 / 64 / 128 parts 17.4 / 19.2 / 22, 6 of
-// 3084 MXFP8 tokens of 8 heads in 4 / 5 / 6 / 8 parts 16.0 / 15.2 / 18.9 / 18.2, 72 of 551 of 2
-// heads in 1 / 2 parts 11.1 / 15.6.  Where requests alone fill the chip, two parts of
-// over 2048 tokens even out their lengths (64 of up to 8192 in 1 / 2 / 8 parts 124 / 120 /
-// 122 us, 256 of up to 1024 in 1 / 2 parts 15.4 / 21.6), and more of over 4096, up to eight
-// times what fills it (20 of up to 21080 NVFP4 tokens of 16 heads of 64 in 2 / 4 / 6 parts
-// 111 / 76 / 75.5).
+// At most `splits` parts of a request.
+void set_parts(fp4lib::AttnArgs& a, int splits) {
+  a.splits = splits;
+  a.items = splits == 1 ? a.requests : a.planned ? a.requests + a.target[0] : static_cast<int64_t>(a.requests) * splits;
+}
+
+// How a request's tokens are shared.  Up to kPlanned requests' parts go by their lengths,
+// which are on the device (planned_item in attention.hip): the page table may have room for far
+// more (64 requests of up to 500 MXFP8 tokens take 16 us with room for 131072 each; parts
+// planned from the room took 57).  Two workgroups on every CU (heads of 64: four), if that
+// leaves a part 8 steps of 128 tokens, else as many as there are CUs, but not more: 4 requests of
+// 120000 NVFP4 tokens in 8 / 16 / 24 / 64 parts 126 / 109 / 112 / 116 us, 1 of 30000 FP8 tokens in
+// 32 / 64 / 128 parts 17.4 / 19.2 / 22, 6 of 3084 MXFP8 tokens of 8 heads in 4 / 5 / 6 / 8 parts
+// 16.0 / 15.2 / 18.9 / 18.2.  Against parts alike for every request: 16 of up to 30000 FP8 tokens
+// 104 -> 95, 200 of up to 4000 MXFP8 tokens 159 -> 144, 1 of 30000 18.4 -> 19.1.
+// More requests: two parts of over 2048 tokens even out lengths (300 of up to 2500 of 2 heads
+// 55 -> 51), up to eight of 4096, while the workgroups are not too many: where the table has
+// more room than that, most of them find nothing to do (1000 of up to 200 MXFP4 tokens with
+// room for 131072 each 241 -> 38).  Where one part per request will do, the join is not launched
+// (72 of 551 tokens of 2 heads in 1 / 2 parts 11.1 / 15.6, 256 of up to 1024 15.4 / 21.6).
 void plan(fp4lib::AttnArgs& a) {
   const int64_t room = static_cast<int64_t>(a.table_width) << a.cache.page_shift, cu = fp4lib::device_cu_count();
   a.group = a.q.heads / a.cache.heads;
@@ -157,6 +179,7 @@ void plan(fp4lib::AttnArgs& a) {
   if (room < 1024 * full) want = cu / each;
   auto parts_of = [&](int64_t tokens, int64_t cap) { return std::min((room + tokens - 1) / tokens, cap); };
   want = std::max({want, parts_of(2048, 2 * full), parts_of(4096, 8 * full)});
+  if (a.requests > kPlanned) want = std::min(want, std::max<int64_t>(1, 16 * slots / each));
   a.min_part = 2 * each >= slots ? 4 * kStep : kStep;
   if (const int forced = g_splits.load()) {
     want = forced;
@@ -188,16 +211,18 @@ void plan(fp4lib::AttnArgs& a) {
       want = 1;
     }
   }
-  a.splits = static_cast<int>(want < 1 ? 1 : want > kMaxParts ? kMaxParts : want);
-  // Longest requests first, where workgroups wait for others (64 of up to 8192 MXFP8 tokens 113 ->
-  // 101 us, 32 of up to 16000 MXFP4 tokens 74.6 -> 58.5; 20 of 3000 NVFP4 tokens 26.5 -> 27.2).
-  a.longest_first = a.requests > 1 && a.requests <= kOrdered && a.waves == kWaves && each * a.splits > cu;
+  const int64_t ht = static_cast<int64_t>(a.cache.heads) * a.tiles, first = a.cache.head_dim == 64 ? 4 * cu : slots;
+  a.target[0] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxParts, first / ht)));
+  a.target[1] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxParts, cu / ht)));
+  a.planned = a.requests <= kPlanned && a.waves == kWaves && !g_splits.load() && (want > 1 || each > cu);
+  if (a.planned && want > 1) want = std::min<int64_t>(most, a.target[0]);
+  set_parts(a, static_cast<int>(want < 1 ? 1 : want > kMaxParts ? kMaxParts : want));
 }
 
 int64_t part_bytes(const fp4lib::AttnArgs& a) {
   return a.splits <= 1 ? 0
-                       : static_cast<int64_t>(a.requests) * a.q.heads * a.splits * (a.cache.head_dim + 2) *
-                             static_cast<int64_t>(sizeof(float));
+                       : a.items * a.q.heads * (a.cache.head_dim + 2) * static_cast<int64_t>(sizeof(float)) +
+                             a.requests * static_cast<int64_t>(sizeof(int2));
 }
 
 }  // namespace
@@ -216,7 +241,7 @@ namespace {
 
 // One launch's requests.
 hipError_t launch_some(const AttnArgs& a, hipStream_t s) {
-  int64_t grid = static_cast<int64_t>(a.requests) * a.cache.heads * a.splits;
+  int64_t grid = a.items * a.cache.heads;
   if (a.tiles > 1) grid = (grid + 7) / 8 * 8 * a.tiles;
   const hipError_t e = with_format(a.cache.fmt, [&](auto f) {
     return launch_attention_fmt<decltype(f)::value>(a, static_cast<uint32_t>(grid), s);
@@ -225,7 +250,7 @@ hipError_t launch_some(const AttnArgs& a, hipStream_t s) {
   return with_dim(a.cache.head_dim, [&](auto d) {
     constexpr int D = decltype(d)::value;
     const int64_t rows = static_cast<int64_t>(a.requests) * a.q.heads;
-    if (a.splits <= kFewParts)
+    if (a.splits <= kFewParts || (a.planned && a.requests * a.q.heads >= 2048))
       hipLaunchKernelGGL(k_attention_join_few<D>, dim3(static_cast<uint32_t>((rows * (D / 4) + 255) / 256)),
                          dim3(256), 0, s, a);
     else
@@ -243,15 +268,16 @@ constexpr int64_t kMostGroups = int64_t(1) << 22;
 hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
   AttnArgs a = args;
   plan(a);
-  if (!a.part || a.part_bytes < part_bytes(a)) a.splits = 1;
+  if (!a.part || a.part_bytes < part_bytes(a)) set_parts(a, 1);
   auto inverse = [](int n) { return static_cast<uint32_t>(((int64_t(1) << 32) + n - 1) / n); };
   a.by_splits = inverse(a.splits);
   a.by_heads = inverse(a.cache.heads);
-  const int64_t groups = static_cast<int64_t>(a.cache.heads) * a.tiles * a.splits;
-  const int most = static_cast<int>(groups < kMostGroups ? kMostGroups / groups : 1);
+  const int64_t groups = static_cast<int64_t>(a.cache.heads) * a.tiles * (a.items / a.requests);
+  const int most = a.planned ? a.requests : static_cast<int>(groups < kMostGroups ? kMostGroups / groups : 1);
   const int64_t row = static_cast<int64_t>(a.q.heads) * a.cache.head_dim * (a.out_f32 ? 4 : 2);
   for (int first = 0; first < args.requests; first += most) {
     a.requests = args.requests - first < most ? args.requests - first : most;
+    if (!a.planned) set_parts(a, a.splits);
     a.q.x = args.q.x + first * args.q.token;
     a.table = args.table + first * args.table_stride;
     a.lens = args.lens + first;

@@ -88,10 +88,12 @@ struct AttnArgs {
   float* lse;                  // null, or [requests, heads]
   float* part;                 // workspace: null with splits == 1
   int64_t part_bytes;
-  int splits, min_part;        // set by the launcher
+  int splits, min_part;        // set by the launcher: parts of a request at most, tokens of one at least
   int waves;                   // set by the launcher: of a workgroup
   int stream;                  // set by the launcher: codes are read past the caches
-  int longest_first;           // set by the launcher: the order of the requests' workgroups
+  int planned;                 // set by the launcher: the parts go by the lengths (attention_common.hpp)
+  int target[2];               // set by the launcher: parts of a key head's requests together (attention.hip)
+  int64_t items;               // set by the launcher: a key head's parts at most
   int group, tiles;            // set by the launcher: query heads of a key head, workgroups that share them
   uint32_t by_splits, by_heads;   // set by the launcher: 2^32 / splits and / cache.heads, rounded up
 };

@@ -337,3 +337,21 @@ def test_order_of_the_requests(requests):
             assert torch.equal(torch.isinf(lse[i]), torch.isinf(b[0])) and (n == 0) == bool(torch.isinf(b).all())
             if n:
                 assert (lse[i] - b[0]).abs().max() <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("fmt,d,group", [("mxfp8", 128, 4), ("nvfp4", 64, 12), ("fp8", 256, 2)])
+@pytest.mark.parametrize("lens", [[700], [0], [5, 700, 0, 300], [640] * 40, [1] * 70 + [1000], list(range(0, 1000, 7))])
+def test_tables_wider_than_the_requests(fmt, d, group, lens):
+    """Room for far more tokens than there are: parts go by the lengths.  Entries behind a
+    request's last page are no pages."""
+    page, heads, pages = 16, 2, 64
+    cache = filled(fmt, pages, page, heads, d)
+    pool = C.contents(cache)
+    for width in (64, 512, 8192):
+        table = tables(lens, page, pages, width, 3)
+        q = query(len(lens), heads * group, d, 4)
+        out, lse = api.attention_decode(q.to(DEV), cache, torch.from_numpy(table).to(DEV),
+                                        torch.tensor(lens, dtype=torch.int32, device=DEV), return_lse=True)
+        sel = list(range(0, len(lens), max(1, len(lens) // 12)))
+        sel += [len(lens) - 1] * (sel[-1] != len(lens) - 1)
+        check(out[sel], lse[sel], q[sel], cache, pool, table[sel], [lens[i] for i in sel], d ** -0.5)
