@@ -2,10 +2,10 @@
 // key-value cache:  out = softmax(scale q K^T) V  over the request's tokens.
 //
 // Bound by reading the codes once, where there are many: 64 requests of up to 8192
-// MXFP8 tokens (8 heads of 128 for 32 query heads) take 101 us, 5.5 TB/s of codes and
-// scales, 64 of 8192 178 us, 6.2 TB/s; 1000 of up to 4000 of heads of 64 365 us, 5.8 TB/s.
+// MXFP8 tokens (8 heads of 128 for 32 query heads) take 102 us, 5.5 TB/s of codes and
+// scales, 64 of 8192 174 us, 6.4 TB/s; 1000 of up to 4000 of heads of 64 329 us, 6.4 TB/s.
 // With 4-bit codes and block scales that are no powers of two by the vector instructions
-// as well (4 of 120000 NVFP4 tokens: 75 % of cycles; 103 to 109 us, 5.1 to 5.4 TB/s).  Few
+// as well (4 of 120000 NVFP4 tokens: 71 % of cycles; 103 to 108 us, 5.1 to 5.4 TB/s).  Few
 // or short requests by their steps, one after the other: about 1 us for 128 tokens of
 // heads of 128 (a tile's 220 vector and 90 scalar instructions, and the wait for its
 // codes), and about 5 for the launch, the loads that wait for one another at the start,
@@ -16,8 +16,9 @@
 // 32 tokens, each with a running maximum and sum of its own, and meet in LDS at the
 // end.  Where a request has several parts, their sums go to the caller's workspace and
 // k_attention_join brings them together in order (no atomics: the same bits every
-// time).  Short requests have a workgroup of eight waves each where they are few, and
-// one of a single wave where they are many (attention_join.hip: plan).
+// time).  Which part a workgroup takes goes by the lengths of all requests, the longest
+// first (planned_item).  Short requests have a workgroup of eight waves each where they are
+// few, and one of a single wave where they are many (attention_join.hip: plan).
 //
 // Codes go from global memory into registers and, widened, straight into MFMA
 // operands: no byte of the cache is used twice, so nothing is staged in LDS.

@@ -148,10 +148,12 @@ __global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
 
 std::atomic<int> g_splits{0};
 
-// At most `splits` parts of a request.
+// At most `splits` parts of a request (and where they go by the lengths, no more than
+// target[0] together but for each request's rounding up).
 void set_parts(fp4lib::AttnArgs& a, int splits) {
   a.splits = splits;
-  a.items = splits == 1 ? a.requests : a.planned ? a.requests + a.target[0] : static_cast<int64_t>(a.requests) * splits;
+  a.items = static_cast<int64_t>(a.requests) * splits;
+  if (a.planned && splits > 1) a.items = std::min<int64_t>(a.items, a.requests + a.target[0]);
 }
 
 // How a request's tokens are shared.  Up to kPlanned requests' parts go by their lengths,
