@@ -18,7 +18,7 @@
 // k_attention_join brings them together in order (no atomics: the same bits every
 // time).  Which part a workgroup takes goes by the lengths of all requests, the longest
 // first (planned_item).  Short requests have a workgroup of eight waves each where they are
-// few, and one of a single wave where they are many (attention_join.hip: plan).
+// few, and one of a single wave where they are many (attention_plan.hpp: plan).
 //
 // Codes go from global memory into registers and, widened, straight into MFMA
 // operands: no byte of the cache is used twice, so nothing is staged in LDS.
@@ -231,13 +231,6 @@ struct Item {
   int request, len, part, parts, per, base;
 };
 
-// x / d rounded down, for x below 2^24 and d of 1 or more.
-__device__ __forceinline__ int quotient(int x, int d) {
-  const int q = static_cast<int>(static_cast<float>(x) * __builtin_amdgcn_rcpf(static_cast<float>(d)));
-  const int rest = x - q * d;
-  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
-}
-
 __device__ __forceinline__ uint32_t wave_sum(uint32_t v) {
   v += dpp<kXor1>(v);
   v += dpp<kXor2>(v);
@@ -261,11 +254,6 @@ __device__ __forceinline__ int wave_scan(int v) {
   return v;
 }
 
-// n / d rounded up (n in steps, kStep tokens), exact below 2^23, and else too much by a step.
-__device__ __forceinline__ int share(uint32_t n, int d) {
-  return n < (1u << 23) ? quotient(n + d - 1, d) : min(1 << 23, static_cast<int>(n / static_cast<uint32_t>(d)) + 1);
-}
-
 // Parts by the lengths; the one that has place nth when the longest come first (in 16
 // classes; in each by request): where more workgroups wait than the chip holds, those
 // that come last should have least to do.  parts = 0: there is no nth.
@@ -273,27 +261,10 @@ __device__ __forceinline__ int share(uint32_t n, int d) {
 template <int D, bool kWhole>
 __device__ __forceinline__ Item planned_item(const fp4lib::AttnArgs& a, int nth, int lane) {
   constexpr int kChunks = kPlanned / 64, kClasses = 16;
-  // parts of as many steps that there are target[0] of all requests', fewer (target[1]: one to a
-  // CU) if they were short
-  int want = 1, step = 1 << 23;
-  auto set_step = [&](uint32_t all) {
-    want = a.target[0];
-    step = share(all, want);
-    if (D == 64 && step < 16) {
-      want = max(want / 2, 1);
-      step = share(all, want);
-    }
-    if (step < (D == 64 ? 5 : 8)) {
-      want = a.target[1];
-      step = share(all, want);
-    }
-    step = max(step, a.min_part / kStep);
-  };
   if (!kWhole && a.requests == 1) {
     const int len = tokens_of(a, 0), size = (len + kStep - 1) / kStep;
-    set_step(size);
-    const int parts = max(1, quotient(size + step - 1, step));
-    return {0, len, nth, parts, quotient(size + parts - 1, parts) * kStep, 0};
+    const int parts = parts_of(size, first_shares<D>(size, a).step);
+    return {0, len, nth, parts, steps_of(size, parts) * kStep, 0};
   }
   int len[kChunks], parts[kChunks], size[kChunks];       // size: steps, then steps of a part
   uint32_t all = 0;
@@ -304,13 +275,14 @@ __device__ __forceinline__ Item planned_item(const fp4lib::AttnArgs& a, int nth,
     size[k] = 64 * k + lane < a.requests ? (len[k] + kStep - 1) / kStep : 0;
     all += size[k];
   }
-  if constexpr (!kWhole) set_step(wave_sum(all));
+  Shares s{1, 1};
+  if constexpr (!kWhole) s = first_shares<D>(wave_sum(all), a);
   auto split = [&] {
     uint32_t count = 0;
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) {
       if (64 * k >= a.requests) break;
-      parts[k] = 64 * k + lane < a.requests ? max(1, quotient(size[k] + step - 1, step)) : 0;
+      parts[k] = 64 * k + lane < a.requests ? parts_of(size[k], s.step) : 0;
       count += parts[k];
     }
     return static_cast<int>(wave_sum(count));
@@ -324,8 +296,8 @@ __device__ __forceinline__ Item planned_item(const fp4lib::AttnArgs& a, int nth,
   }
   // what rounding up each request's number has added comes off again: a round of workgroups that
   // is not full costs as much as one that is
-  if (!kWhole && count > want && a.requests < want) {
-    step = share(static_cast<uint32_t>(min(step, 1 << 12)) * count, want);
+  if (!kWhole && count > s.want && a.requests < s.want) {
+    s.step = longer_step(s.step, count, s.want);
     count = split();
   }
   const bool order = kWhole || count > a.target[1];      // (else each has a CU to itself)
@@ -334,7 +306,7 @@ __device__ __forceinline__ Item planned_item(const fp4lib::AttnArgs& a, int nth,
   for (int k = 0; k < kChunks; ++k) {
     if (64 * k >= a.requests) break;
     const int n = max(parts[k], 1);
-    if constexpr (!kWhole) size[k] = quotient(size[k] + n - 1, n);
+    if constexpr (!kWhole) size[k] = steps_of(size[k], n);
     longest = fp8dev::umax(longest, size[k]);
   }
   int c = 0;
@@ -441,7 +413,7 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
     item.parts = max(1, (item.len + item.per - 1) / item.per);
     item.base = item.request * a.splits;
   }
-  if (item.part >= item.parts) return;
+  if (item.part >= item.parts || item.base + item.part >= a.items) return;
   const int request = __builtin_amdgcn_readfirstlane(item.request);
   const int begin = __builtin_amdgcn_readfirstlane(item.part * item.per);
   const int end = __builtin_amdgcn_readfirstlane(min(item.len, begin + item.per));

@@ -38,8 +38,11 @@ struct Parts {
     const uint32_t heads = a.q.heads, request = row / heads, head = row - request * heads;
     const uint32_t kv = head / static_cast<uint32_t>(a.group);
     const int2 p = request_parts(a)[request];
-    first = (kv * a.items + p.x) * a.group + (head - kv * a.group);
-    count = p.y;
+    // (within the workspace in any case: lengths that change while the kernels run may cost
+    // results, and no more)
+    const int64_t base = std::min<uint32_t>(p.x, static_cast<uint32_t>(a.items - 1));
+    first = (kv * a.items + base) * a.group + (head - kv * a.group);
+    count = static_cast<int>(std::min<int64_t>(std::min(p.y, a.splits), a.items - base));
   }
 };
 
@@ -148,84 +151,7 @@ __global__ __launch_bounds__(256) void k_attention_join(fp4lib::AttnArgs a) {
 
 std::atomic<int> g_splits{0};
 
-// At most `splits` parts of a request (and where they go by the lengths, no more than
-// target[0] together but for each request's rounding up).
-void set_parts(fp4lib::AttnArgs& a, int splits) {
-  a.splits = splits;
-  a.items = static_cast<int64_t>(a.requests) * splits;
-  if (a.planned && splits > 1) a.items = std::min<int64_t>(a.items, a.requests + a.target[0]);
-}
-
-// How a request's tokens are shared.  Up to kPlanned requests' parts go by their lengths,
-// which are on the device (planned_item in attention.hip): the page table may have room for far
-// more (64 requests of up to 500 MXFP8 tokens take 16 us with room for 131072 each; parts
-// planned from the room took 57).  Two workgroups on every CU (heads of 64: four), if that
-// leaves a part 8 steps of 128 tokens, else as many as there are CUs, but not more: 4 requests of
-// 120000 NVFP4 tokens in 8 / 16 / 24 / 64 parts 126 / 109 / 112 / 116 us, 1 of 30000 FP8 tokens in
-// 32 / 64 / 128 parts 17.4 / 19.2 / 22, 6 of 3084 MXFP8 tokens of 8 heads in 4 / 5 / 6 / 8 parts
-// 16.0 / 15.2 / 18.9 / 18.2.  Against parts alike for every request: 16 of up to 30000 FP8 tokens
-// 104 -> 95, 200 of up to 4000 MXFP8 tokens 159 -> 144, 1 of 30000 18.4 -> 19.1.
-// More requests: two parts of over 2048 tokens even out lengths (300 of up to 2500 of 2 heads
-// 55 -> 51), up to eight of 4096, while the workgroups are not too many: where the table has
-// more room than that, most of them find nothing to do (1000 of up to 200 MXFP4 tokens with
-// room for 131072 each 241 -> 38).  Where one part per request will do, the join is not launched
-// (72 of 551 tokens of 2 heads in 1 / 2 parts 11.1 / 15.6, 256 of up to 1024 15.4 / 21.6).
-void plan(fp4lib::AttnArgs& a) {
-  const int64_t room = static_cast<int64_t>(a.table_width) << a.cache.page_shift, cu = fp4lib::device_cu_count();
-  a.group = a.q.heads / a.cache.heads;
-  a.tiles = a.group <= 8 ? 1 : (a.group + 15) / 16;
-  const int64_t each = static_cast<int64_t>(a.requests) * a.cache.heads * a.tiles;
-  const int64_t slots = 2 * cu;
-  const int64_t most = (room + kStep - 1) / kStep, full = slots / each > 1 ? slots / each : 1;
-  int64_t want = full;
-  if (room < 1024 * full) want = cu / each;
-  auto parts_of = [&](int64_t tokens, int64_t cap) { return std::min((room + tokens - 1) / tokens, cap); };
-  want = std::max({want, parts_of(2048, 2 * full), parts_of(4096, 8 * full)});
-  if (a.requests > kPlanned) want = std::min(want, std::max<int64_t>(1, 16 * slots / each));
-  a.min_part = 2 * each >= slots ? 4 * kStep : kStep;
-  if (const int forced = g_splits.load()) {
-    want = forced;
-    a.min_part = kStep;
-  }
-  // More codes than half of the 256 MB last-level cache do not come from there again:
-  // they are read past it (64 requests of up to 8192 MXFP8 tokens 122 -> 115 us, 32 of 6000
-  // FP8 tokens, 197 MB, 45 -> 40; but 1 of 30000, 61 MB, 17.9 -> 19.1 when they are).
-  // More than 16 query heads to a key head: several workgroups read the same codes.
-  const int row = a.cache.head_dim >> (a.cache.fmt != kKvFp8 && a.cache.fmt != kKvMx8);
-  a.stream = a.tiles == 1 && 2.0 * room * a.requests * a.cache.heads * row > 0x1p27;
-  want = want > most ? most : want;
-  // Short requests whole, eight waves each: one launch instead of two (1 of 200 / 500 / 1000
-  // FP8 tokens 7.6 / 9.5 / 12.4 us instead of 8.9 / 8.8 / 9.4, and 8.3 / 10.0 / 12.8 instead of
-  // 11.6 / 11.7 / 11.8 a call where the host's part counts; heads of 64, MXFP4: 5.5 / 6.5 / 8.4
-  // instead of 7.3 / 7.3 / 7.9, and 8.2 / 8.1 / 9.1 instead of 12).
-  // Many of them, a wave each: no meeting at the end (8 heads of 128: 2000 of up to 64 FP8 tokens with
-  // 4 / 2 / 1 waves 98 / 59 / 50 us, 2000 of up to 256 MXFP4 tokens 117 / 83 / 75, 128 of up to 200 MXFP8
-  // tokens 14.4 / - / 11.7; but 256 of up to 512 MXFP4 tokens of 4 heads of 64 11.8 / - / 15.1, and
-  // 512 of up to 1024 MXFP4 tokens 66 / 69 / 78).
-  const int steps = a.cache.head_dim == 64 ? 4 : 2;
-  a.waves = kWaves;
-  if (!g_splits.load()) {
-    if (4 * room <= each && room <= kLoneTokens) {
-      a.waves = 1;
-      want = 1;
-    } else if (a.cache.head_dim <= kWideDim && want > 1 && room <= steps * kWideWaves * kTile) {
-      a.waves = kWideWaves;
-      want = 1;
-    }
-  }
-  const int64_t ht = static_cast<int64_t>(a.cache.heads) * a.tiles, first = a.cache.head_dim == 64 ? 4 * cu : slots;
-  a.target[0] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxParts, first / ht)));
-  a.target[1] = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxParts, cu / ht)));
-  a.planned = a.requests <= kPlanned && a.waves == kWaves && !g_splits.load() && (want > 1 || each > cu);
-  if (a.planned && want > 1) want = std::min<int64_t>(most, a.target[0]);
-  set_parts(a, static_cast<int>(want < 1 ? 1 : want > kMaxParts ? kMaxParts : want));
-}
-
-int64_t part_bytes(const fp4lib::AttnArgs& a) {
-  return a.splits <= 1 ? 0
-                       : a.items * a.q.heads * (a.cache.head_dim + 2) * static_cast<int64_t>(sizeof(float)) +
-                             a.requests * static_cast<int64_t>(sizeof(int2));
-}
+void plan(fp4lib::AttnArgs& a) { fp4attn::plan(a, fp4lib::device_cu_count(), g_splits.load()); }
 
 }  // namespace
 
