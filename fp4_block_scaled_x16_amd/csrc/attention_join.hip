@@ -187,10 +187,6 @@ hipError_t launch_some(const AttnArgs& a, hipStream_t s) {
   });
 }
 
-// Workgroups of a launch: a grid has fewer than 2^32 threads, and the kernel divides a part's
-// number, which is smaller, by up to 1024 with a product.
-constexpr int64_t kMostGroups = int64_t(1) << 22;
-
 }  // namespace
 
 hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
@@ -200,21 +196,7 @@ hipError_t launch_attention(const AttnArgs& args, hipStream_t s) {
   auto inverse = [](int n) { return static_cast<uint32_t>(((int64_t(1) << 32) + n - 1) / n); };
   a.by_splits = inverse(a.splits);
   a.by_heads = inverse(a.cache.heads);
-  const int64_t groups = static_cast<int64_t>(a.cache.heads) * a.tiles * (a.items / a.requests);
-  const int most = a.planned ? a.requests : static_cast<int>(groups < kMostGroups ? kMostGroups / groups : 1);
-  const int64_t row = static_cast<int64_t>(a.q.heads) * a.cache.head_dim * (a.out_f32 ? 4 : 2);
-  for (int first = 0; first < args.requests; first += most) {
-    a.requests = args.requests - first < most ? args.requests - first : most;
-    if (!a.planned) set_parts(a, a.splits);
-    a.q.x = args.q.x + first * args.q.token;
-    a.table = args.table + first * args.table_stride;
-    a.lens = args.lens + first;
-    a.out = static_cast<uint8_t*>(args.out) + first * row;
-    a.lse = args.lse ? args.lse + static_cast<int64_t>(first) * a.q.heads : nullptr;
-    const hipError_t e = launch_some(a, s);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  return by_launches(a, [&](const AttnArgs& some) { return launch_some(some, s); });
 }
 
 }  // namespace fp4lib

@@ -174,4 +174,29 @@ inline int64_t part_bytes(const fp4lib::AttnArgs& a) {
                              a.requests * static_cast<int64_t>(sizeof(int2));
 }
 
+// Workgroups of a launch: a grid has fewer than 2^32 threads, and the kernel divides a part's
+// number, which is smaller, by up to 1024 with a product.
+constexpr int64_t kMostGroups = int64_t(1) << 22;
+
+// Calls launch with the arguments of each launch of planned ones, until one fails.
+template <typename F>
+hipError_t by_launches(const fp4lib::AttnArgs& planned, F&& launch) {
+  fp4lib::AttnArgs a = planned;
+  const int64_t groups = static_cast<int64_t>(a.cache.heads) * a.tiles * (a.items / a.requests);
+  const int most = a.planned ? a.requests : static_cast<int>(groups < kMostGroups ? kMostGroups / groups : 1);
+  const int64_t row = static_cast<int64_t>(a.q.heads) * a.cache.head_dim * (a.out_f32 ? 4 : 2);
+  for (int64_t first = 0; first < planned.requests; first += most) {         // (an int may pass 2^31)
+    a.requests = static_cast<int>(std::min<int64_t>(planned.requests - first, most));
+    if (!a.planned) set_parts(a, a.splits);
+    a.q.x = planned.q.x + first * planned.q.token;
+    a.table = planned.table + first * planned.table_stride;
+    a.lens = planned.lens + first;
+    a.out = static_cast<uint8_t*>(planned.out) + first * row;
+    a.lse = planned.lse ? planned.lse + first * a.q.heads : nullptr;
+    const hipError_t e = launch(a);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 }  // namespace fp4attn
