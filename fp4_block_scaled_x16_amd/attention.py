@@ -63,10 +63,10 @@ class QKNormRope:
 
     As with the linears, the gradients of the weights are added to main_grad
     (float32 [2, head_dim]: q's, then k's; zero it between optimizer steps) and the weights
-    get no .grad; hooks on them run in the backward pass.  Weights changed in place
-    between the two passes are refused there, as is a gradient of the gradient.  A step may be captured into
-    a graph; the captured q and k should be no leaves of an eager graph that is still
-    alive (a leaf keeps its first stream).
+    get no .grad; hooks on them run in the backward pass.  Weights or a table changed in
+    place between the two passes are refused there, as is a gradient of the gradient.  A step
+    may be captured into a graph; the captured q and k should be no leaves of an eager graph
+    that is still alive (a leaf keeps its first stream).
     """
 
     def __init__(self, q_weight=None, k_weight=None, table=None, eps=1e-6, style="half"):
@@ -87,7 +87,11 @@ class QKNormRope:
 class _QKNormRopeFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, positions, layer, *aliases):
-        ctx.save_for_backward(q, k, positions, *aliases)       # the weights for the check of their versions
+        table = layer.norm.table
+        if table is not None and table.is_inference():         # which has no versions, and is not saved
+            table = None
+        # the table and the weights for the check of their versions
+        ctx.save_for_backward(q, k, positions, table, *aliases)
         ctx.layer, ctx.norm, ctx.aliases = layer, layer.norm, aliases
         return api.qk_norm_rope(layer.norm, q, k, positions)
 
