@@ -109,6 +109,19 @@ class _QKNormRopeFunction(torch.autograd.Function):
         return dq, dk, None, None, *(None for _ in ctx.aliases)
 
 
+class _NoGradient(torch.autograd.Function):
+    """The y of (y,), computed from x in a way that has no backward pass (the tuple keeps
+    it from being an input, and the output a view of it that cannot be changed in place)."""
+
+    @staticmethod
+    def forward(ctx, x, made):
+        return made[0]
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("QuantizedAttention has no backward pass: it generates")
+
+
 class QuantizedAttention:
     """The attention layer of a model that generates: one new token per request.
 
@@ -119,6 +132,7 @@ class QuantizedAttention:
 
     A prompt goes through the same call, a token per row: rows of one request share
     its page table's row (which may be expanded) and have lengths that count up.
+    There is no backward pass: one that comes to the layer's output fails.
     """
 
     def __init__(self, qkv, out, heads, kv_heads, norm: api.QKNorm = None, scale=None):
@@ -159,4 +173,5 @@ class QuantizedAttention:
             # in place: the projection's rows are nobody else's
             q = api.kv_cache_write(cache, k, v, slots, q=q, norm=self.norm, positions=positions, q_out=q)
         o = api.attention_decode(q, cache, page_table, lens, self.scale)
-        return self._product(o.view(tokens, h * self.head_dim), self._out, self.out.shape[0])
+        y = self._product(o.view(tokens, h * self.head_dim), self._out, self.out.shape[0])
+        return _NoGradient.apply(x, (y,)) if x.requires_grad and torch.is_grad_enabled() else y

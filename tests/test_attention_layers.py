@@ -58,3 +58,44 @@ def test_a_table_made_in_inference_mode(plain_norm):
     y, k = layer(q, torch.ones((5, 1, 64), dtype=BF).requires_grad_(), torch.arange(5))
     torch.autograd.backward((y, k), (torch.ones_like(y), torch.ones_like(k)))
     assert torch.all(q.grad == 1)
+
+
+class Codes:
+    """What a quantized matrix stands for here: its values."""
+
+    def __init__(self, x):
+        self.codes, self.scales = x.detach().clone(), torch.ones(1)
+
+    def operand(self):
+        op = api.Operand()
+        op._owner = self
+        return op
+
+
+@pytest.fixture
+def plain_layer(monkeypatch):
+    """An attention layer of 2 heads on 1 of 64 whose attention gives the queries."""
+    monkeypatch.setattr(api, "quantize", lambda x, fmt, block="1d": Codes(x))
+    monkeypatch.setattr(api, "gemm", lambda a, b, m, n, k, out_dtype: (
+        a._owner.codes.float() @ b._owner.codes.float().T).to(out_dtype))
+    monkeypatch.setattr(api, "kv_cache_write", lambda *a, **kw: None)
+    monkeypatch.setattr(api, "attention_decode", lambda q, *a: q.contiguous())
+    g = torch.Generator().manual_seed(0)
+    qkv, out = (torch.randn(s, generator=g).to(BF) for s in ((4 * 64, 32), (32, 2 * 64)))
+    return attention.QuantizedAttention(qkv, out, 2, 1)
+
+
+def test_the_generating_layer_has_no_backward_pass(plain_layer):
+    """It takes an input under autograd, with the same result, and says so when a gradient
+    is asked of it; it used to hand on a result that wanted none."""
+    x = torch.randn((3, 32), generator=torch.Generator().manual_seed(1)).to(BF)
+    y = plain_layer(x, None, None, None, None)
+    assert not y.requires_grad
+    leaf = x.clone().requires_grad_()
+    got = plain_layer(leaf, None, None, None, None)
+    assert torch.equal(got, y) and got.requires_grad
+    got += 1                                            # a residual, say
+    with pytest.raises(RuntimeError, match="QuantizedAttention has no backward pass"):
+        (got.float() + leaf.sum()).sum().backward()
+    with torch.no_grad():
+        assert not plain_layer(leaf, None, None, None, None).requires_grad
