@@ -923,8 +923,9 @@ class KVCache:
                 ("k_codes", k_codes, k_codes.shape, k_codes), ("v_codes", v_codes, k_codes.shape, k_codes),
                 ("k_scales", k_scales, (pages, heads, blocks, page), k_scales),
                 ("v_scales", v_scales, (pages, heads, blocks, page), k_scales)):
-            if (t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape) or t.stride() != strides.stride()
-                    or t.stride(3) != 1 or t.device != k_codes.device):
+            if (t.dtype != torch.uint8 or tuple(t.shape) != tuple(shape) or t.stride(3) != 1
+                    or t.device != k_codes.device          # (the stride of a single entry means nothing)
+                    or any(a != b for n, a, b in zip(shape, t.stride(), strides.stride()) if n > 1)):
                 raise ValueError("%s must be uint8 %s on %s, its last dimension contiguous and K's and "
                                  "V's strides alike" % (name, tuple(shape), k_codes.device))
         if f in (NVFP4, UE5M3):
