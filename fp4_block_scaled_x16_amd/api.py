@@ -795,9 +795,16 @@ class QKNorm:
                                 int(q_weight is not None and q_weight.dtype == torch.float32), self.eps,
                                 _addr(table), rows, dim, PAIRINGS[style])
         self._at = ctypes.addressof(self._desc)
+        self._of = self._addresses()
+
+    def _addresses(self):
+        return _addr(self.q_weight), _addr(self.k_weight), _addr(self.table)
 
     def _positions(self, positions, tokens, head_dim, device):
-        """The address of the positions of rows [tokens, heads, head_dim]."""
+        """The address of the positions of rows [tokens, heads, head_dim]; the descriptor
+        (_at) is that of the tensors as they are from here on."""
+        if self._addresses() != self._of:          # a tensor's .data has been replaced
+            self.__init__(self.q_weight, self.k_weight, self.table, self.eps, self.style)
         if device != self.device or (self.head_dim is not None and head_dim != self.head_dim):
             raise ValueError("the norm is for heads of %s on %s" % (self.head_dim, self.device))
         if self.table is None:
@@ -994,7 +1001,8 @@ def kv_cache_write(cache: KVCache, k, v, slots, q=None, norm: QKNorm = None, pos
     at = _index(slots, "slots", tokens, dev)
     pos = where = q_at = out_at = None
     if norm is not None:
-        where, pos = norm._at, norm._positions(positions, tokens, d, dev)
+        pos = norm._positions(positions, tokens, d, dev)
+        where = norm._at
     if q is not None:
         if norm is None:
             raise ValueError("q needs a norm")

@@ -99,3 +99,30 @@ def test_the_generating_layer_has_no_backward_pass(plain_layer):
         (got.float() + leaf.sum()).sum().backward()
     with torch.no_grad():
         assert not plain_layer(leaf, None, None, None, None).requires_grad
+
+
+@pytest.mark.parametrize("what", ["q_weight", "k_weight", "table"])
+def test_a_norm_whose_tensors_data_is_replaced(monkeypatch, what):
+    """The calls get the addresses of the new data: the old memory may be gone."""
+    got = []
+
+    def launch(name, fn, device, *args):
+        assert norm._at in args
+        d = api.QKNormDesc.from_address(norm._at)
+        got.append((d.q_weight, d.k_weight, d.table, d.weight_f32, d.rotary_dim))
+
+    monkeypatch.setattr(api, "_launch", launch)
+    monkeypatch.setattr(api, "_norm_workspace", lambda device, d: 16)
+    t = dict(q_weight=torch.ones(64), k_weight=torch.ones(64), table=torch.ones((8, 32)))
+    norm = api.QKNorm(**t)
+    cache = api.KVCache.empty(2, 16, 1, 64, device="cpu")
+    x, pos = torch.ones((5, 1, 64), dtype=BF), torch.arange(5)
+    calls = [lambda: api.qk_norm_rope(norm, x, x, pos), lambda: api.qk_norm_rope_backward(norm, x, x, pos, x, x),
+             lambda: api.kv_cache_write(cache, x, x, pos, q=x, norm=norm, positions=pos)]
+    for call in calls:
+        t[what].data = t[what].data.clone()
+        call()
+        assert got[-1] == (t["q_weight"].data_ptr(), t["k_weight"].data_ptr(), t["table"].data_ptr(), 1, 32)
+    t["table"].data = torch.ones((9, 64), dtype=torch.float64)
+    with pytest.raises(ValueError, match="table must be"):
+        calls[0]()
