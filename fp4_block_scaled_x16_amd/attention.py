@@ -146,11 +146,23 @@ class QuantizedAttention:
             raise ValueError("out must have heads * head_dim = %d columns" % (heads * self.head_dim))
         self.qkv, self.out, self.heads, self.kv_heads = qkv, out, heads, kv_heads
         self.norm, self.scale = norm, scale
+        self._qkv = self._out = None
         self.refresh()
 
     def refresh(self):
-        """Encode the weights anew."""
-        self._qkv, self._out = (api.quantize(w, "fp8", block="2d").operand() for w in (self.qkv, self.out))
+        """Encode the weights anew, where their codes are: a step that has been captured
+        takes the new ones.  To be called on the stream that the steps run on."""
+        self._qkv, self._out = self._encoded(self.qkv, self._qkv), self._encoded(self.out, self._out)
+
+    @staticmethod
+    def _encoded(w, old):
+        new = api.quantize(w, "fp8", block="2d")
+        into = None if old is None else old._owner
+        if into is None or into.codes.shape != new.codes.shape or into.codes.device != new.codes.device:
+            return new.operand()
+        into.codes.copy_(new.codes)
+        into.scales.copy_(new.scales)
+        return old
 
     @staticmethod
     def _product(x, w, n):

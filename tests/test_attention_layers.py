@@ -126,3 +126,20 @@ def test_a_norm_whose_tensors_data_is_replaced(monkeypatch, what):
     t["table"].data = torch.ones((9, 64), dtype=torch.float64)
     with pytest.raises(ValueError, match="table must be"):
         calls[0]()
+
+
+def test_refresh_writes_the_codes_in_place(plain_layer):
+    """A step that has been captured reads them where they were."""
+    before = [op._owner for op in (plain_layer._qkv, plain_layer._out)]
+    at = [(o.codes.data_ptr(), o.scales.data_ptr()) for o in before]
+    ops = plain_layer._qkv, plain_layer._out
+    plain_layer.qkv.mul_(2)
+    plain_layer.out.add_(1)
+    plain_layer.refresh()
+    assert (plain_layer._qkv, plain_layer._out) == ops
+    for o, w, a in zip(before, (plain_layer.qkv, plain_layer.out), at):
+        assert torch.equal(o.codes, w) and (o.codes.data_ptr(), o.scales.data_ptr()) == a
+    # weights of another shape are other codes
+    plain_layer.out = torch.ones((48, 128), dtype=BF)
+    plain_layer.refresh()
+    assert plain_layer._out._owner.codes.shape == (48, 128) and plain_layer._qkv is ops[0]
