@@ -42,12 +42,14 @@ fp4_status check_heads(const char* name, const fp4_heads* h, int64_t tokens, int
   if (h->token_stride < 0 || h->head_stride < 0 || h->token_stride % 8 || h->head_stride % 8)
     return fail(FP4_ERR_ARG, "%s: strides must be multiples of 8, not negative", name);
   if (output) {
-    // one of the two strides steps over the other's whole extent
-    const int64_t by_head = (h->heads - 1) * h->head_stride + head_dim;
+    // one of the two strides steps over the other's whole extent (which may pass 63 bits)
+    using Wide = __int128;
+    const Wide by_head = Wide(h->heads - 1) * h->head_stride + head_dim;
+    const Wide by_token = Wide(tokens - 1) * h->token_stride + head_dim;
     const bool heads_apart = h->heads == 1 || h->head_stride >= head_dim;
     const bool tokens_outer = heads_apart && (tokens == 1 || h->token_stride >= by_head);
     const bool heads_outer = (tokens == 1 || h->token_stride >= head_dim) &&
-                             (h->heads == 1 || h->head_stride >= (tokens - 1) * h->token_stride + head_dim);
+                             (h->heads == 1 || h->head_stride >= by_token);
     if (!tokens_outer && !heads_outer) return fail(FP4_ERR_ARG, "%s: rows overlap", name);
   }
   return FP4_OK;
