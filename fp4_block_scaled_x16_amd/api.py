@@ -989,7 +989,7 @@ def kv_cache_write(cache: KVCache, k, v, slots, q=None, norm: QKNorm = None, pos
     their slots (int64 [tokens]; a negative one, or one behind the last page, is not
     written; the others are distinct).
 
-    norm: k goes through it first, in the same pass, without a rounding between; with
+    norm: k goes through it first, in the same pass, without a rounding to bf16 between; with
     q, q does too and comes back (bf16; into q_out, if given).  positions as in
     `qk_norm_rope`.  Returns q's result, or None.
     """

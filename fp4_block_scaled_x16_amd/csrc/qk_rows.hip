@@ -145,10 +145,12 @@ __device__ __forceinline__ float to_odd(double z) {
 
 // Rows of k or v into their slot: from head0 on, every kRows-th.
 //
-// What a norm or a rotation gives is formed in 64 bits and encoded with one rounding:
-// in fp32 a value next to a border between two codes would now and then fall on its
-// other side, 6 or 12 % away (12 of 8 million elements, as many as in elementary fp32 operations;
-// 8192 tokens to an MXFP8 cache took 40.7 us, and 64 to an FP8 one 3.4).
+// What a norm or a rotation gives is formed in 64 bits and, rounded to odd in fp32, handed to the
+// encoder.  A scale that is a power of two then gives the code of one rounding (NVFP4's and UE5M3's
+// are none: their product with the inverse scale is rounded in fp32 as fp4_quantize rounds it).
+// With all of it in fp32 a value next to a border between two codes would now and then fall on
+// its other side, 6 or 12 % away (12 of 8 million elements, as many as in elementary fp32
+// operations; 8192 tokens to an MXFP8 cache took 40.7 us, and 64 to an FP8 one 3.4).
 template <int D, int FMT, int R>
 __device__ __forceinline__ void coded_rows(const fp4lib::QkRowsArgs& a, int kind, int64_t token, int head0, int lane) {
   constexpr int kLanes = D / 8, kRows = 64 / kLanes;

@@ -616,10 +616,12 @@ typedef struct {
  *   slots   device int64[tokens].  A token whose slot is negative or behind the
  *           last page is not written.  The others' slots are distinct: where two
  *           tokens name one slot, it may end with bytes of either.
- *   norm    NULL, or what k goes through first (in 64 bits, encoded from there with
- *           one rounding), in the same pass; with it q, which comes out as
- *           q_out in bf16 (both NULL: k alone), and positions (all as in
- *           fp4_qk_norm_rope; q is turned whatever the slot).
+ *   norm    NULL, or what k goes through first, in the same pass; with it q, which
+ *           comes out as q_out in bf16 (both NULL: k alone), and positions (all as in
+ *           fp4_qk_norm_rope; q is turned whatever the slot).  k's values are formed
+ *           in 64 bits.  FP8_E4M3, MXFP8 and MXFP4 encode them with one rounding; for
+ *           NVFP4 and UE5M3 they are rounded to odd in fp32 and go through the
+ *           quantizer's fp32 steps from there (block scale, product with its inverse).
  */
 fp4_status fp4_kv_cache_write(const fp4_kv_cache* cache /* host */, const fp4_heads* k /* host */,
                               const fp4_heads* v /* host */, const int64_t* slots, int64_t tokens,
