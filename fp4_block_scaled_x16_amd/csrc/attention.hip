@@ -34,10 +34,14 @@
 // FP8, MXFP8 and MXFP4 are widened to bf16, their power-of-two scales applied by
 // the same convert; NVFP4 and UE5M3 to fp16, in which code times block scale is
 // exact (UE5M3 times 2^-5), q's row being scaled into fp16's range by a power of
-// two.  Either way the operands are exact.  p is split into a rounded part and
-// what that leaves (bf16: 2^-17 of p; fp16: 2^-22), since rounding it once would
-// add as much error as the output's own: for up to 8 heads the second part takes
-// the other 8 of the matrix's 16 columns, for more a second MFMA.
+// two.  Either way the operands are exact.  So is p in bf16, in three parts of 8 bits; in
+// fp16 a rounded part and what that leaves hold 2^-22 of it.  For up to 8 heads the second
+// part takes the other 8 of the matrix's 16 columns, for more a second MFMA; the third takes
+// one more.  (Two bf16 parts, 2^-17 of p, leave 2.2 of 1000 outputs in bf16 beside the
+// nearest one, 64 requests of up to 8192 MXFP8 tokens, where elementary fp32 operations leave
+// 0.6; three leave 0.3.  They cost nothing where memory bounds, 101.9 and 101.5 us there, and
+// up to 7 % where vector instructions do: 256 of up to 1024 MXFP4 tokens 14.8 and 15.4 us, 8 of
+// 30000 with 64 heads on one 29.2 and 31.2.)
 #include "attention_common.hpp"
 
 using namespace kvdev;
@@ -67,14 +71,18 @@ __device__ __forceinline__ floatx4 mfma(uintx4 a, uintx4 b, floatx4 c) {
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Two floats as bf16 (fp16), to nearest even.
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16)
-    return __builtin_bit_cast(uint32_t, halfx2{static_cast<_Float16>(x), static_cast<_Float16>(y)});
-  else
-    return fp8dev::pack_bf16(x, y);
+// A float's upper half, and those of two (with kZeros: zeros) as bf16.
+__device__ __forceinline__ float upper(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+constexpr uint32_t kUpperHalves = 0x07060302u, kZeros = 0x0C0C0C0Cu;
+__device__ __forceinline__ uint32_t upper_pair(float x, float y, uint32_t which) {
+  return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), which);
 }
+
+// Two floats as fp16, to nearest even.
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  return __builtin_bit_cast(uint32_t, halfx2{static_cast<_Float16>(x), static_cast<_Float16>(y)});
+}
+// The halves of a word, of bf16 or fp16.
 template <bool F16>
 __device__ __forceinline__ float unpack_lo(uint32_t w) {
   if constexpr (F16) return static_cast<float>(__builtin_bit_cast(halfx2, w)[0]);
@@ -454,7 +462,7 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
       for (int k = 0; k < S::kSteps; ++k)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          q[k][i] = pack2<true>(__builtin_ldexpf(unpack_lo<false>(q[k][i]), e),
+          q[k][i] = pack2(__builtin_ldexpf(unpack_lo<false>(q[k][i]), e),
                                 __builtin_ldexpf(unpack_hi<false>(q[k][i]), e));
       factor = __builtin_ldexpf(factor * s_dec, (FMT == kKvUe4 ? 5 : 0) - e);
     }
@@ -511,6 +519,7 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
   // them at once): the last 16 tokens are loaded again then, and not used.  (Two tiles
   // under way at lower occupancy were no faster at any size.)
   const ScalePick pick(c, g);
+  const uint32_t third_of = NP == 2 || c < 8 ? kUpperHalves : kZeros;     // (once for each head)
   HalfPos h[2];
   KHalf<FMT, D, STREAM> k[2];
   VHalf<FMT, D, STREAM> v[2];
@@ -568,14 +577,23 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
         for (int i = 0; i < S::kElems; ++i) acc[i] *= by;
       }
       const float from = top == -__builtin_inff() ? 0.0f : top - kShift;
-      uintx4 p, rest;
+      uintx4 p, rest, third;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float u = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2)], factor, -from));
         const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j / 2][2 * (j % 2) + 1], factor, -from));
         total += u + w;
-        const uint32_t hi = pack2<kF16>(u, w);
-        const uint32_t lo = pack2<kF16>(u - unpack_lo<kF16>(hi), w - unpack_hi<kF16>(hi));
+        uint32_t hi, lo;
+        if constexpr (kF16) {
+          hi = pack2(u, w);
+          lo = pack2(u - unpack_lo<true>(hi), w - unpack_hi<true>(hi));
+        } else {
+          // cut off, not rounded, so that the third part is all that the two leave
+          const float u1 = u - upper(u), w1 = w - upper(w);
+          hi = upper_pair(u, w, kUpperHalves);
+          lo = upper_pair(u1, w1, kUpperHalves);
+          third[j] = upper_pair(u1 - upper(u1), w1 - upper(w1), third_of);
+        }
         if constexpr (NP == 1) {
           p[j] = c < 8 ? hi : lo;
         } else {
@@ -626,6 +644,7 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
           for (int j = 0; j < 4; ++j) o[j] = __builtin_amdgcn_perm(w[2 * j + 1][e / 2], w[2 * j][e / 2], sel);
           acc[e0 + e] = mfma<kF16>(o, p, acc[e0 + e]);
           if constexpr (NP == 2) acc[e0 + e] = mfma<kF16>(o, rest, acc[e0 + e]);
+          if constexpr (!kF16) acc[e0 + e] = mfma<kF16>(o, third, acc[e0 + e]);
         }
       }
 #pragma unroll
@@ -670,7 +689,7 @@ __global__ __launch_bounds__(64 * W, W == kWideWaves ? 2 : waves_per_simd(D)) vo
       for (int i = 0; i < 4; ++i) acc[e][i] += by * meet[w][4 * e + i][lane];
   }
   if constexpr (NP == 1) {
-    // columns 8 .. hold the sums with what rounding p left
+    // columns 8 .. hold the sums with p's second part
 #pragma unroll
     for (int e = 0; e < S::kElems; ++e)
 #pragma unroll

@@ -661,8 +661,8 @@ fp4_status fp4_kv_cache_read(const fp4_kv_cache* cache /* host */, const int64_t
  *            a second kernel; with less, or NULL, they are not.  Contents of no
  *            account; calls that may run at the same time need one each.
  * Operands are exact (NVFP4 and UE5M3: q to 2^-38 of its row's largest element),
- * sums, maxima and p in fp32; p is rounded to 2^-17 of itself or less before it
- * meets V (NVFP4 and UE5M3: or to 2^-32 of the largest, whichever is more).
+ * sums, maxima and p in fp32.  p meets V whole (NVFP4 and UE5M3: rounded to 2^-22 of
+ * itself, or to 2^-32 of the largest, whichever is more).
  * fp4_attention_workspace: 0 where none is used and for invalid arguments.
  */
 fp4_status fp4_attention_decode(const fp4_kv_cache* cache /* host */, const fp4_heads* q /* host */,
