@@ -14,8 +14,9 @@ The layer's step, for one new token of each request:
   o           = softmax(q K^T / sqrt(d)) V over the request's cached tokens
   y           = o W_out^T       FP8 operands, bf16 out
 
-Every computation runs in the library's kernels; this module allocates outputs and
-passes pointers (through `api`).
+The layers' computations run in the library's kernels; this module allocates outputs
+and passes pointers (through `api`).  `rotary_table` and `slots_of` are torch operations,
+made once and about ten small ones a step.
 """
 from __future__ import annotations
 
@@ -62,8 +63,8 @@ class QKNormRope:
     None, and its result then is.
 
     As with the linears, the gradients of the weights are added to main_grad
-    (float32 [2, head_dim]: q's, then k's; zero it between optimizer steps) and the weights
-    get no .grad; hooks on them run in the backward pass.  Weights or a table changed in
+    (float32 [2, head_dim]: q's, then k's; zero it between optimizer steps), whether the
+    weights require one or not, and the weights get no .grad; hooks on them run in the backward pass.  Weights or a table changed in
     place between the two passes are refused there, as is a gradient of the gradient.  A step
     may be captured into a graph; the captured q and k should be no leaves of an eager graph
     that is still alive (a leaf keeps its first stream).

@@ -2,12 +2,12 @@
 // key-value cache:  out = softmax(scale q K^T) V  over the request's tokens.
 //
 // Bound by reading the codes once, where there are many: 64 requests of up to 8192
-// MXFP8 tokens (8 heads of 128 for 32 query heads) take 102 us, 5.5 TB/s of codes and
+// MXFP8 tokens (8 heads of 128 for 32 query heads) take 101.5 us, 5.5 TB/s of codes and
 // scales, 64 of 8192 174 us, 6.4 TB/s; 1000 of up to 4000 of heads of 64 329 us, 6.4 TB/s.
 // With 4-bit codes and block scales that are no powers of two by the vector instructions
 // as well (4 of 120000 NVFP4 tokens: 71 % of cycles; 103 to 108 us, 5.1 to 5.4 TB/s).  Few
 // or short requests by their steps, one after the other: about 1 us for 128 tokens of
-// heads of 128 (a tile's 220 vector and 90 scalar instructions, and the wait for its
+// heads of 128 (a tile's 240 vector and 90 scalar instructions, and the wait for its
 // codes), and about 5 for the launch, the loads that wait for one another at the start,
 // and the meeting of the waves (1 request of 1000 FP8 tokens: 6 us and 3 for the join).
 //
@@ -41,7 +41,8 @@
 // nearest one, 64 requests of up to 8192 MXFP8 tokens, where elementary fp32 operations leave
 // 0.6; three leave 0.3.  They cost nothing where memory bounds, 101.9 and 101.5 us there, and
 // up to 7 % where vector instructions do: 256 of up to 1024 MXFP4 tokens 14.8 and 15.4 us, 8 of
-// 30000 with 64 heads on one 29.2 and 31.2.)
+// 30000 with 64 heads on one 29.2 and 31.2.  Figures below and beside the plan that compare two
+// ways of one step are from kernels with two parts.)
 #include "attention_common.hpp"
 
 using namespace kvdev;

@@ -1,5 +1,5 @@
-// Shared by the attention kernels: how a request's tokens are shared among
-// workgroups, and the launchers of the formats.
+// Shared by the attention kernels: the requests' lengths, where the workspace holds the
+// parts' sums, and the launchers of the formats.
 #pragma once
 
 #include "attention_plan.hpp"

@@ -1,9 +1,9 @@
-// Launch of the attention of one new token per request (attention.hip): how many
-// parts a request's tokens are shared among, and the kernel that joins them:
+// Launch of the attention of one new token per request (attention.hip), and the
+// kernel that joins the parts that a request's tokens are shared among (attention_plan.hpp):
 //   m = max_s m_s,  out = sum_s 2^(m_s - m) o_s / sum_s 2^(m_s - m) l_s
-// of each part's maximum m_s, sum l_s and sum of p v o_s.  Few bytes (1 MB for 64
-// requests of 32 heads in 4 parts), so it is bound by its launch and two rounds of
-// loads: 3 to 5 us.
+// of each part's maximum m_s, sum l_s and sum of p v o_s.  Few bytes (64 requests of up to
+// 8192 tokens, 32 heads on 8 of 128: 1.1 MB read), so it is bound by its launch and two
+// rounds of loads: 3 to 5 us.
 #include <algorithm>
 #include <atomic>
 

@@ -7,9 +7,10 @@
 //   dz = R^T dy;  dw = sum dz x r;  g = dz w;  dx = r (g - x r^2 mean(g x))
 //
 // Bound by memory: 2 bytes in and 2 out per element (backward 4 in, 2 out).  8192 tokens
-// of 32 + 8 heads of 128 take 34.4 us, 4.9 TB/s, where a large copy reaches 5.0 to 5.2;
-// backward 53 us, 4.8 TB/s; 8192 tokens normed, turned and written to an MXFP8 cache 41.5 us,
-// 4.6 TB/s; 64 of them to an FP8 cache 3.9 us, of which a launch is 3.
+// of 32 + 8 heads of 128 take 33.9 us, 5.1 TB/s, where a large copy reaches 5.0 to 5.2;
+// backward 53.4 us, 4.8 TB/s; 8192 tokens normed, turned and written to an MXFP8 cache 41.5 us,
+// 4.6 TB/s (MXFP4 44.0, NVFP4 47.0), without a norm K and V alone 12 us (NVFP4 14.5); 64 of them
+// normed to an FP8 cache 4.0 us, of which a launch is 3.
 //
 // A row lies in D / 8 lanes, 16 bytes each.  A rotated pair's other half ("half"
 // style: D / 2 lanes' distance or less) is not exchanged between lanes but loaded a

@@ -108,8 +108,8 @@ def test_nothing_to_do():
     same_pools(cache, before)
 
 
-# With the norm and rotation in the same pass, K is encoded from fp32 values within
-# some error of the exact ones: each code is that of a value within the error, and
+# With the norm and rotation in the same pass, K is encoded from values formed in 64 bits; here
+# each code has to be that of a value within an fp32 computation's error of the exact one, and
 # each scale that of an amax within it.
 @pytest.mark.parametrize("style,rot,w_dtype", [("half", None, torch.bfloat16), ("interleaved", 32, torch.float32),
                                                ("half", 32, torch.bfloat16), ("half", 0, torch.bfloat16),
