@@ -161,8 +161,9 @@ class QuantizedAttention:
         into = None if old is None else old._owner
         if into is None or into.codes.shape != new.codes.shape or into.codes.device != new.codes.device:
             return new.operand()
-        into.codes.copy_(new.codes)
-        into.scales.copy_(new.scales)
+        with torch.inference_mode():             # (they may have been made in it)
+            into.codes.copy_(new.codes)
+            into.scales.copy_(new.scales)
         return old
 
     @staticmethod

@@ -143,3 +143,17 @@ def test_refresh_writes_the_codes_in_place(plain_layer):
     plain_layer.out = torch.ones((48, 128), dtype=BF)
     plain_layer.refresh()
     assert plain_layer._out._owner.codes.shape == (48, 128) and plain_layer._qkv is ops[0]
+
+
+def test_refresh_of_a_layer_made_in_inference_mode(plain_layer):
+    """Its codes may not be changed outside that mode, so they are changed in it; and those
+    of a layer made outside may be changed inside."""
+    with torch.inference_mode():
+        inside = attention.QuantizedAttention(plain_layer.qkv, plain_layer.out, 2, 1)
+        plain_layer.qkv.add_(1)
+        plain_layer.refresh()
+    at = inside._qkv._owner.codes.data_ptr()
+    inside.refresh()
+    assert inside._qkv._owner.codes.data_ptr() == at
+    for layer in (inside, plain_layer):
+        assert torch.equal(layer._qkv._owner.codes, plain_layer.qkv)
