@@ -804,7 +804,7 @@ class QKNorm:
         """The address of the positions of rows [tokens, heads, head_dim]; the descriptor
         (_at) is that of the tensors as they are from here on."""
         if self._addresses() != self._of:          # a tensor's .data has been replaced
-            self.__init__(self.q_weight, self.k_weight, self.table, self.eps, self.style)
+            QKNorm.__init__(self, self.q_weight, self.k_weight, self.table, self.eps, self.style)
         if device != self.device or (self.head_dim is not None and head_dim != self.head_dim):
             raise ValueError("the norm is for heads of %s on %s" % (self.head_dim, self.device))
         if self.table is None:

@@ -64,10 +64,11 @@ class QKNormRope:
 
     As with the linears, the gradients of the weights are added to main_grad
     (float32 [2, head_dim]: q's, then k's; zero it between optimizer steps), whether the
-    weights require one or not, and the weights get no .grad; hooks on them run in the backward pass.  Weights or a table changed in
-    place between the two passes are refused there, as is a gradient of the gradient.  A step
-    may be captured into a graph; the captured q and k should be no leaves of an eager graph
-    that is still alive (a leaf keeps its first stream).
+    weights require one or not, and the weights get no .grad; hooks on them run in the
+    backward pass.  Weights or a table changed in place between the two passes are refused
+    there, as is a gradient of the gradient.  A step may be captured into a graph; the
+    captured q and k should be no leaves of an eager graph that is still alive (a leaf keeps
+    its first stream).
     """
 
     def __init__(self, q_weight=None, k_weight=None, table=None, eps=1e-6, style="half"):

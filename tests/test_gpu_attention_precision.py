@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("fmt", ["fp8", "mxfp8", "mxfp4"])
 @pytest.mark.parametrize("d,heads,group", [(64, 1, 16), (64, 2, 3), (128, 1, 8), (128, 2, 12), (256, 1, 4), (256, 1, 9)])
-@pytest.mark.parametrize("requests,width", [(600, 1), (600, 80), (20, 1), (20, 300)])
+@pytest.mark.parametrize("requests,width", [(600, 1), (600, 80), (20, 1), (20, 30), (20, 300)])
 def test_probabilities_are_not_rounded(fmt, d, heads, group, requests, width):
     cache = api.KVCache.empty(width, 16, heads, d, fmt, DEV)
     kv = torch.zeros((2, 2, heads, d), dtype=torch.bfloat16, device=DEV)
